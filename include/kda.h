@@ -618,6 +618,179 @@ kda_status_t kda_state_scan(const kda_desc_t* desc, int32_t count, const float* 
                             const float* offsets, const float* initial_state,
                             float* entry_state, kda_stream_t stream);
 
+/*
+ * The 4-bit paged cache of the full-attention layers.
+ *
+ * The architecture puts one full-attention layer after every three KDA layers
+ * (blog.higcp.com "猜想：K3 可能是最适合 TPU 的 MoE 架构", section "第七重").  A
+ * KDA layer keeps a state of fixed size; an attention layer keeps the keys and
+ * values of every token.  The calls below hold those in 4 bits -- E2M1 values
+ * with one E4M3 scale per 16 channels, the main-KV format that
+ * lishengnan.com/aichip names -- in pages handed out on the GPU:
+ *
+ *   kda_cache_tables      block tables and slots from the requests' lengths
+ *   kda_cache_append      new k, v quantised into their slots
+ *   kda_cache_read        the values at given slots
+ *   kda_cache_attention   causal attention of new queries over the cache
+ *
+ * One cache belongs to one layer; the block tables are shared by all layers.
+ *
+ * Format.  A block of 16 neighbouring channels x of one token and head is held
+ * as  s = e4m3(max |x| / 6)  and  c_i = e2m1(x_i / s), both rounded to nearest
+ * with ties to even and saturating at 448 and 6; it stands for c_i s.  (A block
+ * whose s rounds to 0 stands for zeros.)  With exponents e_h given, x is scaled
+ * by 2^-e_h first and the stored value by 2^e_h when it is used, both exact:
+ * the E4M3 scale spans 2^-9 .. 448, and a head whose values are small or large
+ * throughout is moved into the middle of it that way.
+ *
+ * Layout.  pages is [num_pages][num_kv_heads][page_size / 16][18 * head_dim]
+ * bytes, D = head_dim.  The 18 D bytes hold 16 tokens (i = 0 .. 15):
+ *     K codes    byte  i D/2 + c/2
+ *     V codes    byte  8 D + (i/8) 4 D + (c/16) 64 + (i%8) 8 + (c%16)/2
+ *     K scales   byte  16 D + (i%8) D/8 + (b/n) 2 n + (i/8) n + b%n,  n = D/64
+ *     V scales   byte  17 D + 16 b + (i%8)/2 4 + (i/8) 2 + i%2
+ * for channel c (even channels in the low nibble) and block b = c/16.  Slot s is
+ * token s % page_size of page s / page_size.
+ */
+typedef struct {
+  void* pages;              /* device, 16-byte aligned                        */
+  int32_t num_pages;        /* >= 0                                           */
+  int32_t page_size;        /* tokens per page: a multiple of 16, <= 4096     */
+  int32_t num_kv_heads;     /* >= 1                                           */
+  int32_t head_dim;         /* 64 or 128                                      */
+  const int32_t* k_exponent; /* device [num_kv_heads], -64 .. 64, or NULL (0) */
+  const int32_t* v_exponent; /* device [num_kv_heads], -64 .. 64, or NULL (0) */
+} kda_cache_t;
+
+/*
+ * kda_cache_tables -- block tables that follow the requests' lengths.
+ *
+ * Request b holds pages for held_lens[b] tokens: the first
+ * ceil(held_lens[b] / page_size) entries of its row of block_table.  Its first
+ * seq_lens[b] <= held_lens[b] tokens stay (fewer than held when drafted tokens
+ * were rejected) and new_lens[b] >= 0 follow; new_lens[b] = -1 ends the request
+ * (nothing stays).  Pages that the length kv_lens[b] = seq_lens[b] + new_lens[b]
+ * needs beyond those held are taken from free_pages, in request order; held
+ * pages that it does not need go back there, also in request order.  Entries of
+ * a row past its length are left as they are and stand for nothing.
+ *
+ * free_pages is a ring of ring_size entries.  Positions free_range[0] (head) to
+ * free_range[1] - 1 (tail), taken modulo ring_size, are free pages; pages are
+ * taken at the head and put back at the tail, where a later call finds them.
+ * ring_size >= the number of pages, so that the ring cannot run over.
+ *
+ *   seq_lens, held_lens, new_lens   device, [num_seqs] int32
+ *   block_table      device, [num_seqs][max_blocks] int32, updated
+ *   free_pages       device, [ring_size] int32, updated
+ *   free_range       device, [2] int64
+ *   free_range_out   device, [2] int64, written; may be free_range
+ *   kv_lens          device, [num_seqs] int32, written; may be held_lens or
+ *                    seq_lens
+ *   cu_new           device, [num_seqs + 1] int32, written: where each request's
+ *                    new tokens start in the packed batch
+ *   slots            device, [max_tokens] int64, written: the slot of each packed
+ *                    new token, -1 past cu_new[num_seqs]
+ *
+ * Checked on the device (KDA_ERR_DEVICE_CHECK in the error word): a request
+ * whose row is too short, or for which no pages are left (requests after it that
+ * need pages get none either), keeps its seq_lens[b] tokens -- kv_lens[b] =
+ * seq_lens[b] -- and its new tokens, counted in cu_new all the same, get slot -1.
+ * A request with a negative length, seq_lens[b] > held_lens[b] or more tokens
+ * held than its row has room for gets kv_lens[b] = 0 and slots -1, and its pages
+ * stay where they are.  Tokens past max_tokens get no slot.  A free_range that
+ * is negative, reversed or longer than the ring counts as empty.
+ */
+kda_status_t kda_cache_tables(int32_t page_size, int32_t num_seqs, int32_t max_blocks,
+                              int32_t max_tokens, int32_t ring_size, const int32_t* held_lens,
+                              const int32_t* seq_lens, const int32_t* new_lens,
+                              int32_t* block_table, int32_t* free_pages,
+                              const int64_t* free_range, int64_t* free_range_out,
+                              int32_t* kv_lens, int32_t* cu_new, int64_t* slots,
+                              kda_stream_t stream);
+
+/*
+ * kda_cache_append -- k, v of num_tokens tokens, quantised into the cache.
+ *
+ *   k, v       device, [num_tokens, num_kv_heads, head_dim] io dtype; the
+ *              channels are contiguous, tokens and heads lie strides[0 .. 3]
+ *              elements apart: k's token, k's head, v's token, v's head stride
+ *              (NULL: packed).  Any alignment of the dtype; 16-byte aligned
+ *              rows load faster.
+ *   slots      device, [num_tokens] int64, no slot twice; -1 skips a token
+ * A slot outside the cache is skipped and sets the device error word.  An
+ * infinity is stored as the largest value of its sign and a NaN as zero, and
+ * either sets the error word.
+ */
+kda_status_t kda_cache_append(const kda_cache_t* cache, int32_t io_dtype, int32_t num_tokens,
+                              const void* k, const void* v, const int64_t* strides,
+                              const int64_t* slots, kda_stream_t stream);
+
+/*
+ * kda_cache_read -- the inverse of kda_cache_append: the values that the cache
+ * holds at slots, written packed to k, v [num_tokens, num_kv_heads, head_dim]
+ * (io dtype, 16-byte aligned).  They have at most 6 significant bits, so bf16
+ * holds them exactly.  Slot -1 reads as zeros; one outside the cache too, and
+ * sets the device error word.
+ */
+kda_status_t kda_cache_read(const kda_cache_t* cache, int32_t io_dtype, int32_t num_tokens,
+                            const int64_t* slots, void* k, void* v, kda_stream_t stream);
+
+/*
+ * kda_cache_attention -- attention of each request's new tokens over its cache.
+ *
+ * New token i (0 <= i < n_b = cu_new[b+1] - cu_new[b]) of request b is the
+ * request's token kv_lens[b] - n_b + i (append it first) and sees the tokens up
+ * to and including itself:
+ *
+ *     out = sum_j p_j v_j,   p = softmax_j (scale q . k_j),  j <= kv_lens[b] - n_b + i
+ *
+ * Query head h reads kv head h / (num_heads / num_kv_heads).  One new token per
+ * request is a decode step, a few are a drafted window, many a prefill chunk.
+ * A row that sees no token (kv_lens[b] < n_b) gives zeros and the log-sum-exp
+ * -infinity.  Scores, softmax statistics and sums are fp32; see the kernels for
+ * the operands' types.  Bytes of a page past the request's length are not used,
+ * whatever they are.
+ *
+ *   q             device, [total_tokens, num_heads, head_dim] io dtype, tokens
+ *                 and heads q_strides[0], q_strides[1] elements apart (both 0:
+ *                 packed), channels contiguous
+ *   block_table   device, [num_seqs][max_blocks] int32
+ *   kv_lens       device, [num_seqs] int32
+ *   cu_new        device, [num_seqs + 1] int32
+ *   out           device, [total_tokens, num_heads, head_dim] io dtype, 16-byte
+ *                 aligned; tokens past cu_new[num_seqs] are not written
+ *   lse           device, [total_tokens, num_heads] fp32 or NULL: natural log of
+ *                 the sum of exp(scale q . k_j)
+ *
+ * desc->max_new is the largest n_b that the caller expects: it sizes the
+ * workspace and the launches (a larger n_b gives the same results, slower).
+ * Checked on the device: a request whose cu_new or kv_lens is out of range is
+ * skipped; a page index outside the cache hides that page's tokens; both set the
+ * device error word.
+ */
+typedef struct {
+  int32_t num_seqs;
+  int32_t total_tokens;  /* packed new tokens (room for them in q and out)      */
+  int32_t num_heads;     /* query heads, a multiple of the cache's num_kv_heads */
+  int32_t max_new;       /* new tokens of the longest request, >= 1             */
+  int32_t max_blocks;    /* columns of block_table                              */
+  int32_t io_dtype;      /* kda_dtype_t of q and out                            */
+  float scale;           /* of the scores; finite                               */
+  int64_t q_strides[2];
+  void* workspace;       /* device, 256-byte aligned                            */
+  size_t workspace_bytes;
+} kda_attention_t;
+
+kda_status_t kda_cache_attention(const kda_cache_t* cache, const kda_attention_t* desc,
+                                 const void* q, const int32_t* block_table,
+                                 const int32_t* kv_lens, const int32_t* cu_new, void* out,
+                                 float* lse, kda_stream_t stream);
+
+/* Bytes of device scratch that kda_cache_attention needs for this descriptor
+ * (on the current device; the workspace fields are not read). */
+kda_status_t kda_cache_attention_workspace_size(const kda_cache_t* cache,
+                                                const kda_attention_t* desc, size_t* bytes);
+
 const char* kda_status_string(kda_status_t status);
 
 /* Synchronise `stream`, then read and clear the device error word of the

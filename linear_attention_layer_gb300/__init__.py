@@ -9,6 +9,8 @@ Entry points (same names as the C ABI, without the ``kda_`` prefix):
     chunk_fwd      -- chunked prefill over a packed variable-length batch
     recurrent_fwd  -- token-by-token prefill (the GPU reference path)
     decode_step    -- one token for each live request, state updated in place
+    cache_tables, cache_append, cache_read, cache_attention
+                   -- the full-attention layers' 4-bit paged cache
 """
 from __future__ import annotations
 
@@ -26,7 +28,9 @@ __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "recurrent_fwd", "decode_step",
            "chunk_fwd_host_workspace_size", "chunk_fwd_summary",
            "chunk_fwd_summary_workspace_size", "state_scan", "decode_step_fused",
            "decode_replay_window_fused", "chunk_fwd_fused", "chunk_bwd",
-           "chunk_bwd_workspace_size", "EXPORTED_SYMBOLS"]
+           "chunk_bwd_workspace_size", "cache_empty", "cache_tables", "cache_append",
+           "cache_read", "cache_attention", "cache_attention_workspace_size",
+           "EXPORTED_SYMBOLS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libkda.so")
 
@@ -45,7 +49,9 @@ EXPORTED_SYMBOLS = ("kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_recurr
                     "kda_chunk_fwd_summary", "kda_chunk_fwd_summary_workspace_size",
                     "kda_state_scan", "kda_decode_step_fused",
                     "kda_decode_replay_window_fused", "kda_chunk_fwd_fused", "kda_chunk_bwd",
-                    "kda_chunk_bwd_workspace_size")
+                    "kda_chunk_bwd_workspace_size", "kda_cache_tables", "kda_cache_append",
+                    "kda_cache_read", "kda_cache_attention",
+                    "kda_cache_attention_workspace_size")
 
 #: Size of the library's own scratch array used by chunk_fwd_noalloc
 #: (KDA_NOALLOC_SCRATCH_BYTES in include/kda.h).
@@ -73,6 +79,21 @@ class KdaFusion(ctypes.Structure):
                 ("conv_weight_k", ctypes.c_void_p), ("conv_state_q", ctypes.c_void_p),
                 ("conv_state_k", ctypes.c_void_p), ("out_norm_weight", ctypes.c_void_p),
                 ("out_norm_eps", ctypes.c_float)]
+
+
+class KdaCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("k_exponent", ctypes.c_void_p),
+                ("v_exponent", ctypes.c_void_p)]
+
+
+class KdaAttention(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q_strides", ctypes.c_int64 * 2),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -125,6 +146,18 @@ def load() -> ctypes.CDLL:
         lib.kda_decode_replay_window_fused.restype = ctypes.c_int
         lib.kda_decode_replay_window_fused.argtypes = (
             [dp, fp, ctypes.c_int32] + [vp] * 6 + [ctypes.c_int32] + [vp] * 8)
+        cp, ap, i32 = ctypes.POINTER(KdaCache), ctypes.POINTER(KdaAttention), ctypes.c_int32
+        lib.kda_cache_tables.restype = ctypes.c_int
+        lib.kda_cache_tables.argtypes = [i32] * 5 + [vp] * 11
+        lib.kda_cache_append.restype = ctypes.c_int
+        lib.kda_cache_append.argtypes = [cp, i32, i32] + [vp] * 5
+        lib.kda_cache_read.restype = ctypes.c_int
+        lib.kda_cache_read.argtypes = [cp, i32, i32] + [vp] * 4
+        lib.kda_cache_attention.restype = ctypes.c_int
+        lib.kda_cache_attention.argtypes = [cp, ap] + [vp] * 7
+        lib.kda_cache_attention_workspace_size.restype = ctypes.c_int
+        lib.kda_cache_attention_workspace_size.argtypes = [cp, ap,
+                                                           ctypes.POINTER(ctypes.c_size_t)]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_testing_inject_wait_timeout.restype = None
@@ -873,3 +906,223 @@ def state_scan(transitions, offsets, initial_state=None, *, count=None, out=None
     if st != KDA_OK:
         raise KDAError(st, "kda_state_scan")
     return out
+
+
+# ------------------------------------------------- the 4-bit paged cache ---
+
+def cache_empty(num_pages, page_size, num_kv_heads, head_dim, device="cuda"):
+    """A cache for one attention layer: uint8 [num_pages, num_kv_heads,
+    page_size / 16, 18 * head_dim] (byte layout in include/kda.h), 9/8 of a byte
+    for each key/value channel pair.  The contents are undefined until appended."""
+    if page_size <= 0 or page_size % 16 or page_size > 4096:
+        raise ValueError(f"page_size must be a multiple of 16 up to 4096, got {page_size}")
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    return torch.empty((num_pages, num_kv_heads, page_size // 16, 18 * head_dim),
+                       dtype=torch.uint8, device=device)
+
+
+def _cache_struct(cache, k_exponent, v_exponent):
+    """The kda_cache_t of a cache tensor."""
+    if cache.dim() != 4 or cache.shape[3] % 18:
+        raise ValueError("cache must be uint8 [num_pages, kv heads, page_size / 16, 18 head_dim], "
+                         f"got {tuple(cache.shape)}")
+    _check_tensor("cache", cache, torch.uint8, cache.shape, cache.device)
+    c = KdaCache()
+    c.pages = ctypes.c_void_p(cache.data_ptr())
+    c.num_pages, c.num_kv_heads = cache.shape[0], cache.shape[1]
+    c.page_size, c.head_dim = cache.shape[2] * 16, cache.shape[3] // 18
+    for name, e in (("k_exponent", k_exponent), ("v_exponent", v_exponent)):
+        if e is not None:
+            _check_tensor(name, e, torch.int32, (cache.shape[1],), cache.device)
+            setattr(c, name, ctypes.c_void_p(e.data_ptr()))
+    return c
+
+
+def _row_strides(name, t, dtype, shape, device):
+    """Token and head strides of a [T, H, D] tensor whose channels are contiguous."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def _new_on(stream, device):
+    """Allocations made inside belong to the stream that the call runs on."""
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+
+
+def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_range, *,
+                 page_size, max_tokens, kv_lens=None, cu_new=None, slots=None,
+                 free_range_out=None, stream=None):
+    """``kda_cache_tables``: take and give back pages as the requests' lengths
+    change.  held_lens, seq_lens, new_lens int32 [B] (tokens with pages now,
+    tokens that stay, tokens to come; new_lens -1 ends a request), block_table
+    int32 [B, max_blocks] and free_pages int32 (a ring) updated in place,
+    free_range int64 [2].  Returns (kv_lens [B], cu_new [B + 1], slots
+    [max_tokens], free_range_out [2]); kv_lens may be held_lens or seq_lens and
+    free_range_out may be free_range, for a loop that updates in place."""
+    lib = load()
+    dev = held_lens.device
+    B = held_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    for name, t in (("held_lens", held_lens), ("seq_lens", seq_lens), ("new_lens", new_lens)):
+        _check_tensor(name, t, torch.int32, (B,), dev)
+    _check_tensor("block_table", block_table, torch.int32, (B, block_table.shape[1]), dev)
+    _check_tensor("free_pages", free_pages, torch.int32, (free_pages.numel(),), dev)
+    _check_tensor("free_range", free_range, torch.int64, (2,), dev)
+    max_tokens = int(max_tokens)
+    with torch.cuda.device(dev), _new_on(stream, dev):
+        if kv_lens is None:
+            kv_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        if cu_new is None:
+            cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty(max(max_tokens, 0), dtype=torch.int64, device=dev)
+        if free_range_out is None:
+            free_range_out = torch.empty(2, dtype=torch.int64, device=dev)
+    _check_tensor("kv_lens", kv_lens, torch.int32, (B,), dev)
+    _check_tensor("cu_new", cu_new, torch.int32, (B + 1,), dev)
+    _check_tensor("slots", slots, torch.int64, (max_tokens,), dev)
+    _check_tensor("free_range_out", free_range_out, torch.int64, (2,), dev)
+    with torch.cuda.device(dev):
+        st = lib.kda_cache_tables(int(page_size), B, block_table.shape[1], max_tokens,
+                                  free_pages.numel(), _ptr(held_lens), _ptr(seq_lens),
+                                  _ptr(new_lens), _ptr(block_table), _ptr(free_pages),
+                                  _ptr(free_range), _ptr(free_range_out), _ptr(kv_lens),
+                                  _ptr(cu_new), _ptr(slots), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_tables")
+    return kv_lens, cu_new, slots, free_range_out
+
+
+def cache_append(k, v, slots, cache, *, k_exponent=None, v_exponent=None, stream=None):
+    """``kda_cache_append``: quantise k, v [T, kv heads, head_dim] (fp32 or bf16;
+    slices of a larger tensor will do, the channels contiguous) into ``cache`` at
+    ``slots`` int64 [T] (-1 skips a token)."""
+    lib = load()
+    dev = cache.device
+    c = _cache_struct(cache, k_exponent, v_exponent)
+    io = _io_code(k.dtype)
+    shape = (slots.numel(), c.num_kv_heads, c.head_dim)
+    strides = (ctypes.c_int64 * 4)(*_row_strides("k", k, k.dtype, shape, dev),
+                                   *_row_strides("v", v, k.dtype, shape, dev))
+    _check_tensor("slots", slots, torch.int64, (slots.numel(),), dev)
+    with torch.cuda.device(dev):
+        st = lib.kda_cache_append(ctypes.byref(c), io, shape[0], _ptr(k), _ptr(v), strides,
+                                  _ptr(slots), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_append")
+
+
+def cache_read(slots, cache, dtype=torch.bfloat16, *, k_exponent=None, v_exponent=None, k=None,
+               v=None, stream=None):
+    """``kda_cache_read``: the values that ``cache`` holds at ``slots`` int64 [T], as
+    (k, v) [T, kv heads, head_dim] of ``dtype`` (-1 reads as zeros)."""
+    lib = load()
+    dev = cache.device
+    c = _cache_struct(cache, k_exponent, v_exponent)
+    io = _io_code(dtype)
+    shape = (slots.numel(), c.num_kv_heads, c.head_dim)
+    _check_tensor("slots", slots, torch.int64, (slots.numel(),), dev)
+    with torch.cuda.device(dev), _new_on(stream, dev):
+        k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
+    _check_tensor("k", k, dtype, shape, dev)
+    _check_tensor("v", v, dtype, shape, dev)
+    with torch.cuda.device(dev):
+        st = lib.kda_cache_read(ctypes.byref(c), io, shape[0], _ptr(slots), _ptr(k), _ptr(v),
+                                _stream_handle(stream))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_read")
+    return k, v
+
+
+def _attention_desc(q_shape, num_seqs, max_new, max_blocks, dtype, scale):
+    d = KdaAttention()
+    d.num_seqs, d.total_tokens, d.num_heads = int(num_seqs), int(q_shape[0]), int(q_shape[1])
+    d.max_new, d.max_blocks, d.io_dtype = int(max_new), int(max_blocks), _io_code(dtype)
+    d.scale = float(q_shape[2]) ** -0.5 if scale is None else float(scale)
+    return d
+
+
+def cache_attention_workspace_size(cache, num_seqs, total_tokens, num_heads, max_new, max_blocks,
+                                   dtype):
+    """Bytes of device scratch that ``cache_attention`` needs for calls of this shape."""
+    c = _cache_struct(cache, None, None)
+    d = _attention_desc((total_tokens, num_heads, c.head_dim), num_seqs, max_new, max_blocks,
+                        dtype, None)
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(cache.device):
+        st = load().kda_cache_attention_workspace_size(ctypes.byref(c), ctypes.byref(d),
+                                                       ctypes.byref(n))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_attention_workspace_size")
+    return int(n.value)
+
+
+def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=None,
+                    k_exponent=None, v_exponent=None, out=None, return_lse=False, lse=None,
+                    workspace="auto", stream=None):
+    """``kda_cache_attention``: causal attention of the new tokens q [T, heads,
+    head_dim] (packed over the requests by cu_new int32 [B + 1]; their keys are in
+    the cache already) over ``cache`` through block_table int32 [B, max_blocks] and
+    kv_lens int32 [B], the lengths with the new tokens.  ``max_new``: new tokens of
+    the longest request (1 for a decode step).  ``scale``: of the scores, default
+    head_dim ** -0.5.  Returns out [T, heads, head_dim], with ``return_lse`` also
+    the log-sum-exp [T, heads] fp32.  ``workspace``: a uint8 tensor of
+    ``cache_attention_workspace_size`` bytes or "auto" (allocated here)."""
+    lib = load()
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, head_dim]")
+    dev = cache.device
+    c = _cache_struct(cache, k_exponent, v_exponent)
+    T, H, D = q.shape
+    B = kv_lens.numel()
+    if D != c.head_dim or H % c.num_kv_heads:
+        raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {c.num_kv_heads} heads of "
+                         f"{c.head_dim} channels")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    _check_tensor("block_table", block_table, torch.int32, (B, block_table.shape[1]), dev)
+    _check_tensor("kv_lens", kv_lens, torch.int32, (B,), dev)
+    _check_tensor("cu_new", cu_new, torch.int32, (B + 1,), dev)
+    d = _attention_desc(q.shape, B, max_new, block_table.shape[1], q.dtype, scale)
+    st_t, st_h = _row_strides("q", q, q.dtype, (T, H, D), dev)
+    if not q.is_contiguous():
+        d.q_strides[0], d.q_strides[1] = st_t, st_h
+    auto = isinstance(workspace, str)
+    if auto and workspace != "auto":
+        raise ValueError("workspace must be a tensor or 'auto'")
+    with torch.cuda.device(dev), _new_on(stream, dev):
+        if out is None:
+            out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+        if lse is None and return_lse:
+            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        if auto:
+            n = ctypes.c_size_t(0)
+            st = lib.kda_cache_attention_workspace_size(ctypes.byref(c), ctypes.byref(d),
+                                                        ctypes.byref(n))
+            if st != KDA_OK:
+                raise KDAError(st, "kda_cache_attention_workspace_size")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+    _check_tensor("out", out, q.dtype, (T, H, D), dev)
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, (T, H), dev)
+    if workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+        d.workspace = ctypes.c_void_p(workspace.data_ptr())
+        d.workspace_bytes = workspace.numel()
+    with torch.cuda.device(dev):
+        st = lib.kda_cache_attention(ctypes.byref(c), ctypes.byref(d), _ptr(q), _ptr(block_table),
+                                     _ptr(kv_lens), _ptr(cu_new), _ptr(out), _ptr(lse),
+                                     _stream_handle(stream))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_attention")
+    return (out, lse) if return_lse else out

@@ -220,6 +220,70 @@ size_t chunk_fwd_host_workspace_bytes(const Problem& p, bool gate_per_head);
 cudaError_t launch_chunk_fwd_host(const Problem& p, const HostArgs& h, int groups, void* ws,
                                   cudaStream_t stream);
 
+// The 4-bit paged cache (kda_cache.cuh).
+namespace cache {
+struct View {
+  uint8_t* pages;
+  int num_pages;
+  int page_size;
+  int kv_heads;
+  const int32_t* k_exp;  // may be null
+  const int32_t* v_exp;
+};
+}  // namespace cache
+
+// Block tables, slots and the free-page ring from lengths (kda_cache_tables.cu).
+struct TableArgs {
+  int page_size, num_seqs, max_blocks, max_tokens, ring_size;
+  const int32_t* held_lens;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* block_table;
+  int32_t* free_pages;
+  const int64_t* free_range;
+  int64_t* free_range_out;  // may equal free_range
+  int32_t* kv_lens;         // may equal held_lens or seq_lens
+  int32_t* cu_new;
+  int64_t* slots;
+  int* err;
+};
+cudaError_t launch_cache_tables(const TableArgs& a, cudaStream_t st);
+
+// Values into and out of the cache (kda_cache_store.cu).
+struct CacheArgs {
+  cache::View view;
+  int head_dim;
+  int bf16;
+  int tokens;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  int64_t strides[4] = {};  // elements: k token, k head, v token, v head
+  const int64_t* slots = nullptr;
+  void* k_out = nullptr;
+  void* v_out = nullptr;
+  int* err = nullptr;
+};
+cudaError_t launch_cache_append(const CacheArgs& a, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheArgs& a, cudaStream_t st);
+
+// Attention over the cache (kda_cache_attention.cu).
+struct AttentionArgs {
+  int num_seqs, total_tokens, num_heads, head_dim, max_new, max_blocks;
+  int bf16;
+  float scale;
+  int64_t q_token_stride, q_head_stride;  // elements
+  const void* q = nullptr;
+  const int32_t* block_table = nullptr;
+  const int32_t* kv_lens = nullptr;
+  const int32_t* cu_new = nullptr;
+  void* out = nullptr;
+  float* lse = nullptr;  // may be null
+  void* workspace = nullptr;
+  int* err = nullptr;
+};
+size_t cache_attention_workspace_bytes(const cache::View& c, const AttentionArgs& a);
+cudaError_t launch_cache_attention(const cache::View& c, const AttentionArgs& a, cudaStream_t st);
+
 }  // namespace kda
 
 #include "../../include/kda.h"
