@@ -83,6 +83,13 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
       : "r"(w));
 }
 
+// Product of two pairs of halves.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // E2M1 codes of (lo, hi), nearest with ties to even, saturating: one byte.
 __device__ __forceinline__ uint32_t f32x2_to_e2m1(float lo, float hi) {
   uint32_t r;
