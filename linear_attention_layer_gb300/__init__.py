@@ -103,6 +103,8 @@ _lock = threading.Lock()
 def load() -> ctypes.CDLL:
     """Load libkda.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -922,39 +924,76 @@ def cache_empty(num_pages, page_size, num_kv_heads, head_dim, device="cuda"):
                        dtype=torch.uint8, device=device)
 
 
-def _cache_struct(cache, k_exponent, v_exponent):
+# The cache calls take microseconds on the GPU, and a decode step makes them once a layer: their
+# checks look at each tensor once and describe what is wrong only when something is.
+
+def _bad(name, t, dtype, shape, device):
+    """Raises what is wrong with a tensor that a call's quick check refused."""
+    _check_tensor(name, t, dtype, shape, device)
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)}, contiguous, on {device}")
+
+
+def _need(name, t, dtype, shape, device):
+    if t is None or t.dtype != dtype or t.shape != shape or t.device != device or \
+            not t.is_contiguous():
+        _bad(name, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _need_rows(name, t, dtype, shape, device):
+    """The same for [T, heads, channels] with strides; only the channels are contiguous."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or \
+            (t.stride(2) != 1 and t.numel()):
+        if t.device == device and t.dtype == dtype and t.shape == shape:
+            raise ValueError(f"{name}'s channels must be contiguous")
+        _bad(name, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _cuda_only(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+    return t.device
+
+
+class _Launch:
+    """Makes ``device`` current for a call and its allocations, which belong to the stream
+    that the call runs on."""
+    __slots__ = ("handle", "device", "stream")
+
+    def __init__(self, device, stream):
+        self.device = None if device.index == torch.cuda.current_device() else \
+            torch.cuda.device(device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+        self.handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
+            stream.cuda_stream
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _cache_struct(cache, k_exponent, v_exponent, device):
     """The kda_cache_t of a cache tensor."""
-    if cache.dim() != 4 or cache.shape[3] % 18:
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] % 18:
         raise ValueError("cache must be uint8 [num_pages, kv heads, page_size / 16, 18 head_dim], "
-                         f"got {tuple(cache.shape)}")
-    _check_tensor("cache", cache, torch.uint8, cache.shape, cache.device)
-    c = KdaCache()
-    c.pages = ctypes.c_void_p(cache.data_ptr())
-    c.num_pages, c.num_kv_heads = cache.shape[0], cache.shape[1]
-    c.page_size, c.head_dim = cache.shape[2] * 16, cache.shape[3] // 18
-    for name, e in (("k_exponent", k_exponent), ("v_exponent", v_exponent)):
-        if e is not None:
-            _check_tensor(name, e, torch.int32, (cache.shape[1],), cache.device)
-            setattr(c, name, ctypes.c_void_p(e.data_ptr()))
-    return c
-
-
-def _row_strides(name, t, dtype, shape, device):
-    """Token and head strides of a [T, H, D] tensor whose channels are contiguous."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() and t.stride(2) != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
-    return t.stride(0), t.stride(1)
-
-
-def _new_on(stream, device):
-    """Allocations made inside belong to the stream that the call runs on."""
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+                         f"got {tuple(shape)}")
+    heads = (shape[1],)
+    return KdaCache(
+        _need("cache", cache, torch.uint8, shape, device), shape[0], shape[2] * 16, shape[1],
+        shape[3] // 18,
+        None if k_exponent is None else _need("k_exponent", k_exponent, torch.int32, heads, device),
+        None if v_exponent is None else _need("v_exponent", v_exponent, torch.int32, heads, device))
 
 
 def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_range, *,
@@ -968,35 +1007,35 @@ def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_ra
     [max_tokens], free_range_out [2]); kv_lens may be held_lens or seq_lens and
     free_range_out may be free_range, for a loop that updates in place."""
     lib = load()
-    dev = held_lens.device
+    dev = _cuda_only("held_lens", held_lens)
     B = held_lens.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
-    for name, t in (("held_lens", held_lens), ("seq_lens", seq_lens), ("new_lens", new_lens)):
-        _check_tensor(name, t, torch.int32, (B,), dev)
-    _check_tensor("block_table", block_table, torch.int32, (B, block_table.shape[1]), dev)
-    _check_tensor("free_pages", free_pages, torch.int32, (free_pages.numel(),), dev)
-    _check_tensor("free_range", free_range, torch.int64, (2,), dev)
+    blocks, ring = block_table.shape[1], free_pages.numel()
+    lens, i32, i64 = (B,), torch.int32, torch.int64
     max_tokens = int(max_tokens)
-    with torch.cuda.device(dev), _new_on(stream, dev):
+    if max_tokens < 0:
+        raise ValueError(f"max_tokens must not be negative, got {max_tokens}")
+    with _Launch(dev, stream) as handle:
         if kv_lens is None:
-            kv_lens = torch.empty(B, dtype=torch.int32, device=dev)
+            kv_lens = torch.empty(B, dtype=i32, device=dev)
         if cu_new is None:
-            cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+            cu_new = torch.empty(B + 1, dtype=i32, device=dev)
         if slots is None:
-            slots = torch.empty(max(max_tokens, 0), dtype=torch.int64, device=dev)
+            slots = torch.empty(max_tokens, dtype=i64, device=dev)
         if free_range_out is None:
-            free_range_out = torch.empty(2, dtype=torch.int64, device=dev)
-    _check_tensor("kv_lens", kv_lens, torch.int32, (B,), dev)
-    _check_tensor("cu_new", cu_new, torch.int32, (B + 1,), dev)
-    _check_tensor("slots", slots, torch.int64, (max_tokens,), dev)
-    _check_tensor("free_range_out", free_range_out, torch.int64, (2,), dev)
-    with torch.cuda.device(dev):
-        st = lib.kda_cache_tables(int(page_size), B, block_table.shape[1], max_tokens,
-                                  free_pages.numel(), _ptr(held_lens), _ptr(seq_lens),
-                                  _ptr(new_lens), _ptr(block_table), _ptr(free_pages),
-                                  _ptr(free_range), _ptr(free_range_out), _ptr(kv_lens),
-                                  _ptr(cu_new), _ptr(slots), _stream_handle(stream))
+            free_range_out = torch.empty(2, dtype=i64, device=dev)
+        st = lib.kda_cache_tables(
+            int(page_size), B, blocks, max_tokens, ring,
+            _need("held_lens", held_lens, i32, lens, dev),
+            _need("seq_lens", seq_lens, i32, lens, dev),
+            _need("new_lens", new_lens, i32, lens, dev),
+            _need("block_table", block_table, i32, (B, blocks), dev),
+            _need("free_pages", free_pages, i32, (ring,), dev),
+            _need("free_range", free_range, i64, (2,), dev),
+            _need("free_range_out", free_range_out, i64, (2,), dev),
+            _need("kv_lens", kv_lens, i32, lens, dev), _need("cu_new", cu_new, i32, (B + 1,), dev),
+            _need("slots", slots, i64, (max_tokens,), dev), handle)
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_tables")
     return kv_lens, cu_new, slots, free_range_out
@@ -1007,16 +1046,16 @@ def cache_append(k, v, slots, cache, *, k_exponent=None, v_exponent=None, stream
     slices of a larger tensor will do, the channels contiguous) into ``cache`` at
     ``slots`` int64 [T] (-1 skips a token)."""
     lib = load()
-    dev = cache.device
-    c = _cache_struct(cache, k_exponent, v_exponent)
-    io = _io_code(k.dtype)
-    shape = (slots.numel(), c.num_kv_heads, c.head_dim)
-    strides = (ctypes.c_int64 * 4)(*_row_strides("k", k, k.dtype, shape, dev),
-                                   *_row_strides("v", v, k.dtype, shape, dev))
-    _check_tensor("slots", slots, torch.int64, (slots.numel(),), dev)
-    with torch.cuda.device(dev):
-        st = lib.kda_cache_append(ctypes.byref(c), io, shape[0], _ptr(k), _ptr(v), strides,
-                                  _ptr(slots), _stream_handle(stream))
+    dev = _cuda_only("cache", cache)
+    c = _cache_struct(cache, k_exponent, v_exponent, dev)
+    T = slots.numel()
+    shape, dtype = (T, c.num_kv_heads, c.head_dim), k.dtype
+    io = _io_code(dtype)
+    kp, vp = _need_rows("k", k, dtype, shape, dev), _need_rows("v", v, dtype, shape, dev)
+    strides = (ctypes.c_int64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
+    with _Launch(dev, stream) as handle:
+        st = lib.kda_cache_append(c, io, T, kp, vp, strides,
+                                  _need("slots", slots, torch.int64, (T,), dev), handle)
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_append")
 
@@ -1026,45 +1065,41 @@ def cache_read(slots, cache, dtype=torch.bfloat16, *, k_exponent=None, v_exponen
     """``kda_cache_read``: the values that ``cache`` holds at ``slots`` int64 [T], as
     (k, v) [T, kv heads, head_dim] of ``dtype`` (-1 reads as zeros)."""
     lib = load()
-    dev = cache.device
-    c = _cache_struct(cache, k_exponent, v_exponent)
+    dev = _cuda_only("cache", cache)
+    c = _cache_struct(cache, k_exponent, v_exponent, dev)
     io = _io_code(dtype)
-    shape = (slots.numel(), c.num_kv_heads, c.head_dim)
-    _check_tensor("slots", slots, torch.int64, (slots.numel(),), dev)
-    with torch.cuda.device(dev), _new_on(stream, dev):
-        k = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-    _check_tensor("k", k, dtype, shape, dev)
-    _check_tensor("v", v, dtype, shape, dev)
-    with torch.cuda.device(dev):
-        st = lib.kda_cache_read(ctypes.byref(c), io, shape[0], _ptr(slots), _ptr(k), _ptr(v),
-                                _stream_handle(stream))
+    T = slots.numel()
+    shape = (T, c.num_kv_heads, c.head_dim)
+    with _Launch(dev, stream) as handle:
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=dev)
+        st = lib.kda_cache_read(c, io, T, _need("slots", slots, torch.int64, (T,), dev),
+                                _need("k", k, dtype, shape, dev),
+                                _need("v", v, dtype, shape, dev), handle)
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_read")
     return k, v
 
 
-def _attention_desc(q_shape, num_seqs, max_new, max_blocks, dtype, scale):
-    d = KdaAttention()
-    d.num_seqs, d.total_tokens, d.num_heads = int(num_seqs), int(q_shape[0]), int(q_shape[1])
-    d.max_new, d.max_blocks, d.io_dtype = int(max_new), int(max_blocks), _io_code(dtype)
-    d.scale = float(q_shape[2]) ** -0.5 if scale is None else float(scale)
-    return d
-
-
 def cache_attention_workspace_size(cache, num_seqs, total_tokens, num_heads, max_new, max_blocks,
                                    dtype):
     """Bytes of device scratch that ``cache_attention`` needs for calls of this shape."""
-    c = _cache_struct(cache, None, None)
-    d = _attention_desc((total_tokens, num_heads, c.head_dim), num_seqs, max_new, max_blocks,
-                        dtype, None)
+    dev = _cuda_only("cache", cache)
+    c = _cache_struct(cache, None, None, dev)
+    with _Launch(dev, None):
+        return _attention_workspace(c, KdaAttention(
+            int(num_seqs), int(total_tokens), int(num_heads), int(max_new), int(max_blocks),
+            _io_code(dtype), 1.0))
+
+
+def _attention_workspace(c, d):
     n = ctypes.c_size_t(0)
-    with torch.cuda.device(cache.device):
-        st = load().kda_cache_attention_workspace_size(ctypes.byref(c), ctypes.byref(d),
-                                                       ctypes.byref(n))
+    st = load().kda_cache_attention_workspace_size(c, d, ctypes.byref(n))
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_attention_workspace_size")
-    return int(n.value)
+    return n.value
 
 
 def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=None,
@@ -1079,50 +1114,39 @@ def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=No
     the log-sum-exp [T, heads] fp32.  ``workspace``: a uint8 tensor of
     ``cache_attention_workspace_size`` bytes or "auto" (allocated here)."""
     lib = load()
-    if q.dim() != 3:
-        raise ValueError("q must be [T, heads, head_dim]")
-    dev = cache.device
-    c = _cache_struct(cache, k_exponent, v_exponent)
-    T, H, D = q.shape
-    B = kv_lens.numel()
+    dev = _cuda_only("cache", cache)
+    c = _cache_struct(cache, k_exponent, v_exponent, dev)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [T, heads, head_dim] and block_table [B, max_blocks]")
+    shape, dtype = q.shape, q.dtype
+    T, H, D = shape
+    B, blocks = kv_lens.numel(), block_table.shape[1]
     if D != c.head_dim or H % c.num_kv_heads:
-        raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {c.num_kv_heads} heads of "
+        raise ValueError(f"q {tuple(shape)} does not fit a cache of {c.num_kv_heads} heads of "
                          f"{c.head_dim} channels")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    _check_tensor("block_table", block_table, torch.int32, (B, block_table.shape[1]), dev)
-    _check_tensor("kv_lens", kv_lens, torch.int32, (B,), dev)
-    _check_tensor("cu_new", cu_new, torch.int32, (B + 1,), dev)
-    d = _attention_desc(q.shape, B, max_new, block_table.shape[1], q.dtype, scale)
-    st_t, st_h = _row_strides("q", q, q.dtype, (T, H, D), dev)
+    i32 = torch.int32
+    qp = _need_rows("q", q, dtype, shape, dev)
+    d = KdaAttention(B, T, H, int(max_new), blocks, _io_code(dtype),
+                     D ** -0.5 if scale is None else float(scale))
     if not q.is_contiguous():
-        d.q_strides[0], d.q_strides[1] = st_t, st_h
-    auto = isinstance(workspace, str)
-    if auto and workspace != "auto":
-        raise ValueError("workspace must be a tensor or 'auto'")
-    with torch.cuda.device(dev), _new_on(stream, dev):
+        d.q_strides[0], d.q_strides[1] = q.stride(0), q.stride(1)
+    with _Launch(dev, stream) as handle:
         if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+            out = torch.empty(shape, dtype=dtype, device=dev)
         if lse is None and return_lse:
             lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        if auto:
-            n = ctypes.c_size_t(0)
-            st = lib.kda_cache_attention_workspace_size(ctypes.byref(c), ctypes.byref(d),
-                                                        ctypes.byref(n))
-            if st != KDA_OK:
-                raise KDAError(st, "kda_cache_attention_workspace_size")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
-    _check_tensor("out", out, q.dtype, (T, H, D), dev)
-    if lse is not None:
-        _check_tensor("lse", lse, torch.float32, (T, H), dev)
-    if workspace is not None:
-        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
-        d.workspace = ctypes.c_void_p(workspace.data_ptr())
-        d.workspace_bytes = workspace.numel()
-    with torch.cuda.device(dev):
-        st = lib.kda_cache_attention(ctypes.byref(c), ctypes.byref(d), _ptr(q), _ptr(block_table),
-                                     _ptr(kv_lens), _ptr(cu_new), _ptr(out), _ptr(lse),
-                                     _stream_handle(stream))
+        if isinstance(workspace, str):
+            if workspace != "auto":
+                raise ValueError("workspace must be a tensor or 'auto'")
+            workspace = torch.empty(_attention_workspace(c, d), dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            d.workspace_bytes = workspace.numel()
+            d.workspace = _need("workspace", workspace, torch.uint8, (d.workspace_bytes,), dev)
+        st = lib.kda_cache_attention(
+            c, d, qp, _need("block_table", block_table, i32, (B, blocks), dev),
+            _need("kv_lens", kv_lens, i32, (B,), dev), _need("cu_new", cu_new, i32, (B + 1,), dev),
+            _need("out", out, dtype, shape, dev),
+            None if lse is None else _need("lse", lse, torch.float32, (T, H), dev), handle)
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_attention")
     return (out, lse) if return_lse else out
