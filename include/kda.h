@@ -654,9 +654,9 @@ kda_status_t kda_state_scan(const kda_desc_t* desc, int32_t count, const float* 
  */
 typedef struct {
   void* pages;              /* device, 16-byte aligned                        */
-  int32_t num_pages;        /* >= 0                                           */
+  int32_t num_pages;        /* >= 0; num_pages * page_size < 2^31             */
   int32_t page_size;        /* tokens per page: a multiple of 16, <= 4096     */
-  int32_t num_kv_heads;     /* >= 1                                           */
+  int32_t num_kv_heads;     /* 1 .. 4096                                      */
   int32_t head_dim;         /* 64 or 128                                      */
   const int32_t* k_exponent; /* device [num_kv_heads], -64 .. 64, or NULL (0) */
   const int32_t* v_exponent; /* device [num_kv_heads], -64 .. 64, or NULL (0) */
@@ -699,6 +699,7 @@ typedef struct {
  * held than its row has room for gets kv_lens[b] = 0 and slots -1, and its pages
  * stay where they are.  Tokens past max_tokens get no slot.  A free_range that
  * is negative, reversed or longer than the ring counts as empty.
+ * num_seqs * max_blocks < 2^31 (else KDA_ERR_UNSUPPORTED).
  */
 kda_status_t kda_cache_tables(int32_t page_size, int32_t num_seqs, int32_t max_blocks,
                               int32_t max_tokens, int32_t ring_size, const int32_t* held_lens,

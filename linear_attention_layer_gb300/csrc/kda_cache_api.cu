@@ -16,7 +16,8 @@ kda_status_t check_cache(const kda_cache_t* c) {
     return KDA_ERR_INVALID_ARGUMENT;
   if (c->page_size % 16 != 0 || c->page_size > 4096) return KDA_ERR_INVALID_ARGUMENT;
   if (c->head_dim != 64 && c->head_dim != 128) return KDA_ERR_UNSUPPORTED;
-  if (c->num_kv_heads > 65536) return KDA_ERR_UNSUPPORTED;
+  if (c->num_kv_heads > 4096) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)c->num_pages * c->page_size > INT32_MAX) return KDA_ERR_UNSUPPORTED;
   if ((c->num_pages > 0 && !c->pages) || !aligned(c->pages, 16)) return KDA_ERR_INVALID_ARGUMENT;
   if (!aligned(c->k_exponent, 4) || !aligned(c->v_exponent, 4)) return KDA_ERR_INVALID_ARGUMENT;
   return KDA_OK;
@@ -77,6 +78,7 @@ kda_status_t kda_cache_tables(int32_t page_size, int32_t num_seqs, int32_t max_b
   if (page_size <= 0 || page_size % 16 != 0 || page_size > 4096) return KDA_ERR_INVALID_ARGUMENT;
   if (num_seqs < 0 || max_blocks < 0 || max_tokens < 0 || ring_size < 1)
     return KDA_ERR_INVALID_ARGUMENT;
+  if ((int64_t)num_seqs * max_blocks > INT32_MAX) return KDA_ERR_UNSUPPORTED;
   if (!cu_new || !free_range || !free_range_out || !free_pages) return KDA_ERR_INVALID_ARGUMENT;
   if (num_seqs > 0 && (!held_lens || !seq_lens || !new_lens || !kv_lens))
     return KDA_ERR_INVALID_ARGUMENT;

@@ -42,7 +42,7 @@ using namespace cache;
 
 constexpr int kTileGroups = 2;                   // groups of 16 keys in a tile
 constexpr int kTileKeys = kTileGroups * kGroup;  // 32
-constexpr int kMaxSeqs = 2048;                   // requests of one launch (their plan is in smem)
+constexpr int kMaxSeqs = 1024;                   // requests of one launch (their plan is in smem)
 constexpr float kSlack = 8.f;                    // log2 head room of p over the reference m
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -157,13 +157,22 @@ __device__ __forceinline__ void store_row(T* p, const float (&x)[D / 8]) {
   }
 }
 
+// Halves of a query or weight: two for fp32 outputs, one for bf16.
 template <typename T>
-constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;  // halves of a query or weight
+constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
 
 template <typename T, int D, int NT, int WARPS, int STAGES>
 struct Smem {
   static constexpr int kStage = kTileGroups * Layout<D>::kGroupBytes;
+#ifndef QT
+#define QT 2
+#define C1 4
+#define C2 3
+#define C3 3
+#endif
+  static constexpr bool kQueriesHere = NT * kTerms<T> > QT;  // else they stay in registers
   alignas(128) uint8_t ring[WARPS][STAGES][kStage];
+  uint2 q[kQueriesHere ? WARPS : 1][kQueriesHere ? NT * kTerms<T> * (D / 16) * 32 : 1];
   unsigned long long plan[kMaxSeqs + 1];
   uint64_t full[WARPS][STAGES];
   uint32_t valid[WARPS][STAGES];
@@ -180,6 +189,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   constexpr int QC = D / 4;       // channels of a query row per lane
   constexpr int KM = D / 16;      // products along the channels of K, and 16-channel tiles of V
   constexpr int VC = D / 8;       // channels of V per lane
+  constexpr bool QREG = !S::kQueriesHere;
   extern __shared__ uint8_t raw[];
   S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
 
   // ---- the plan: tiles before each request ----
   if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) tc::mbar_init(&sm.full[warp][s], 1);
+    for (int s = 0; s < STAGES; ++s) tc::mbar_init(&sm.full[warp][s], kTileGroups);
     tc::mbar_fence_init();
   }
   {
@@ -237,65 +247,59 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
     ld = cp;
     const int count = (int)min(x1 - x0, (unsigned long long)INT32_MAX);
     int issued = 0;
-    int pages = -1, pages_of = -1;  // lane l: page of group 32 pages_of + l of ld's request
-    int pages_b = -1;
-
+    // Lane i holds the place of group 32 n + i of ld's unit, for the n being loaded, and issues
+    // that group's copy itself.
+    const uint8_t* src = nullptr;
+    uint32_t present = 0;  // groups of the 32 that can be read
+    auto find_pages = [&]() {
+      const int gi = (ld.tile * kTileGroups & ~31) + lane;
+      const bool in = gi < (ld.q.kv + kGroup - 1) / kGroup;
+      const int page =
+          in ? __ldg(a.block_table + (int64_t)(seq0 + ld.b) * a.max_blocks + gi / GP) : 0;
+      const bool sound = page >= 0 && page < c.num_pages;
+      if (in && !sound) report_error(a.err, kErrDeviceCheck);
+      src = c.pages + (((int64_t)page * c.kv_heads + ld.h) * GP + gi % GP) * L::kGroupBytes;
+      present = __ballot_sync(0xffffffffu, in && sound);
+    };
     auto issue = [&](int stage) {
-      const int g0 = ld.tile * kTileGroups;
-      if (pages_b != ld.b || pages_of != (g0 >> 5)) {
-        pages_b = ld.b;
-        pages_of = g0 >> 5;
-        const int gi = pages_of * 32 + lane;
-        pages = gi * (int64_t)kGroup < ld.q.kv
-                    ? __ldg(a.block_table + (int64_t)(seq0 + ld.b) * a.max_blocks + gi / GP)
-                    : 0;
-        if (pages < 0 || pages >= c.num_pages) {
-          report_error(a.err, kErrDeviceCheck);
-          pages = -1;
-        }
-      }
-      const int p0 = __shfl_sync(0xffffffffu, pages, g0 & 31);
-      const int p1 = __shfl_sync(0xffffffffu, pages, (g0 + 1) & 31);
-      if (lane == 0) {
-        const bool v0 = p0 >= 0 && g0 * kGroup < ld.q.kv;
-        const bool v1 = p1 >= 0 && (g0 + 1) * kGroup < ld.q.kv;
+      const int first = ld.tile * kTileGroups & 31;
+      if ((lane ^ first) < kTileGroups) {
         uint64_t* bar = &sm.full[warp][stage];
-        uint8_t* dst = sm.ring[warp][stage];
-        sm.valid[warp][stage] = (v0 ? 1u : 0u) | (v1 ? 2u : 0u);
-        const int i0 = g0 % GP;
-        const uint8_t* s0 =
-            c.pages + (((int64_t)p0 * c.kv_heads + ld.h) * GP + i0) * L::kGroupBytes;
-        if (v0 && v1 && i0 + 1 < GP) {
-          tc::mbar_arrive_expect_tx(bar, 2 * L::kGroupBytes);
-          tc::bulk_load(dst, s0, 2 * L::kGroupBytes, bar);
-        } else if (v0 || v1) {
-          tc::mbar_arrive_expect_tx(bar, (v0 && v1 ? 2 : 1) * L::kGroupBytes);
-          if (v0) tc::bulk_load(dst, s0, L::kGroupBytes, bar);
-          if (v1)
-            tc::bulk_load(dst + L::kGroupBytes,
-                          c.pages + (((int64_t)p1 * c.kv_heads + ld.h) * GP + (g0 + 1) % GP) *
-                                        L::kGroupBytes,
-                          L::kGroupBytes, bar);
+        const int u = lane ^ first;
+        if (u == 0) sm.valid[warp][stage] = present >> first & ((1u << kTileGroups) - 1);
+        if (present >> lane & 1) {
+          tc::mbar_arrive_expect_tx(bar, L::kGroupBytes);
+          tc::bulk_load(sm.ring[warp][stage] + u * L::kGroupBytes, src, L::kGroupBytes, bar);
         } else {
           tc::mbar_arrive(bar);
         }
       }
-      ++issued;
-      if (issued < count) ld.next(c, a, seq0, nseq, ROWS);
+      if (++issued < count) {
+        const bool turn = ld.next(c, a, seq0, nseq, ROWS);
+        if (turn || (ld.tile * kTileGroups & 31) == 0) find_pages();
+      }
     };
-
+    find_pages();
     for (int s = 0; s < STAGES && s < count; ++s) issue(s);
 
-    uint32_t qf[NT][KM][TERMS][2];
+    uint2 qf[QREG ? NT : 1][QREG ? KM : 1][QREG ? TERMS : 1];
+    uint2* const qs = sm.q[QREG ? 0 : warp];
+    auto query = [&](int n, int i, int e) {
+      if constexpr (QREG)
+        return qf[n][i][e];
+      else
+        return qs[((n * KM + i) * TERMS + e) * 32 + lane];
+    };
     float o[KM][NT][4];
-    float m[NT][2], l[NT][2], sf[NT][2];
-    int see[NT][2];  // keys that the lane's rows see
-    int all_see = 0;  // keys that every row of the unit sees
+    float l[NT][2];                          // the lane's sums of the weights
+    float sf[NT][2], neg[NT][2], thr[NT][2]; // score factor, -m, raw score that moves m
+    int see[NT][2];                          // keys that the lane's rows see
+    int all_see = 0;                         // keys that every row of the unit sees
     int seg_tile = 0;
 
     auto start_unit = [&]() {
-      const int rows = (int)min((int64_t)cp.q.n * group - (int64_t)cp.r * ROWS, (int64_t)ROWS);
       const int64_t row0 = (int64_t)cp.r * ROWS;
+      const int rows = (int)min((int64_t)cp.q.n * group - row0, (int64_t)ROWS);
       all_see = cp.q.kv - cp.q.n + (int)(row0 / group) + 1;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -332,33 +336,46 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         for (int i = 0; i < QC; ++i) top = fmaxf(top, fabsf(x[i]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-e with top 2^-e in [1, 2); e held to the normal range, 0 where top is not finite
+        // 2^-e with top 2^-e in [1, 2); e held to the normal range, 0 where top is not finite.
+        // The sign of the score factor goes into the queries.
         int e = ((__float_as_int(top) >> 23) & 255) - 127;
         e = e == 128 ? 0 : max(-126, min(e, 126));
-        const float down = __int_as_float((127 - e) << 23);
+        const float down = copysignf(__int_as_float((127 - e) << 23), a.scale);
         const float up = __int_as_float((127 + e) << 23);
-        const float f = a.scale * kLog2e * exponent_scale(c.k_exp, cp.h, 1) * up;
+        // kept positive and finite, so that a masked score stays -infinity
+        const float f = fminf(fmaxf(fabsf(a.scale) * kLog2e * exponent_scale(c.k_exp, cp.h, 1) * up,
+                                    1.2e-38f),
+                              3.e38f);
         sf[n][0] = __shfl_sync(0xffffffffu, f, t * 8);
         sf[n][1] = __shfl_sync(0xffffffffu, f, t * 8 + 4);
 #pragma unroll
-        for (int i = 0; i < QC / 2; ++i) {
-          const float y0 = x[2 * i] * down, y1 = x[2 * i + 1] * down;
-          const uint32_t hi = tc::pack_f16(y0, y1);
-          qf[n][i / 2][0][i % 2] = hi;
+        for (int i = 0; i < KM; ++i) {
+          const float y[4] = {x[4 * i] * down, x[4 * i + 1] * down, x[4 * i + 2] * down,
+                              x[4 * i + 3] * down};
+          uint2 f2[TERMS];
+          f2[0] = make_uint2(tc::pack_f16(y[0], y[1]), tc::pack_f16(y[2], y[3]));
           if constexpr (TERMS == 2) {
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-            qf[n][i / 2][1][i % 2] = tc::pack_f16(y0 - b.x, y1 - b.y);
+            const float2 b0 = __half22float2(*reinterpret_cast<const __half2*>(&f2[0].x));
+            const float2 b1 = __half22float2(*reinterpret_cast<const __half2*>(&f2[0].y));
+            f2[1] = make_uint2(tc::pack_f16(y[0] - b0.x, y[1] - b0.y),
+                               tc::pack_f16(y[2] - b1.x, y[3] - b1.y));
+          }
+#pragma unroll
+          for (int e2 = 0; e2 < TERMS; ++e2) {
+            if constexpr (QREG)
+              qf[n][i][e2] = f2[e2];
+            else
+              qs[((n * KM + i) * TERMS + e2) * 32 + lane] = f2[e2];
           }
         }
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
-          m[n][e2] = -INFINITY;
-          l[n][e2] = 0.f;
-          const int64_t rr = row0 + n * 8 + 2 * t + e2;
-          see[n][e2] = n * 8 + 2 * t + e2 < rows
-                           ? cp.q.kv - cp.q.n + (int)(rr / group) + 1
-                           : 0;
+          neg[n][e2] = 0.f;
+          thr[n][e2] = -INFINITY;
+          const int r = n * 8 + 2 * t + e2;
+          see[n][e2] = r < rows ? cp.q.kv - cp.q.n + (int)((row0 + r) / group) + 1 : 0;
         }
+        l[n][0] = l[n][1] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < KM; ++i)
@@ -369,7 +386,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
       seg_tile = cp.tile;
     };
 
-    // Ends the part of the unit that this warp had; `last` tile of the unit or not.
+    // Ends the part of the unit that this warp had.
     auto end_part = [&](bool ends_unit) {
       const bool whole = ends_unit && seg_tile == 0;
       const int64_t row0 = (int64_t)cp.r * ROWS;
@@ -382,150 +399,220 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         for (int e = 0; e < 2; ++e) {
           float sum = l[n][e];
 #pragma unroll
-          for (int s = 4; s < 32; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+          for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          const float m = thr[n][e] == -INFINITY ? -INFINITY : -neg[n][e];
           const int row = n * 8 + 2 * t + e;
           float x[VC];
           if (row < rows) {
-            if (whole) {
-              const float inv = sum == 0.f ? 0.f : post / sum;
+            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : post / sum;
 #pragma unroll
-              for (int i = 0; i < KM; ++i) {
-                x[2 * i] = o[i][n][e] * inv;
-                x[2 * i + 1] = o[i][n][2 + e] * inv;
-              }
+            for (int i = 0; i < KM; ++i) {
+              x[2 * i] = o[i][n][e] * inv;
+              x[2 * i + 1] = o[i][n][2 + e] * inv;
+            }
+            if (whole) {
               const int64_t rr = row0 + row;
               const int64_t at =
                   (cp.q.bos + rr / group) * a.num_heads + cp.h * group + rr % group;
               store_row<T, D>(static_cast<T*>(a.out) + at * D + g * VC, x);
-              if (a.lse && g == 0)
-                a.lse[at] = sum == 0.f ? -INFINITY : (m[n][e] + log2f(sum)) * kLn2;
+              if (a.lse && g == 0) a.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
             } else {
-#pragma unroll
-              for (int i = 0; i < KM; ++i) {
-                x[2 * i] = o[i][n][e];
-                x[2 * i + 1] = o[i][n][2 + e];
-              }
               const int64_t at = (int64_t)slot * ROWS + row;
               store_row<float, D>(parts.o + at * D + g * VC, x);
-              if (g == 0) parts.ml[at] = make_float2(m[n][e], sum);
+              if (g == 0) parts.ml[at] = make_float2(m, sum);
             }
           }
         }
     };
 
-    start_unit();
-    bool alive = true;
-    for (int i = 0; i < count && alive; ++i) {
-      const int stage = i % STAGES;
-      if (!tc::mbar_wait(&sm.full[warp][stage], (i / STAGES) & 1, kWaitLimit)) {
-        if (lane == 0) report_error(a.err, kErrTimeout);
-        alive = false;
-        break;
-      }
-      const uint32_t valid = sm.valid[warp][stage];
-      const int key0 = cp.tile * kTileKeys;
-      float s[kTileGroups][NT][4];
-      // ---- scores ----
+    // The K side of one tile, in registers as it comes from shared memory.
+    struct Keys {
+      uint32_t a[kTileGroups][D / 32], b[kTileGroups][D / 32];  // codes of keys g and g + 8
+      uint32_t sc[kTileGroups][2][L::kPer];                     // their scales, twice in a word
+    };
+    float s[kTileGroups][NT][4];
+    uint32_t pf[kTileGroups][NT][TERMS][2];
+    auto load_keys = [&](const uint8_t* base, Keys& k) {
 #pragma unroll
       for (int u = 0; u < kTileGroups; ++u) {
+        const uint8_t* p = base + u * L::kGroupBytes;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p + g * 64 + t * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(p + (g + 8) * 64 + t * 16);
+          k.a[u][0] = x.x, k.a[u][1] = x.y, k.a[u][2] = x.z, k.a[u][3] = x.w;
+          k.b[u][0] = y.x, k.b[u][1] = y.y, k.b[u][2] = y.z, k.b[u][3] = y.w;
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(p + L::kKScales + g * 16 + t * 4);
+          const uint32_t wa = e4m3x2_to_f16x2(w), wb = e4m3x2_to_f16x2(w >> 16);
+          k.sc[u][0][0] = __byte_perm(wa, 0, 0x1010), k.sc[u][0][1] = __byte_perm(wa, 0, 0x3232);
+          k.sc[u][1][0] = __byte_perm(wb, 0, 0x1010), k.sc[u][1][1] = __byte_perm(wb, 0, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(p + g * 32 + t * 8);
+          const uint2 y = *reinterpret_cast<const uint2*>(p + (g + 8) * 32 + t * 8);
+          k.a[u][0] = x.x, k.a[u][1] = x.y;
+          k.b[u][0] = y.x, k.b[u][1] = y.y;
+          const uint32_t w = e4m3x2_to_f16x2(
+              *reinterpret_cast<const uint16_t*>(p + L::kKScales + g * 8 + t * 2));
+          k.sc[u][0][0] = __byte_perm(w, 0, 0x1010);
+          k.sc[u][1][0] = __byte_perm(w, 0, 0x3232);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[u][n][j] = 0.f;
-        if (!(valid >> u & 1)) continue;
-        const uint8_t* base = sm.ring[warp][stage] + u * L::kGroupBytes;
-        uint32_t ka[D / 32], kb[D / 32];  // codes of keys g and g + 8
-        uint32_t sc[2][L::kPer];          // their scales, twice in a word
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(base + g * 64 + t * 16);
-          const uint4 y = *reinterpret_cast<const uint4*>(base + (g + 8) * 64 + t * 16);
-          ka[0] = x.x, ka[1] = x.y, ka[2] = x.z, ka[3] = x.w;
-          kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
-          const uint32_t w =
-              *reinterpret_cast<const uint32_t*>(base + L::kKScales + g * 16 + t * 4);
-          const uint32_t wa = e4m3x2_to_f16x2(w), wb = e4m3x2_to_f16x2(w >> 16);
-          sc[0][0] = __byte_perm(wa, 0, 0x1010), sc[0][1] = __byte_perm(wa, 0, 0x3232);
-          sc[1][0] = __byte_perm(wb, 0, 0x1010), sc[1][1] = __byte_perm(wb, 0, 0x3232);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(base + g * 32 + t * 8);
-          const uint2 y = *reinterpret_cast<const uint2*>(base + (g + 8) * 32 + t * 8);
-          ka[0] = x.x, ka[1] = x.y;
-          kb[0] = y.x, kb[1] = y.y;
-          const uint32_t w = e4m3x2_to_f16x2(
-              *reinterpret_cast<const uint16_t*>(base + L::kKScales + g * 8 + t * 2));
-          sc[0][0] = __byte_perm(w, 0, 0x1010);
-          sc[1][0] = __byte_perm(w, 0, 0x3232);
-        }
+      }
+    };
+    // 8 channels a lane of every key: two products.
+    auto score_word = [&](const Keys& k, int w) {
+      uint32_t af[kTileGroups][2][4];
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          uint32_t xa[4], xb[4];
-          e2m1x8_to_f16(ka[w], xa);
-          e2m1x8_to_f16(kb[w], xb);
+      for (int u = 0; u < kTileGroups; ++u) {
+        uint32_t xa[4], xb[4];
+        e2m1x8_to_f16(k.a[u][w], xa);
+        e2m1x8_to_f16(k.b[u][w], xb);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            xa[j] = mul_f16x2(xa[j], sc[0][w / 2]);
-            xb[j] = mul_f16x2(xb[j], sc[1][w / 2]);
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t af[4] = {xa[2 * j], xb[2 * j], xa[2 * j + 1], xb[2 * j + 1]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < TERMS; ++e)
-                tc::mma_16816_f16(s[u][n], af, qf[n][2 * w + j][e][0], qf[n][2 * w + j][e][1]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          af[u][j >> 1][2 * (j & 1)] = mul_f16x2(xa[j], k.sc[u][0][w / 2]);
+          af[u][j >> 1][2 * (j & 1) + 1] = mul_f16x2(xb[j], k.sc[u][1][w / 2]);
         }
       }
-      // ---- softmax ----
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e) {
+            const uint2 q = query(n, 2 * w + j, e);
+#pragma unroll
+            for (int u = 0; u < kTileGroups; ++u) tc::mma_16816_f16(s[u][n], af[u][j], q.x, q.y);
+          }
+    };
+    struct Values {
+      uint32_t c0[2][D / 64], c1[2][D / 64];  // [token][word] of tokens 2t.., 2t + 8..
+    };
+    auto load_values = [&](const uint8_t* base, int u, Values& v) {
+      const uint8_t* vb = base + u * L::kGroupBytes + L::kVCodes;
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vb + g * 64 + t * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(vb + 4 * D + g * 64 + t * 16);
+        v.c0[0][0] = x.x, v.c0[0][1] = x.y, v.c0[1][0] = x.z, v.c0[1][1] = x.w;
+        v.c1[0][0] = y.x, v.c1[0][1] = y.y, v.c1[1][0] = y.z, v.c1[1][1] = y.w;
+      } else {
+        const uint8_t* p = vb + (g >> 1) * 64 + t * 16 + (g & 1) * 4;
+        v.c0[0][0] = *reinterpret_cast<const uint32_t*>(p);
+        v.c0[1][0] = *reinterpret_cast<const uint32_t*>(p + 8);
+        v.c1[0][0] = *reinterpret_cast<const uint32_t*>(p + 4 * D);
+        v.c1[1][0] = *reinterpret_cast<const uint32_t*>(p + 4 * D + 8);
+      }
+    };
+    // 8 channels a lane of one group's values: four products.
+    auto value_word = [&](const Values& v, uint32_t scales, int u, int wd) {
+      const uint32_t s0 = e4m3x2_to_f16x2(scales), s1 = e4m3x2_to_f16x2(scales >> 16);
+      // bytes of (even channel of the first token, of the second), then the odd channels
+      uint32_t e0[4], d0[4], e1[4], d1[4];
+      e2m1x8_to_f16((v.c0[0][wd] & 0x0f0f0f0fu) | ((v.c0[1][wd] << 4) & 0xf0f0f0f0u), e0);
+      e2m1x8_to_f16(((v.c0[0][wd] >> 4) & 0x0f0f0f0fu) | (v.c0[1][wd] & 0xf0f0f0f0u), d0);
+      e2m1x8_to_f16((v.c1[0][wd] & 0x0f0f0f0fu) | ((v.c1[1][wd] << 4) & 0xf0f0f0f0u), e1);
+      e2m1x8_to_f16(((v.c1[0][wd] >> 4) & 0x0f0f0f0fu) | (v.c1[1][wd] & 0xf0f0f0f0u), d1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t af[4] = {mul_f16x2(e0[j], s0), mul_f16x2(d0[j], s0), mul_f16x2(e1[j], s1),
+                                mul_f16x2(d1[j], s1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e)
+            tc::mma_16816_f16(o[wd * 4 + j][n], af, pf[u][n][e][0], pf[u][n][e][1]);
+      }
+    };
+
+    int stage = 0;
+    uint32_t parity = 0;
+    auto wait = [&](int st, uint32_t par) {
+      const bool ok = tc::mbar_wait(&sm.full[warp][st], par, kWaitLimit);
+      if (!ok && lane == 0) report_error(a.err, kErrTimeout);
+      return ok;
+    };
+    start_unit();
+    bool fed = wait(0, 0);
+    if (fed) {
+      Keys k;
+      load_keys(sm.ring[warp][0], k);
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) score_word(k, w);
+    }
+    for (int i = 0; i < count && fed; ++i) {
+      // s holds the raw scores of tile i
+      const uint8_t* const base = sm.ring[warp][stage];
+      const uint32_t valid = sm.valid[warp][stage];
+      const int key0 = cp.tile * kTileKeys;
+      // A tile that some row does not see in full, or that is not all there.
+      const bool edge = key0 + kTileKeys > all_see || valid != (1u << kTileGroups) - 1;
+      uint32_t vs[kTileGroups];  // scales of V: tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+      for (int u = 0; u < kTileGroups; ++u)
+        vs[u] = *reinterpret_cast<const uint32_t*>(base + u * L::kGroupBytes + L::kVScales +
+                                                   (D == 128 ? g : g >> 1) * 16 + t * 4);
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < kTileGroups; ++u) {
+          const bool here = valid >> u & 1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!here || key0 + u * kGroup + g + 8 * (j >> 1) >= see[n][j & 1])
+                s[u][n][j] = -INFINITY;
+          // what lies past the request's length may be anything: its scales become 0
+          const int left = here ? cp.q.kv - key0 - u * kGroup : 0;
+          if (2 * t >= left) vs[u] &= 0xffffff00u;
+          if (2 * t + 1 >= left) vs[u] &= 0xffff00ffu;
+          if (2 * t + 8 >= left) vs[u] &= 0xff00ffffu;
+          if (2 * t + 9 >= left) vs[u] &= 0x00ffffffu;
+        }
+      }
       bool move = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < kTileGroups; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[u][n][j] *= sf[n][j & 1];
-            if (key0 + kTileKeys > all_see || valid != 3u) {
-              const int key = key0 + u * kGroup + g + 8 * (j >> 1);
-              if (key >= see[n][j & 1] || !(valid >> u & 1)) s[u][n][j] = -INFINITY;
-            }
-            move |= s[u][n][j] > m[n][j & 1] + kSlack;
-          }
+          for (int j = 0; j < 4; ++j) move |= s[u][n][j] > thr[n][j & 1];
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = m[n][e];
+            float top = -INFINITY;
 #pragma unroll
             for (int u = 0; u < kTileGroups; ++u)
               top = fmaxf(top, fmaxf(s[u][n][e], s[u][n][2 + e]));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float keep = top == -INFINITY ? 1.f : ex2_approx(m[n][e] - top);
-            m[n][e] = top;
-            l[n][e] *= keep;
+            if (top > -INFINITY) {
+              const float before = thr[n][e] == -INFINITY ? -INFINITY : -neg[n][e];
+              const float m = fmaxf(before, top * sf[n][e]);
+              const float keep = ex2_approx(before - m);
+              neg[n][e] = -m;
+              thr[n][e] = (m + kSlack) / sf[n][e];
+              l[n][e] *= keep;
 #pragma unroll
-            for (int i2 = 0; i2 < KM; ++i2) {
-              o[i2][n][e] *= keep;
-              o[i2][n][2 + e] *= keep;
+              for (int i2 = 0; i2 < KM; ++i2) {
+                o[i2][n][e] *= keep;
+                o[i2][n][2 + e] *= keep;
+              }
             }
           }
       }
-      uint32_t pf[kTileGroups][NT][TERMS][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float ref[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0],
-                              m[n][1] == -INFINITY ? 0.f : m[n][1]};
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < kTileGroups; ++u) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[u][n][j] = ex2_approx(s[u][n][j] - ref[j & 1]);
-            l[n][j & 1] += s[u][n][j];
-          }
+          for (int j = 0; j < 4; ++j)
+            s[u][n][j] = ex2_approx(fmaf(s[u][n][j], sf[n][j & 1], neg[n][j & 1]));
+          l[n][0] += s[u][n][0] + s[u][n][2];
+          l[n][1] += s[u][n][1] + s[u][n][3];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t hi = tc::pack_f16(s[u][n][2 * j], s[u][n][2 * j + 1]);
@@ -537,68 +624,55 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
             }
           }
         }
+      int next = stage + 1;
+      uint32_t next_parity = parity;
+      if (next == STAGES) {
+        next = 0;
+        next_parity ^= 1;
       }
-      // ---- values ----
+      const bool more = i + 1 < count;
+      const bool ends_unit = cp.tile + 1 == cp.q.tiles;
+      if (more && !ends_unit) {
+        // values of tile i and scores of tile i + 1, two independent streams side by side
+        fed = wait(next, next_parity);
+        if (!fed) break;
+        Keys k;
+        load_keys(sm.ring[warp][next], k);
 #pragma unroll
-      for (int u = 0; u < kTileGroups; ++u) {
-        if (!(valid >> u & 1)) continue;
-        const uint8_t* base = sm.ring[warp][stage] + u * L::kGroupBytes;
-        const int blk = D == 128 ? g : g >> 1;
-        uint32_t w = *reinterpret_cast<const uint32_t*>(base + L::kVScales + blk * 16 + t * 4);
-        const int left = cp.q.kv - key0 - u * kGroup;
-        if (left < kGroup) {  // bytes past the request's length: scale 0
-          if (2 * t >= left) w &= 0xffffff00u;
-          if (2 * t + 1 >= left) w &= 0xffff00ffu;
-          if (2 * t + 8 >= left) w &= 0xff00ffffu;
-          if (2 * t + 9 >= left) w &= 0x00ffffffu;
-        }
-        const uint32_t s0 = e4m3x2_to_f16x2(w), s1 = e4m3x2_to_f16x2(w >> 16);
-        uint32_t c0[2][D / 64], c1[2][D / 64];  // [token][word] of tokens 2t.., 2t+8..
-        const uint8_t* vb = base + L::kVCodes;
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vb + g * 64 + t * 16);
-          const uint4 y = *reinterpret_cast<const uint4*>(vb + 4 * D + g * 64 + t * 16);
-          c0[0][0] = x.x, c0[0][1] = x.y, c0[1][0] = x.z, c0[1][1] = x.w;
-          c1[0][0] = y.x, c1[0][1] = y.y, c1[1][0] = y.z, c1[1][1] = y.w;
-        } else {
-          const uint8_t* p = vb + blk * 64 + t * 16 + (g & 1) * 4;
-          c0[0][0] = *reinterpret_cast<const uint32_t*>(p);
-          c0[1][0] = *reinterpret_cast<const uint32_t*>(p + 8);
-          c1[0][0] = *reinterpret_cast<const uint32_t*>(p + 4 * D);
-          c1[1][0] = *reinterpret_cast<const uint32_t*>(p + 4 * D + 8);
-        }
+        for (int u = 0; u < kTileGroups; ++u) {
+          Values v;
+          load_values(base, u, v);
 #pragma unroll
-        for (int wd = 0; wd < D / 64; ++wd) {
-          // bytes of (even channel of the first token, of the second), then the odd channels
-          uint32_t e0[4], d0[4], e1[4], d1[4];
-          e2m1x8_to_f16((c0[0][wd] & 0x0f0f0f0fu) | ((c0[1][wd] << 4) & 0xf0f0f0f0u), e0);
-          e2m1x8_to_f16(((c0[0][wd] >> 4) & 0x0f0f0f0fu) | (c0[1][wd] & 0xf0f0f0f0u), d0);
-          e2m1x8_to_f16((c1[0][wd] & 0x0f0f0f0fu) | ((c1[1][wd] << 4) & 0xf0f0f0f0u), e1);
-          e2m1x8_to_f16(((c1[0][wd] >> 4) & 0x0f0f0f0fu) | (c1[1][wd] & 0xf0f0f0f0u), d1);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t af[4] = {mul_f16x2(e0[j], s0), mul_f16x2(d0[j], s0),
-                                    mul_f16x2(e1[j], s1), mul_f16x2(d1[j], s1)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < TERMS; ++e)
-                tc::mma_16816_f16(o[wd * 4 + j][n], af, pf[u][n][e][0], pf[u][n][e][1]);
+          for (int wd = 0; wd < D / 64; ++wd) {
+            score_word(k, u * (D / 64) + wd);
+            value_word(v, vs[u], u, wd);
           }
+        }
+        ++cp.tile;
+      } else {
+#pragma unroll
+        for (int u = 0; u < kTileGroups; ++u) {
+          Values v;
+          load_values(base, u, v);
+#pragma unroll
+          for (int wd = 0; wd < D / 64; ++wd) value_word(v, vs[u], u, wd);
+        }
+        end_part(ends_unit);
+        if (more) {
+          cp.next(c, a, seq0, nseq, ROWS);
+          start_unit();
+          fed = wait(next, next_parity);
+          if (!fed) break;
+          Keys k;
+          load_keys(sm.ring[warp][next], k);
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) score_word(k, w);
         }
       }
       __syncwarp();  // every lane has read the stage
       if (issued < count) issue(stage);
-      const bool ends_unit = cp.tile + 1 == cp.q.tiles;
-      if (ends_unit || i + 1 == count) {
-        end_part(ends_unit);
-        if (i + 1 < count) {
-          cp.next(c, a, seq0, nseq, ROWS);
-          start_unit();
-        }
-      } else {
-        ++cp.tile;
-      }
+      stage = next;
+      parity = next_parity;
     }
   }
 
@@ -762,7 +836,7 @@ auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
   if (a.bf16) {
     using T = __nv_bfloat16;
     if (a.head_dim == 128) {
-      if (rows <= 8) return f(Split<T, 128, 1, 8, 2, 2>{});
+      if (rows <= 8) return f(Split<T, 128, 1, C1, C2, C3>{});
       if (rows <= 16) return f(Split<T, 128, 2, 8, 4, 1>{});
       return f(Split<T, 128, 4, 8, 4, 1>{});
     }

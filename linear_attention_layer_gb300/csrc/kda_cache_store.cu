@@ -3,12 +3,18 @@
 //
 // One thread takes one block of 16 channels: its scale is a maximum over the
 // thread's own registers, its codes are one 8-byte store, and nothing is shared
-// between threads.  Both calls are bound by HBM: they read and write each value
-// once.
+// between threads.  Both calls read and write each value once and are bound by
+// HBM as long as a value costs few enough instructions (about six; HBM's rate
+// leaves 11), which decides how the rounding below is done.
+//
+// Threads of K go blocks first: the 8 (4) blocks of a token's head are one run of
+// code bytes.  Threads of V go 8 neighbouring tokens first: the layout keeps the
+// blocks of 8 tokens together, so tokens of one prompt fill whole sectors.
 #include <algorithm>
 
 #include "kda_cache.cuh"
 #include "kda_launch.h"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -17,33 +23,65 @@ using namespace cache;
 
 constexpr int kThreads = 256;
 
-// 16 channels at p, as fp32.  VEC: p is 16-byte aligned.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_block(const T* p, float (&x)[16]) {
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = IO<T>::ld(p + i);
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
-      x[4 * i] = v.x;
-      x[4 * i + 1] = v.y;
-      x[4 * i + 2] = v.z;
-      x[4 * i + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    }
+// n / d for n < 2^31 by a product (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994): m = floor(2^(31 + s) / d) + 1, 2^s >= d.
+struct FastDiv {
+  uint32_t d, m, s;
+  explicit FastDiv(uint32_t x) : d(x), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)((1ull << (31 + s)) / d + 1);
   }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * m) >> (31 + s));
+  }
+};
+
+// Where the threads' blocks lie: kv heads of a token, tokens of a page.
+struct Grid {
+  FastDiv heads, page;
+  int tokens;
+  int64_t limit;
+  Grid(const View& c, int n)
+      : heads(c.kv_heads), page(c.page_size), tokens(n),
+        limit((int64_t)c.num_pages * c.page_size) {}
+};
+
+// One thread's block: a CTA takes 8 tokens, K in the first half of the grid's y.
+template <int D>
+struct Item {
+  int token, head, block;
+  __device__ __forceinline__ bool set(const Grid& gr, bool is_v, int i) {
+    constexpr int kBlocks = D / kGroup;
+    int t;
+    if (is_v) {  // tokens, blocks, heads
+      t = i & 7;
+      block = (i >> 3) & (kBlocks - 1);
+      head = i / (8 * kBlocks);
+    } else {  // blocks, heads, tokens
+      block = i & (kBlocks - 1);
+      const uint32_t r = (uint32_t)i / kBlocks;
+      t = gr.heads.div(r);
+      head = r - t * gr.heads.d;
+    }
+    token = blockIdx.x * 8 + t;
+    return token < gr.tokens;
+  }
+};
+
+// Which bytes of the cache a slot's block has.
+struct Place {
+  uint8_t* codes;
+  uint8_t* scale;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const View& c, const Grid& gr, bool is_v, int64_t slot,
+                                          int head, int b) {
+  const int page = gr.page.div((uint32_t)slot);
+  const int tok = (int)slot - page * c.page_size;
+  uint8_t* g = group_of<D>(c, page, tok, head);
+  const int i = tok % kGroup;
+  return {g + (is_v ? Layout<D>::v_codes(i, b) : Layout<D>::k_codes(i, b)),
+          g + (is_v ? Layout<D>::v_scale(i, b) : Layout<D>::k_scale(i, b))};
 }
 
 struct Source {
@@ -52,9 +90,9 @@ struct Source {
   int64_t head_stride;
 };
 
-// The block's scale byte and its 16 codes.
+// Scale byte and codes of 16 fp32 values; `pre` is the head's power of two.
 __device__ __forceinline__ uint32_t quantise(float (&x)[16], float pre, uint2& codes,
-                                             bool& odd_values) {
+                                             bool& not_finite) {
   float top = 0.f, probe = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -63,7 +101,7 @@ __device__ __forceinline__ uint32_t quantise(float (&x)[16], float pre, uint2& c
     top = fmaxf(top, fabsf(x[i]));
   }
   if (probe != 0.f) {
-    odd_values = true;
+    not_finite = true;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (isnan(x[i])) x[i] = 0.f;
@@ -83,45 +121,92 @@ __device__ __forceinline__ uint32_t quantise(float (&x)[16], float pre, uint2& c
   return sb;
 }
 
+// The same of 16 bf16 values, two in a word.  x has 8 significant bits and s 4, a
+// border between two codes times s at most 7, so x / s either is a border or lies
+// 2^-9 of it away at least: the product with the rounded 1 / s, 2^-23 off at most,
+// is brought back onto the borders by rounding it to 16 fraction bits.  That costs
+// two integer instructions a value where the exact division above costs twenty.
+__device__ __forceinline__ uint32_t quantise(uint32_t (&x)[8], float pre, uint2& codes,
+                                             bool& not_finite) {
+  uint32_t top2 = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, x[i] & 0x7fff7fffu);
+  const uint32_t top_bits = max(top2 & 0xffffu, top2 >> 16);
+  if (top_bits >= 0x7f80u) {
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[2 * i] = tc::bf16_lo(x[i]);
+      y[2 * i + 1] = tc::bf16_hi(x[i]);
+    }
+    return quantise(y, pre, codes, not_finite);
+  }
+  const float top = fminf(__uint_as_float(top_bits << 16) * pre, 3.e38f);
+  const uint32_t sb = f32_to_e4m3(div_to_odd(top, 6.f));
+  const float r = sb ? pre / e4m3_to_f32(sb) : 0.f;  // a power of two times 8 / 8 .. 8 / 15
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = tc::bf16_lo(x[i]) * r, b = tc::bf16_hi(x[i]) * r;
+    w[i >> 2] |= f32x2_to_e2m1(__uint_as_float((__float_as_uint(a) + 0x40u) & ~0x7fu),
+                               __uint_as_float((__float_as_uint(b) + 0x40u) & ~0x7fu))
+                 << (8 * (i & 3));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return sb;
+}
+
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    append_kernel(View c, Source k, Source v, const int64_t* __restrict__ slots, int tokens,
+    append_kernel(View c, Grid gr, Source k, Source v, const int64_t* __restrict__ slots,
                   int* err) {
-  constexpr int kBlocks = D / kGroup;
-  const int per_token = c.kv_heads * kBlocks;
-  const int64_t n = 2ll * tokens * per_token;
-  const int64_t limit = (int64_t)c.num_pages * c.page_size;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n;
-       e += (int64_t)gridDim.x * kThreads) {
-    // neighbouring threads: blocks, heads, k then v, tokens
-    const int b = (int)(e % kBlocks);
-    const int64_t r = e / kBlocks;
-    const int h = (int)(r % c.kv_heads);
-    const int64_t r2 = r / c.kv_heads;
-    const bool is_v = r2 & 1;
-    const int64_t t = r2 >> 1;
-    const int64_t slot = __ldg(slots + t);
-    if (slot < 0 || slot >= limit) {
+  const bool is_v = blockIdx.y;
+  const Source src = is_v ? v : k;
+  const int items = 8 * c.kv_heads * (D / kGroup);
+  for (int j = threadIdx.x; j < items; j += kThreads) {
+    Item<D> it;
+    if (!it.set(gr, is_v, j)) continue;
+    const int64_t slot = __ldg(slots + it.token);
+    const T* p = static_cast<const T*>(src.p) + it.token * src.token_stride +
+                 it.head * src.head_stride + it.block * kGroup;
+    uint2 codes;
+    uint32_t sb;
+    bool not_finite = false;
+    const float pre = exponent_scale(is_v ? c.v_exp : c.k_exp, it.head, -1);
+    if (slot < 0 || slot >= gr.limit) {
       if (slot != -1) report_error(err, kErrDeviceCheck);
       continue;
     }
-    const Source& src = is_v ? v : k;
-    float x[16];
-    load_block<T, VEC>(static_cast<const T*>(src.p) + t * src.token_stride + h * src.head_stride +
-                           b * kGroup,
-                       x);
-    uint2 codes;
-    bool odd_values = false;
-    const uint32_t sb =
-        quantise(x, exponent_scale(is_v ? c.v_exp : c.k_exp, h, -1), codes, odd_values);
-    if (odd_values) report_error(err, kErrDeviceCheck);
-    const int64_t page = slot / c.page_size;
-    const int tok = (int)(slot - page * c.page_size);
-    uint8_t* g = group_of<D>(c, page, tok, h);
-    const int i = tok % kGroup;
-    *reinterpret_cast<uint2*>(
-        g + (is_v ? Layout<D>::v_codes(i, b) : Layout<D>::k_codes(i, b))) = codes;
-    g[is_v ? Layout<D>::v_scale(i, b) : Layout<D>::k_scale(i, b)] = (uint8_t)sb;
+    if constexpr (sizeof(T) == 2 && VEC) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+      const uint4 b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+      uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      sb = quantise(x, pre, codes, not_finite);
+    } else if constexpr (sizeof(T) == 2) {
+      uint32_t x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = __float_as_uint(IO<T>::ld(p + 2 * i)) >> 16 |
+               __float_as_uint(IO<T>::ld(p + 2 * i + 1));
+      sb = quantise(x, pre, codes, not_finite);
+    } else {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (VEC) {
+          const float4 f = __ldcs(reinterpret_cast<const float4*>(p) + i);
+          x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+        } else {
+#pragma unroll
+          for (int l = 0; l < 4; ++l) x[4 * i + l] = IO<T>::ld(p + 4 * i + l);
+        }
+      }
+      sb = quantise(x, pre, codes, not_finite);
+    }
+    if (not_finite) report_error(err, kErrDeviceCheck);
+    const Place pl = place_of<D>(c, gr, is_v, slot, it.head, it.block);
+    *reinterpret_cast<uint2*>(pl.codes) = codes;
+    *pl.scale = (uint8_t)sb;
   }
 }
 
@@ -146,82 +231,61 @@ __device__ __forceinline__ void store_block(T* p, const float (&x)[16]) {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-    read_kernel(View c, const int64_t* __restrict__ slots, int tokens, T* __restrict__ k,
+    read_kernel(View c, Grid gr, const int64_t* __restrict__ slots, T* __restrict__ k,
                 T* __restrict__ v, int* err) {
-  constexpr int kBlocks = D / kGroup;
-  const int64_t n = 2ll * tokens * c.kv_heads * kBlocks;
-  const int64_t limit = (int64_t)c.num_pages * c.page_size;
-  for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < n;
-       e += (int64_t)gridDim.x * kThreads) {
-    const int b = (int)(e % kBlocks);
-    const int64_t r = e / kBlocks;
-    const int h = (int)(r % c.kv_heads);
-    const int64_t r2 = r / c.kv_heads;
-    const bool is_v = r2 & 1;
-    const int64_t t = r2 >> 1;
-    const int64_t slot = __ldg(slots + t);
+  const bool is_v = blockIdx.y;
+  const int items = 8 * c.kv_heads * (D / kGroup);
+  for (int j = threadIdx.x; j < items; j += kThreads) {
+    Item<D> it;
+    if (!it.set(gr, false, j)) continue;  // blocks first for both: whole rows are written
+    const int64_t slot = __ldg(slots + it.token);
     float x[16];
-    if (slot < 0 || slot >= limit) {
+    if (slot < 0 || slot >= gr.limit) {
       if (slot != -1) report_error(err, kErrDeviceCheck);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = 0.f;
     } else {
-      const int64_t page = slot / c.page_size;
-      const int tok = (int)(slot - page * c.page_size);
-      const uint8_t* g = group_of<D>(c, page, tok, h);
-      const int i = tok % kGroup;
-      const uint2 codes = *reinterpret_cast<const uint2*>(
-          g + (is_v ? Layout<D>::v_codes(i, b) : Layout<D>::k_codes(i, b)));
-      const float s = e4m3_to_f32(
-                          g[is_v ? Layout<D>::v_scale(i, b) : Layout<D>::k_scale(i, b)]) *
-                      exponent_scale(is_v ? c.v_exp : c.k_exp, h, 1);
+      const Place pl = place_of<D>(c, gr, is_v, slot, it.head, it.block);
+      const uint2 codes = *reinterpret_cast<const uint2*>(pl.codes);
+      const float s =
+          e4m3_to_f32(*pl.scale) * exponent_scale(is_v ? c.v_exp : c.k_exp, it.head, 1);
       const uint32_t w[2] = {codes.x, codes.y};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int l = 0; l < 2; ++l) {
         uint32_t r4[4];
-        e2m1x8_to_f16(w[j], r4);
+        e2m1x8_to_f16(w[l], r4);
 #pragma unroll
-        for (int l = 0; l < 4; ++l) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r4[l]));
-          x[8 * j + 2 * l] = f.x * s;
-          x[8 * j + 2 * l + 1] = f.y * s;
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r4[i]));
+          x[8 * l + 2 * i] = f.x * s;
+          x[8 * l + 2 * i + 1] = f.y * s;
         }
       }
     }
-    store_block((is_v ? v : k) + (t * c.kv_heads + h) * D + b * kGroup, x);
+    store_block((is_v ? v : k) + ((int64_t)it.token * c.kv_heads + it.head) * D + it.block * kGroup,
+                x);
   }
-}
-
-// Enough CTAs for every block once, at most 16 per SM (a grid stride takes the rest).
-int grid_for(int64_t n) {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return (int)std::min<int64_t>((n + kThreads - 1) / kThreads, 16ll * sms);
 }
 
 template <typename T, int D>
 cudaError_t append(const CacheArgs& a, cudaStream_t st) {
-  const int64_t n = 2ll * a.tokens * a.view.kv_heads * (D / kGroup);
   const Source k{a.k, a.strides[0], a.strides[1]}, v{a.v, a.strides[2], a.strides[3]};
   const int el = 16 / sizeof(T);
   bool vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0;
   for (int64_t s : a.strides) vec = vec && s % el == 0;
-  if (vec)
-    append_kernel<T, D, true><<<grid_for(n), kThreads, 0, st>>>(a.view, k, v, a.slots, a.tokens,
-                                                                a.err);
-  else
-    append_kernel<T, D, false><<<grid_for(n), kThreads, 0, st>>>(a.view, k, v, a.slots, a.tokens,
-                                                                 a.err);
+  const Grid gr(a.view, a.tokens);
+  const dim3 grid((unsigned)((a.tokens + 7ll) / 8), 2);
+  auto* kernel = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
+  kernel<<<grid, kThreads, 0, st>>>(a.view, gr, k, v, a.slots, a.err);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t read(const CacheArgs& a, cudaStream_t st) {
-  const int64_t n = 2ll * a.tokens * a.view.kv_heads * (D / kGroup);
-  read_kernel<T, D><<<grid_for(n), kThreads, 0, st>>>(a.view, a.slots, a.tokens,
-                                                      static_cast<T*>(a.k_out),
-                                                      static_cast<T*>(a.v_out), a.err);
+  const dim3 grid((unsigned)((a.tokens + 7ll) / 8), 2);
+  read_kernel<T, D><<<grid, kThreads, 0, st>>>(a.view, Grid(a.view, a.tokens), a.slots,
+                                               static_cast<T*>(a.k_out), static_cast<T*>(a.v_out),
+                                               a.err);
   return cudaGetLastError();
 }
 

@@ -71,8 +71,29 @@ __device__ __forceinline__ int64_t slot_of(const TableArgs& a, int i) {
          pos % a.page_size;
 }
 
+// Requests of one pass of the CTA, for the page moves that follow their sums.
+struct Pass {
+  int32_t taken_at[kThreads + 1];  // pages taken before each request of the pass
+  int32_t freed_at[kThreads + 1];
+  int32_t from[kThreads];          // first column that changes
+};
+
+// The request of the pass that page i belongs to.
+__device__ __forceinline__ int owner(const int32_t* at, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write_slots) {
   __shared__ int64_t warp_sums[kWarps];
+  __shared__ Pass ps;
   const int P = a.page_size;
   int64_t head = a.free_range[0], tail = a.free_range[1];
   const bool ring_ok = head >= 0 && tail >= head && tail - head <= a.ring_size;
@@ -95,33 +116,50 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write
     int64_t target = sound ? keep + add : 0;
     bool refused = !sound || pages_of(target, P) > a.max_blocks || target > INT32_MAX;
     int grow = refused ? 0 : max(0, pages_of(target, P) - have);
-    int64_t sum;
-    const int64_t asked_incl = asked + block_scan(grow, warp_sums, sum);
-    asked += sum;
-    if (grow > 0 && asked_incl > avail) {
-      refused = true;
-      grow = 0;
+    int64_t sum, pass_taken, pass_freed;
+    int64_t taken_at = block_scan(grow, warp_sums, sum) - grow;
+    pass_taken = sum;
+    if (asked + sum > avail) {  // the ring runs dry in this pass or before
+      if (grow > 0 && asked + taken_at + grow > avail) {
+        refused = true;
+        grow = 0;
+      }
+      taken_at = block_scan(grow, warp_sums, pass_taken) - grow;
     }
+    asked += sum;
     if (refused) target = keep;
     if (in && refused && (add > 0 || !sound)) report_error(a.err, kErrDeviceCheck);
-    const int shrink = max(0, have - pages_of(target, P));
-    const int64_t freed_at = freed + block_scan(shrink, warp_sums, sum) - shrink;
-    freed += sum;
-    const int64_t taken_at = taken + block_scan(grow, warp_sums, sum) - grow;
-    taken += sum;
+    const int want = pages_of(target, P);
+    const int shrink = max(0, have - want);
+    const int64_t freed_at = block_scan(shrink, warp_sums, pass_freed) - shrink;
     const int64_t first = tokens + block_scan(add, warp_sums, sum) - add;
     tokens += sum;
+    ps.taken_at[threadIdx.x] = (int32_t)taken_at;
+    ps.freed_at[threadIdx.x] = (int32_t)freed_at;
+    ps.from[threadIdx.x] = grow > 0 ? have : want;
     if (in) {
-      int32_t* row = a.block_table + (int64_t)b * a.max_blocks;
-      for (int j = 0; j < shrink; ++j)
-        a.free_pages[(tail + freed_at + j) % a.ring_size] = row[have - shrink + j];
-      for (int j = 0; j < grow; ++j)
-        row[have + j] = a.free_pages[(head + taken_at + j) % a.ring_size];
       a.kv_lens[b] = (int32_t)target;
       a.cu_new[b] = (int32_t)min(first, (int64_t)INT32_MAX);
-      if (add > 0 && first < a.max_tokens)
-        a.slots[first] = refused ? -1 : (int64_t)row[keep / P] * P + keep % P;
     }
+    __syncthreads();
+    // pages change hands, a thread each: what a request gives back may be thousands
+    for (int i = threadIdx.x; i < pass_freed; i += kThreads) {
+      const int o = owner(ps.freed_at, kThreads, i);
+      a.free_pages[(tail + freed + i) % a.ring_size] =
+          a.block_table[(int64_t)(base + o) * a.max_blocks + ps.from[o] + i - ps.freed_at[o]];
+    }
+    for (int i = threadIdx.x; i < pass_taken; i += kThreads) {
+      const int o = owner(ps.taken_at, kThreads, i);
+      a.block_table[(int64_t)(base + o) * a.max_blocks + ps.from[o] + i - ps.taken_at[o]] =
+          a.free_pages[(head + taken + i) % a.ring_size];
+    }
+    taken += pass_taken;
+    freed += pass_freed;
+    __syncthreads();
+    if (in && add > 0 && first < a.max_tokens)
+      a.slots[first] =
+          refused ? -1
+                  : (int64_t)a.block_table[(int64_t)b * a.max_blocks + keep / P] * P + keep % P;
   }
   if (threadIdx.x == 0) {
     a.cu_new[a.num_seqs] = (int32_t)min(tokens, (int64_t)INT32_MAX);

@@ -52,7 +52,8 @@ def _cache(**over):
 
 BAD_CACHES = [(dict(num_pages=-1), INVALID), (dict(page_size=0), INVALID),
               (dict(page_size=24), INVALID), (dict(page_size=8192), INVALID),
-              (dict(num_kv_heads=0), INVALID), (dict(head_dim=96), UNSUPPORTED),
+              (dict(num_kv_heads=0), INVALID), (dict(num_kv_heads=4097), UNSUPPORTED),
+              (dict(num_pages=1 << 26), UNSUPPORTED), (dict(head_dim=96), UNSUPPORTED),
               (dict(head_dim=0), UNSUPPORTED), (dict(pages=None), INVALID),
               (dict(pages=0x10008), INVALID), (dict(k_exponent=0x10002), INVALID)]
 
@@ -113,6 +114,10 @@ def _tables(lib, **over):
     dict(kv=0x8000)])
 def test_tables_refuses(lib, over):
     assert _tables(lib, **over) == INVALID
+
+
+def test_tables_too_large(lib):
+    assert _tables(lib, seqs=1 << 16, blocks=1 << 15) == UNSUPPORTED
 
 
 def _desc(**over):
