@@ -31,9 +31,7 @@
 
 #include <algorithm>
 
-#include "kda_cache.cuh"
-#include "kda_launch.h"
-#include "tc_ptx.cuh"
+#include "kda_cache_attention.cuh"
 
 namespace kda {
 namespace {
@@ -43,10 +41,6 @@ using namespace cache;
 constexpr int kTileGroups = 2;                   // groups of 16 keys in a tile
 constexpr int kTileKeys = kTileGroups * kGroup;  // 32
 constexpr int kMaxSeqs = 1024;                   // requests of one launch (their plan is in smem)
-constexpr float kSlack = 8.f;                    // log2 head room of p over the reference m
-constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // What a launch leaves in the workspace.
 struct Parts {
@@ -63,46 +57,9 @@ struct Shape {
   __host__ __device__ int slots() const { return warp_slots() + 2 * ctas; }
 };
 
-// A request of the launch, as the split sees it.
-struct Request {
-  int kv, n, bos;
-  int tiles;   // of one unit
-  int64_t rt;  // row tiles
-};
-
-__device__ __forceinline__ bool load_request(const View& c, const AttentionArgs& a, int b,
-                                             int rows_per_tile, bool report, Request& r) {
-  const int group = a.num_heads / c.kv_heads;
-  int eos;
-  // a decreasing offset takes both of its neighbours out: their tokens may overlap others'
-  const bool ok = seq_range(a.cu_new, b, a.total_tokens, report ? a.err : nullptr, r.bos, eos) &&
-                  (b == 0 || __ldg(a.cu_new + b - 1) <= r.bos);
-  r.kv = __ldg(a.kv_lens + b);
-  if (!ok || r.kv < 0 || r.kv > (int64_t)a.max_blocks * c.page_size) {
-    if (report) report_error(a.err, kErrDeviceCheck);
-    r.n = 0;
-    r.rt = 0;
-    r.tiles = 1;
-    return false;
-  }
-  r.n = eos - r.bos;
-  r.rt = ((int64_t)r.n * group + rows_per_tile - 1) / rows_per_tile;
-  r.tiles = max(1, (r.kv + kTileKeys - 1) / kTileKeys);  // a unit without keys still writes zeros
-  return r.rt > 0;
-}
-
-// The last index i with plan[i] <= x.
-template <typename P>
-__device__ __forceinline__ int find_request(const P* plan, int n, unsigned long long x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (plan[mid] <= x)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
+// Tiles of one unit: one at least, since a unit without keys still writes its zeros.
+__device__ __forceinline__ int tiles_of(const Request& r) {
+  return max(1, (r.kv + kTileKeys - 1) / kTileKeys);
 }
 
 // A place in the sequence of all tiles.
@@ -111,29 +68,38 @@ struct Cursor {
   int h;  // kv head
   int r;  // row tile
   int tile;
+  int tiles;   // of the unit
+  int64_t rt;  // row tiles of the request
   Request q;
 
+  __device__ __forceinline__ bool load(const View& c, const AttentionArgs& a, int seq0,
+                                       const RowRange& range, int rows_per_tile) {
+    const bool live = load_request(c, a, seq0 + b, range, false, q);
+    tiles = tiles_of(q);
+    rt = (q.rows + rows_per_tile - 1) / rows_per_tile;
+    return live;
+  }
   __device__ __forceinline__ void seek(const View& c, const AttentionArgs& a, int seq0, int nseq,
-                                       int rows_per_tile, const unsigned long long* plan,
-                                       unsigned long long x) {
-    b = find_request(plan, nseq, x);
-    load_request(c, a, seq0 + b, rows_per_tile, false, q);
+                                       const RowRange& range, int rows_per_tile,
+                                       const unsigned long long* plan, unsigned long long x) {
+    b = find_last(plan, nseq, x);
+    load(c, a, seq0, range, rows_per_tile);
     const unsigned long long off = x - plan[b];
-    const unsigned long long u = off / q.tiles;
-    tile = (int)(off - u * q.tiles);
-    h = (int)(u / q.rt);
-    r = (int)(u - (unsigned long long)h * q.rt);
+    const unsigned long long u = off / tiles;
+    tile = (int)(off - u * tiles);
+    h = (int)(u / rt);
+    r = (int)(u - (unsigned long long)h * rt);
   }
   // The next tile; returns true when it starts a new unit.  Not past the last one.
   __device__ __forceinline__ bool next(const View& c, const AttentionArgs& a, int seq0, int nseq,
-                                       int rows_per_tile) {
-    if (++tile < q.tiles) return false;
+                                       const RowRange& range, int rows_per_tile) {
+    if (++tile < tiles) return false;
     tile = 0;
-    if (++r < q.rt) return true;
+    if (++r < rt) return true;
     r = 0;
     if (++h < c.kv_heads) return true;
     h = 0;
-    while (++b < nseq && !load_request(c, a, seq0 + b, rows_per_tile, false, q)) {
+    while (++b < nseq && !load(c, a, seq0, range, rows_per_tile)) {
     }
     return true;
   }
@@ -181,7 +147,8 @@ struct Smem {
 
 template <typename T, int D, int NT, int WARPS, int STAGES, int CTAS>
 __global__ void __launch_bounds__(WARPS * 32, CTAS)
-    split_kernel(View c, AttentionArgs a, int seq0, int nseq, Parts parts, int q_vec) {
+    split_kernel(View c, AttentionArgs a, int seq0, int nseq, RowRange range, Parts parts,
+                 int q_vec) {
   using L = Layout<D>;
   using S = Smem<T, D, NT, WARPS, STAGES>;
   constexpr int ROWS = 8 * NT;
@@ -211,9 +178,10 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
       const int b = b0 + i;
       if (b >= nseq) break;
       Request r;
-      const bool live = load_request(c, a, seq0 + b, ROWS, blockIdx.x == 0, r);
+      const bool live = load_request(c, a, seq0 + b, range, blockIdx.x == 0, r);
       sm.plan[b] = mine;
-      if (live) mine += (unsigned long long)r.rt * r.tiles * c.kv_heads;
+      if (live)
+        mine += (unsigned long long)((r.rows + ROWS - 1) / ROWS) * tiles_of(r) * c.kv_heads;
     }
     unsigned long long incl = mine;
 #pragma unroll
@@ -243,7 +211,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
 
   if (x0 < x1) {
     Cursor ld, cp;
-    cp.seek(c, a, seq0, nseq, ROWS, sm.plan, x0);
+    cp.seek(c, a, seq0, nseq, range, ROWS, sm.plan, x0);
     ld = cp;
     const int count = (int)min(x1 - x0, (unsigned long long)INT32_MAX);
     int issued = 0;
@@ -275,14 +243,14 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         }
       }
       if (++issued < count) {
-        const bool turn = ld.next(c, a, seq0, nseq, ROWS);
+        const bool turn = ld.next(c, a, seq0, nseq, range, ROWS);
         if (turn || (ld.tile * kTileGroups & 31) == 0) find_pages();
       }
     };
     find_pages();
     for (int s = 0; s < STAGES && s < count; ++s) issue(s);
 
-    uint2 qf[QREG ? NT : 1][QREG ? KM : 1][QREG ? TERMS : 1];
+    uint2 qf[QREG ? NT : 1][QREG ? KM : 1][QREG ? TERMS : 1] = {};
     uint2* const qs = sm.q[QREG ? 0 : warp];
     auto query = [&](int n, int i, int e) {
       if constexpr (QREG)
@@ -336,16 +304,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         for (int i = 0; i < QC; ++i) top = fmaxf(top, fabsf(x[i]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-e with top 2^-e in [1, 2); e held to the normal range, 0 where top is not finite.
-        // The sign of the score factor goes into the queries.
-        int e = ((__float_as_int(top) >> 23) & 255) - 127;
-        e = e == 128 ? 0 : max(-126, min(e, 126));
-        const float down = copysignf(__int_as_float((127 - e) << 23), a.scale);
-        const float up = __int_as_float((127 + e) << 23);
-        // kept positive and finite, so that a masked score stays -infinity
-        const float f = fminf(fmaxf(fabsf(a.scale) * kLog2e * exponent_scale(c.k_exp, cp.h, 1) * up,
-                                    1.2e-38f),
-                              3.e38f);
+        const RowScale rs = row_scale(top, a.scale, exponent_scale(c.k_exp, cp.h, 1));
+        const float down = rs.down, f = rs.f;
         sf[n][0] = __shfl_sync(0xffffffffu, f, t * 8);
         sf[n][1] = __shfl_sync(0xffffffffu, f, t * 8 + 4);
 #pragma unroll
@@ -528,7 +488,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
     int stage = 0;
     uint32_t parity = 0;
     auto wait = [&](int st, uint32_t par) {
-      const bool ok = tc::mbar_wait(&sm.full[warp][st], par, kWaitLimit);
+      const bool ok = wait_phase(&sm.full[warp][st], par, nullptr);
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
       return ok;
     };
@@ -631,7 +591,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         next_parity ^= 1;
       }
       const bool more = i + 1 < count;
-      const bool ends_unit = cp.tile + 1 == cp.q.tiles;
+      const bool ends_unit = cp.tile + 1 == cp.tiles;
       if (more && !ends_unit) {
         // values of tile i and scores of tile i + 1, two independent streams side by side
         fed = wait(next, next_parity);
@@ -659,7 +619,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         }
         end_part(ends_unit);
         if (more) {
-          cp.next(c, a, seq0, nseq, ROWS);
+          cp.next(c, a, seq0, nseq, range, ROWS);
           start_unit();
           fed = wait(next, next_parity);
           if (!fed) break;
@@ -686,9 +646,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
     if (w0 >= w1) break;
     Cursor cu;
     unsigned long long u0, u1;
-    cu.seek(c, a, seq0, nseq, ROWS, sm.plan, job == 0 ? w0 : w1 - 1);
+    cu.seek(c, a, seq0, nseq, range, ROWS, sm.plan, job == 0 ? w0 : w1 - 1);
     u0 = (job == 0 ? w0 : w1 - 1) - cu.tile;
-    u1 = u0 + cu.q.tiles;
+    u1 = u0 + cu.tiles;
     if (job == 0 ? u0 == w0 : (u0 < w0 || u1 <= w1)) continue;  // no such unit
     const bool starts = u0 >= c0, ends = u1 <= c1;
     const unsigned long long p0 = max(u0, c0), p1 = min(u1, c1);
@@ -735,7 +695,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
 // Joins the parts of units that several CTAs had: one warp per row.
 template <typename T, int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(128)
-    join_kernel(View c, AttentionArgs a, int seq0, int nseq, Parts parts, Shape shape) {
+    join_kernel(View c, AttentionArgs a, int seq0, int nseq, RowRange range, Parts parts,
+                Shape shape) {
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int group = a.num_heads / c.kv_heads;
@@ -743,15 +704,17 @@ __global__ void __launch_bounds__(128)
   const int hq = (int)(w - tok * a.num_heads);
   const int32_t* cu = a.cu_new + seq0;
   if (tok >= a.total_tokens || tok < cu[0] || tok >= cu[nseq]) return;
-  const int b = find_request(cu, nseq, (unsigned long long)tok);
+  const int b = find_last(cu, nseq, (unsigned long long)tok);
   Request q;
-  if (!load_request(c, a, seq0 + b, ROWS, false, q) || tok < q.bos || tok >= q.bos + q.n) return;
+  if (!load_request(c, a, seq0 + b, range, false, q) || tok < q.bos || tok >= q.bos + q.n) return;
+  const int tiles = tiles_of(q);
+  const int64_t rt = (q.rows + ROWS - 1) / ROWS;
   const unsigned long long per = parts.plan[nseq + 1] * WARPS;
   const int h = hq / group;
   const int64_t rr = (tok - q.bos) * group + hq % group;
   const unsigned long long u0 =
-      parts.plan[b] + (unsigned long long)(h * q.rt + rr / ROWS) * q.tiles;
-  const int first = (int)(u0 / per), last = (int)((u0 + q.tiles - 1) / per);
+      parts.plan[b] + (unsigned long long)(h * rt + rr / ROWS) * tiles;
+  const int first = (int)(u0 / per), last = (int)((u0 + tiles - 1) / per);
   if (first == last) return;
   const int row = (int)(rr % ROWS);
   auto at_of = [&](int cta) {
@@ -796,7 +759,8 @@ struct Split {
     const size_t slots = shape().slots();
     return kPlanBytes + slots * ROWS * (D * 4 + 8);
   }
-  static cudaError_t launch(const View& c, const AttentionArgs& a, cudaStream_t st) {
+  static cudaError_t launch(const View& c, const AttentionArgs& a, const RowRange& range,
+                            cudaStream_t st) {
     static PerDeviceInit init;
     using S = Smem<T, D, NT, WARPS, STAGES>;
     auto* kernel = split_kernel<T, D, NT, WARPS, STAGES, CTAS>;
@@ -817,11 +781,11 @@ struct Split {
     const int64_t rows = (int64_t)a.total_tokens * a.num_heads;
     for (int seq0 = 0; seq0 < a.num_seqs; seq0 += kMaxSeqs) {
       const int nseq = std::min(kMaxSeqs, a.num_seqs - seq0);
-      kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, seq0, nseq, parts, q_vec);
+      kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, seq0, nseq, range, parts, q_vec);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
       join_kernel<T, D, ROWS, WARPS>
-          <<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(c, a, seq0, nseq, parts, sh);
+          <<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(c, a, seq0, nseq, range, parts, sh);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
@@ -854,12 +818,27 @@ auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
 
 }  // namespace
 
+// Requests with more rows per kv head than this go to the chunk kernel, whose work for
+// a key is that of 256 rows whatever their number (measured: see kda_cache_chunk.cu).
+constexpr int64_t kSplitRows = 64;
+
 size_t cache_attention_workspace_bytes(const View& c, const AttentionArgs& a) {
-  return dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });
+  const size_t split = dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });
+  return std::max(split, cache_chunk_wanted(c, a) ? cache_chunk_workspace_bytes(c, a) : 0);
+}
+
+bool cache_chunk_wanted(const View& c, const AttentionArgs& a) {
+  return a.bf16 && (int64_t)a.max_new * (a.num_heads / c.kv_heads) > kSplitRows;
 }
 
 cudaError_t launch_cache_attention(const View& c, const AttentionArgs& a, cudaStream_t st) {
-  return dispatch(c, a, [&](auto v) { return decltype(v)::launch(c, a, st); });
+  const bool chunk = cache_chunk_wanted(c, a);
+  // without the second kernel the first takes every request, whatever max_new said
+  const RowRange few{0, chunk ? kSplitRows : INT64_MAX}, many{kSplitRows, INT64_MAX};
+  const cudaError_t e =
+      dispatch(c, a, [&](auto v) { return decltype(v)::launch(c, a, few, st); });
+  if (e != cudaSuccess || !chunk) return e;
+  return launch_cache_chunk(c, a, many, st);
 }
 
 }  // namespace kda

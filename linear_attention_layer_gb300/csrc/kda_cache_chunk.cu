@@ -1,0 +1,725 @@
+// kda_cache_chunk.cu -- kda_cache_attention for many rows per kv head (prefill
+// chunks, bf16): causal attention over the 4-bit paged cache on tcgen05.
+//
+// A unit is a request, a kv head and up to 256 of the rows (new token x query head)
+// that share it, as two blocks of 128 rows.  Its keys are walked in tiles of 64,
+//     S = q K^T,   P = 2^(S f - m),   l += row sums of P,   O += P V,
+// with the running reference m of kda_cache_attention.cu (moved, and O rescaled,
+// only when a score passes it by more than 8).  4 * 64 * 128 * D flops a block and
+// tile stand against the softmax of 128 x 64 scores and, shared by the blocks, the
+// dequantisation of 2 * 64 * D codes: the tensor cores bound it if those two keep
+// out of their way.
+//
+// Operands.  q (halves, a power of two per row taken out, see row_scale) and P stay in
+// tensor memory as A operands; K and V are dequantised to halves in shared memory
+// (code x scale is exact), K as a K-major and V as an MN-major B operand -- the same
+// bytes in both cases: rows of keys, 64 channels to a 128-byte swizzled row.  With A in
+// tensor memory shared memory only feeds B, 64 bytes a cycle of the 128 it has, which
+// leaves room for writing the dequantised tiles.  Tensor memory, 512 columns of 32
+// bits: S 2 x 64 (P overlays S), q 2 x D/2, O 2 x D.
+//
+// Warps.  0-3 and 4-7: softmax of the two blocks, a thread a row; 8-11: dequantisation;
+// 12: issues the matrix products; 13: copies pages into a ring.  The blocks alternate,
+// so that one's products run under the other's softmax.  P of a tile is read by its
+// product with V before the next S of that block overwrites it: both are issued by one
+// thread, in that order.
+//
+// Work split.  The tiles of all units in one sequence are cut evenly over the CTAs, one
+// per SM; parts of a unit are joined by a second kernel.  Units of one chunk differ in
+// length (causality), so a planner kernel sums them first.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kda_cache_attention.cuh"
+
+namespace kda {
+namespace {
+
+using namespace cache;
+
+constexpr int kBlock = 128;             // rows of a block
+constexpr int kRows = 2 * kBlock;       // rows of a unit
+constexpr int kKeys = 64;               // keys of a tile
+constexpr int kGroups = kKeys / kGroup;
+constexpr int kRawStages = 4, kTileStages = 3;
+constexpr int kValidRing = 16;          // more tiles than can be under way
+constexpr int kThreads = 14 * 32;
+constexpr uint32_t kCols = 512;
+
+struct Plan {
+  unsigned long long* tiles;  // [entries + 1] tiles before each entry (request, row unit)
+  int2* entry;                // request, row unit
+  int* first;                 // [num_seqs + 1] first entry of each request
+  float* o;                   // [2 * ctas][kRows][D]
+  float2* ml;                 // [2 * ctas][kRows]
+};
+
+// Keys that the rows of a unit see at most: those its last row sees.
+__device__ __forceinline__ int unit_tiles(const Request& q, int group, int r) {
+  const int64_t last = min((int64_t)(r + 1) * kRows, q.rows) - 1;
+  const int see = q.kv - q.n + (int)(last / group) + 1;
+  return max(1, (see + kKeys - 1) / kKeys);  // rows that see nothing still get their zeros
+}
+
+// Sums over the block, inclusive.
+__device__ __forceinline__ unsigned long long scan1024(unsigned long long x,
+                                                       unsigned long long* sums,
+                                                       unsigned long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    unsigned long long s = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    sums[lane] = s;
+  }
+  __syncthreads();
+  total = sums[31];
+  return warp ? x + sums[warp - 1] : x;
+}
+
+__global__ void __launch_bounds__(1024) plan_kernel(View c, AttentionArgs a, RowRange range,
+                                                    Plan plan, int max_entries) {
+  __shared__ unsigned long long sums[32];
+  const int group = a.num_heads / c.kv_heads;
+  unsigned long long at = 0, total;
+  for (int base = 0; base < a.num_seqs; base += 1024) {
+    const int b = base + threadIdx.x;
+    Request q;
+    const bool live = b < a.num_seqs && load_request(c, a, b, range, false, q);
+    const unsigned long long n = live ? (q.rows + kRows - 1) / kRows : 0;
+    const unsigned long long incl = scan1024(n, sums, total);
+    if (b < a.num_seqs) plan.first[b] = (int)min(at + incl - n, (unsigned long long)max_entries);
+    at += total;
+  }
+  // ranges that overlap (malformed offsets) could ask for more entries than there is room for
+  const int entries = (int)min(at, (unsigned long long)max_entries);
+  if (threadIdx.x == 0) plan.first[a.num_seqs] = entries;
+  __syncthreads();
+  unsigned long long tiles = 0;
+  for (int base = 0; base < entries; base += 1024) {
+    const int e = base + threadIdx.x;
+    unsigned long long n = 0;
+    if (e < entries) {
+      const int b = find_last(plan.first, a.num_seqs, e);
+      Request q;
+      load_request(c, a, b, range, false, q);
+      const int r = e - plan.first[b];
+      n = (unsigned long long)unit_tiles(q, group, r) * c.kv_heads;
+      plan.entry[e] = make_int2(b, r);
+    }
+    const unsigned long long incl = scan1024(n, sums, total);
+    if (e < entries) plan.tiles[e] = tiles + incl - n;
+    tiles += total;
+  }
+  if (threadIdx.x == 0) plan.tiles[entries] = tiles;
+}
+
+// The part of a unit that a CTA works on next.
+struct Piece {
+  Request q;
+  int h, r;
+  int b;
+  int begin, end;  // tiles
+  int tiles;       // of the unit
+  int entry;
+
+  // x: first tile of the piece in the sequence of all; stop: the CTA's last + 1.
+  __device__ __forceinline__ void set(const View& c, const AttentionArgs& a, const RowRange& range,
+                                      const Plan& plan, int entries, unsigned long long x,
+                                      unsigned long long stop) {
+    entry = find_last(plan.tiles, entries, x);
+    const int2 er = plan.entry[entry];
+    b = er.x;
+    r = er.y;
+    load_request(c, a, b, range, false, q);
+    tiles = unit_tiles(q, a.num_heads / c.kv_heads, r);
+    const unsigned long long off = x - plan.tiles[entry];
+    h = (int)(off / tiles);
+    begin = (int)(off - (unsigned long long)h * tiles);
+    end = (int)min((unsigned long long)tiles, begin + (stop - x));
+  }
+  __device__ __forceinline__ int rows() const {
+    return (int)min(q.rows - (int64_t)r * kRows, (int64_t)kRows);
+  }
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = kKeys * D * 2;
+  static constexpr int kRaw = kGroups * Layout<D>::kGroupBytes;
+  alignas(1024) uint8_t k[kTileStages][kTile];
+  alignas(1024) uint8_t v[kTileStages][kTile];
+  alignas(128) uint8_t raw[kRawStages][kRaw];
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint32_t valid[kValidRing];  // groups of a tile that can be read
+  uint32_t tmem;
+  int failed;
+};
+
+// A position in a ring of N barriers: index and the parity of the fill being waited for.
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(View c, AttentionArgs a, RowRange range, Plan plan, int q_vec) {
+  using L = Layout<D>;
+  constexpr uint32_t TS = 0, TQ = 2 * kKeys, TO = 2 * kKeys + D;  // columns of S, q, O
+  extern __shared__ uint8_t raw_smem[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw_smem + (-tc::smem_u32(raw_smem) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.num_heads / c.kv_heads;
+
+  if (warp == 12) {
+    tc::tmem_alloc(&sm.tmem, kCols);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRawStages; ++i) {
+      tc::mbar_init(&sm.raw_full[i], kGroups);
+      tc::mbar_init(&sm.raw_empty[i], 4);
+    }
+    for (int i = 0; i < kTileStages; ++i) {
+      tc::mbar_init(&sm.k_full[i], 4);
+      tc::mbar_init(&sm.v_full[i], 4);
+      tc::mbar_init(&sm.k_empty[i], 1);
+      tc::mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sm.q_full[i], 4);
+      tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.p_full[i], 4);
+      tc::mbar_init(&sm.o_full[i], 1);
+    }
+    sm.failed = 0;
+    tc::mbar_fence_init();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  const int entries = plan.first[a.num_seqs];
+  const unsigned long long total = entries ? plan.tiles[entries] : 0;
+  const unsigned long long per = (total + gridDim.x - 1) / gridDim.x;
+  const unsigned long long x0 = min(per * blockIdx.x, total), x1 = min(x0 + per, total);
+
+  // A wait that gives up tells the other warps, who give up as well.
+  volatile int* failed = &sm.failed;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (wait_phase(bar, parity, failed)) return true;
+    *failed = 1;
+    report_error(a.err, kErrTimeout);
+    return false;
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax ----
+    const int blk = warp >> 2;
+    const int row = tid & (kBlock - 1);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = lanes + TS + blk * kKeys, tq = lanes + TQ + blk * (D / 2),
+                   to = lanes + TO + blk * D;
+    Ring<1> s_full, o_full;
+    uint32_t tile_no = 0;  // tiles since the start, over all pieces
+    bool ok = true;
+    for (unsigned long long x = x0; x < x1 && ok;) {
+      Piece p;
+      p.set(c, a, range, plan, entries, x, x1);
+      x += p.end - p.begin;
+      const int rows = p.rows();
+      if (blk * kBlock >= rows) {
+        tile_no += p.end - p.begin;
+        continue;
+      }
+      const int64_t rr = (int64_t)p.r * kRows + blk * kBlock + row;  // row of the request
+      const bool live = blk * kBlock + row < rows;
+      const int64_t tok = p.q.bos + rr / group;
+      const int head = p.h * group + (int)(rr % group);
+      const int see = live ? p.q.kv - p.q.n + (int)(rr / group) + 1 : 0;
+      // what every row of the block sees
+      const int all_see = p.q.kv - p.q.n + (int)(((int64_t)p.r * kRows + blk * kBlock) / group) + 1;
+      // ---- queries ----
+      float f;
+      {
+        uint32_t w[D / 2];
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                   tok * a.q_token_stride + head * a.q_head_stride;
+        if (!live) {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) w[i] = 0;
+        } else if (q_vec) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i)
+            w[i] = __float_as_uint(IO<__nv_bfloat16>::ld(src + 2 * i)) >> 16 |
+                   __float_as_uint(IO<__nv_bfloat16>::ld(src + 2 * i + 1));
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          top = fmaxf(top, fmaxf(fabsf(tc::bf16_lo(w[i])), fabsf(tc::bf16_hi(w[i]))));
+        const RowScale rs = row_scale(top, a.scale, exponent_scale(c.k_exp, p.h, 1));
+        f = rs.f;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i)
+          w[i] = tc::pack_f16(tc::bf16_lo(w[i]) * rs.down, tc::bf16_hi(w[i]) * rs.down);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          uint32_t part[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) part[j] = w[32 * i + j];
+          tc::tmem_st32(tq + 32 * i, part);
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.q_full[blk]);
+      }
+      float neg = 0.f, thr = -INFINITY, l = 0.f;
+      for (int j = p.begin; j < p.end; ++j, ++tile_no) {
+        ok = wait(&sm.s_full[blk], s_full.parity);
+        if (!ok) break;
+        s_full.step();
+        tc::tc_fence_after();
+        float s[kKeys];
+        {
+          float h0[32], h1[32];
+          tc::tmem_ld32(ts, h0);
+          tc::tmem_ld32(ts + 32, h1);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = h0[i], s[32 + i] = h1[i];
+        }
+        const uint32_t valid = *(volatile uint32_t*)&sm.valid[tile_no % kValidRing];
+        const int key0 = j * kKeys;
+        if (key0 + kKeys > all_see || valid != (1u << kGroups) - 1) {
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (key0 + i >= see || !(valid >> (i / kGroup) & 1)) s[i] = -INFINITY;
+        }
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < kKeys; ++i) top = fmaxf(top, s[i]);
+        if (__any_sync(0xffffffffu, top > thr)) {
+          float keep = 1.f;
+          if (top > -INFINITY) {
+            const float before = thr == -INFINITY ? -INFINITY : -neg;
+            const float m = fmaxf(before, top * f);
+            keep = ex2_approx(before - m);
+            neg = -m;
+            thr = (m + kSlack) / f;
+          }
+          l *= keep;
+          if (j > p.begin) {
+            // the product of the tile before has to be in O
+            ok = wait(&sm.o_full[blk], o_full.parity);
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              float o[32];
+              uint32_t w[32];
+              tc::tmem_ld32(to + i, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 32; ++q) w[q] = __float_as_uint(o[q] * keep);
+              tc::tmem_st32(to + i, w);
+            }
+          }
+        }
+        uint32_t w[kKeys / 2];
+        float l2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < kKeys / 2; ++i) {
+          const float p0 = ex2_approx(fmaf(s[2 * i], f, neg));
+          const float p1 = ex2_approx(fmaf(s[2 * i + 1], f, neg));
+          l += p0;
+          l2 += p1;
+          w[i] = tc::pack_f16(p0, p1);
+        }
+        l += l2;
+        tc::tmem_st32(ts, w);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.p_full[blk]);
+        if (j > p.begin) o_full.step();  // that product is past by now, waited for or not
+      }
+      if (!ok) break;
+      // ---- end of the piece ----
+      ok = wait(&sm.o_full[blk], o_full.parity);
+      if (!ok) break;
+      o_full.step();
+      tc::tc_fence_after();
+      const bool whole = p.begin == 0 && p.end == p.tiles;
+      const float inv =
+          !whole ? 1.f : l == 0.f ? 0.f : exponent_scale(c.v_exp, p.h, 1) / l;
+      const float m = thr == -INFINITY ? -INFINITY : -neg;
+      const int64_t out_at = tok * a.num_heads + head;
+      const int64_t part_at =
+          (int64_t)(2 * blockIdx.x + (p.begin == 0 ? 1 : 0)) * kRows + blk * kBlock + row;
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {
+        float o[32];
+        tc::tmem_ld32(to + i, o);
+        tc::tmem_ld_wait();
+        if (!live) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_at * D + i);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(tc::pack_bf16(o[8 * q] * inv, o[8 * q + 1] * inv),
+                                tc::pack_bf16(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                tc::pack_bf16(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                                tc::pack_bf16(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(plan.o + part_at * D + i);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+      if (live) {
+        if (!whole)
+          plan.ml[part_at] = make_float2(m, l);
+        else if (a.lse)
+          a.lse[out_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      tc::tc_fence_before();  // the reads of O come before the next piece's products
+    }
+  } else if (warp < 12) {
+    // ----------------------------------------------------- dequantisation ----
+    const int dw = warp - 8;
+    Ring<kRawStages> raw;
+    Ring<kTileStages> st;
+    uint32_t empty_parity = 1;  // a fresh barrier passes for the phase before
+    uint32_t tile_no = 0;
+    bool ok = true;
+    for (unsigned long long x = x0; x < x1 && ok;) {
+      Piece p;
+      p.set(c, a, range, plan, entries, x, x1);
+      x += p.end - p.begin;
+      for (int j = p.begin; j < p.end; ++j, ++tile_no) {
+        ok = wait(&sm.raw_full[raw.i], raw.parity);
+        if (!ok) break;
+        // warp dw takes group dw of the tile: lane = token of a half (8) x block of 4
+        const uint8_t* g = sm.raw[raw.i] + dw * L::kGroupBytes;
+        const bool here = sm.valid[tile_no % kValidRing] >> dw & 1;
+        const int left = here ? p.q.kv - j * kKeys - dw * kGroup : 0;  // tokens of the group
+        const int t8 = lane & 7;
+        auto put = [&](uint8_t* tile, int i, int b, uint2 codes, uint32_t scale) {
+          const uint32_t h = e4m3x2_to_f16x2(scale);
+          const uint32_t s2 = __byte_perm(h, 0, 0x1010);
+          uint32_t lo[4], hi[4];
+          e2m1x8_to_f16(codes.x, lo);
+          e2m1x8_to_f16(codes.y, hi);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) lo[q] = mul_f16x2(lo[q], s2), hi[q] = mul_f16x2(hi[q], s2);
+          const uint32_t key = dw * kGroup + i;
+          uint8_t* at = tile + (b >> 2) * (kKeys * 128) + key * 128;
+          const uint32_t chunk = (b & 3) * 2, x7 = key & 7;
+          *reinterpret_cast<uint4*>(at + ((chunk ^ x7) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ x7) << 4)) =
+              make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        };
+        ok = wait(&sm.k_empty[st.i], empty_parity);
+        if (!ok) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int bb = 0; bb < D / 64; ++bb) {
+            const int i = half * 8 + t8, b = bb * 4 + (lane >> 3);
+            put(sm.k[st.i], i, b, *reinterpret_cast<const uint2*>(g + L::k_codes(i, b)),
+                g[L::k_scale(i, b)]);
+          }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.k_full[st.i]);
+        ok = wait(&sm.v_empty[st.i], empty_parity);
+        if (!ok) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int bb = 0; bb < D / 64; ++bb) {
+            const int i = half * 8 + t8, b = bb * 4 + (lane >> 3);
+            // what lies past the request's length may be anything: its scale becomes 0
+            put(sm.v[st.i], i, b, *reinterpret_cast<const uint2*>(g + L::v_codes(i, b)),
+                i < left ? g[L::v_scale(i, b)] : 0u);
+          }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&sm.v_full[st.i]);
+          tc::mbar_arrive(&sm.raw_empty[raw.i]);
+        }
+        raw.step();
+        st.step();
+        if (st.i == 0) empty_parity ^= 1;
+      }
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------ matrix products ----
+    if (lane == 0) {
+      const uint64_t kd = tc::make_sdesc(tc::smem_u32(sm.k), 0, 1024, tc::kSwizzle128);
+      const uint64_t vd = tc::make_sdesc(tc::smem_u32(sm.v), kKeys * 128, 1024, tc::kSwizzle128);
+      const uint32_t id_s = tc::make_idesc_f16(128, kKeys, false, false);
+      const uint32_t id_o = tc::make_idesc_f16(128, D, false, true);
+      Ring<kTileStages> ks, vs;
+      Ring<1> q_full[2], p_full[2];
+      bool ok = true;
+      for (unsigned long long x = x0; x < x1 && ok;) {
+        Piece p;
+        p.set(c, a, range, plan, entries, x, x1);
+        x += p.end - p.begin;
+        const int blocks = p.rows() > kBlock ? 2 : 1;
+        const int n = p.end - p.begin;
+        auto scores = [&](int blk) {
+          const uint64_t b0 = kd + (uint64_t)(ks.i * Smem<D>::kTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ts(tmem + TS + blk * kKeys, tmem + TQ + blk * (D / 2) + kk * 8,
+                       b0 + (uint64_t)(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4), id_s,
+                       kk > 0);
+          tc::mma_commit(&sm.s_full[blk]);
+        };
+        auto next_keys = [&]() {
+          ok = wait(&sm.k_full[ks.i], ks.parity);
+          tc::tc_fence_after();
+          return ok;
+        };
+        for (int blk = 0; blk < blocks && ok; ++blk) {
+          ok = wait(&sm.q_full[blk], q_full[blk].parity);
+          q_full[blk].step();
+        }
+        if (!ok || !next_keys()) break;
+        for (int blk = 0; blk < blocks; ++blk) scores(blk);
+        tc::mma_commit(&sm.k_empty[ks.i]);
+        ks.step();
+        for (int j = 0; j < n && ok; ++j) {
+          ok = wait(&sm.v_full[vs.i], vs.parity);
+          if (!ok) break;
+          for (int blk = 0; blk < blocks && ok; ++blk) {
+            ok = wait(&sm.p_full[blk], p_full[blk].parity);
+            if (!ok) break;
+            p_full[blk].step();
+            tc::tc_fence_after();
+            const uint64_t b0 = vd + (uint64_t)(vs.i * Smem<D>::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc::mma_ts(tmem + TO + blk * D, tmem + TS + blk * kKeys + kk * 8,
+                         b0 + (uint64_t)(kk * 2048 >> 4), id_o, j > 0 || kk > 0);
+            tc::mma_commit(&sm.o_full[blk]);
+            if (blk == blocks - 1) tc::mma_commit(&sm.v_empty[vs.i]);
+            if (j + 1 < n) {
+              if (blk == 0 && !next_keys()) break;
+              scores(blk);
+              if (blk == blocks - 1) tc::mma_commit(&sm.k_empty[ks.i]);
+            }
+          }
+          vs.step();
+          if (j + 1 < n) ks.step();
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- pages ----
+    const int GP = c.page_size / kGroup;
+    Ring<kRawStages> raw;
+    uint32_t empty_parity = 1, tile_no = 0;
+    bool ok = true;
+    for (unsigned long long x = x0; x < x1 && ok;) {
+      Piece p;
+      p.set(c, a, range, plan, entries, x, x1);
+      x += p.end - p.begin;
+      const uint8_t* src = nullptr;
+      uint32_t present = 0;  // of the 32 groups from 32 n on, for the n being loaded
+      for (int j = p.begin; j < p.end; ++j, ++tile_no) {
+        const int first = j * kGroups & 31;
+        if (first == 0 || j == p.begin) {
+          const int gi = (j * kGroups & ~31) + lane;
+          const bool in = gi < (p.q.kv + kGroup - 1) / kGroup;
+          const int page =
+              in ? __ldg(a.block_table + (int64_t)p.b * a.max_blocks + gi / GP) : 0;
+          const bool sound = page >= 0 && page < c.num_pages;
+          if (in && !sound) report_error(a.err, kErrDeviceCheck);
+          src = c.pages + (((int64_t)page * c.kv_heads + p.h) * GP + gi % GP) * L::kGroupBytes;
+          present = __ballot_sync(0xffffffffu, in && sound);
+        }
+        ok = wait(&sm.raw_empty[raw.i], empty_parity);
+        if (!ok) break;
+        if ((lane ^ first) < kGroups) {
+          const int u = lane ^ first;
+          if (u == 0)
+            *(volatile uint32_t*)&sm.valid[tile_no % kValidRing] =
+                present >> first & ((1u << kGroups) - 1);
+          if (present >> lane & 1) {
+            tc::mbar_arrive_expect_tx(&sm.raw_full[raw.i], L::kGroupBytes);
+            tc::bulk_load(sm.raw[raw.i] + u * L::kGroupBytes, src, L::kGroupBytes,
+                          &sm.raw_full[raw.i]);
+          } else {
+            tc::mbar_arrive(&sm.raw_full[raw.i]);
+          }
+        }
+        __syncwarp();
+        raw.step();
+        if (raw.i == 0) empty_parity ^= 1;
+      }
+    }
+  }
+  // After a wait gave up, copies and products may be under way: let them land.
+  if (*failed) __nanosleep(1000000);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 12) tc::tmem_dealloc(tmem, kCols);
+}
+
+// Joins the parts of units that several CTAs had: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128)
+    chunk_join_kernel(View c, AttentionArgs a, RowRange range, Plan plan, int ctas) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int group = a.num_heads / c.kv_heads;
+  const int64_t tok = w / a.num_heads;
+  const int hq = (int)(w - tok * a.num_heads);
+  if (tok >= a.total_tokens || tok < a.cu_new[0] || tok >= a.cu_new[a.num_seqs]) return;
+  const int b = find_last(a.cu_new, a.num_seqs, (unsigned long long)tok);
+  Request q;
+  if (!load_request(c, a, b, range, false, q) || tok < q.bos || tok >= q.bos + q.n) return;
+  const int entries = plan.first[a.num_seqs];
+  const unsigned long long total = plan.tiles[entries];
+  const unsigned long long per = (total + ctas - 1) / ctas;
+  const int h = hq / group;
+  const int64_t rr = (tok - q.bos) * group + hq % group;
+  const int r = (int)(rr / kRows), row = (int)(rr % kRows);
+  const int e = plan.first[b] + r;
+  if (e >= entries) return;
+  const int tiles = unit_tiles(q, group, r);
+  const unsigned long long u0 = plan.tiles[e] + (unsigned long long)h * tiles;
+  const int first = (int)(u0 / per), last = (int)((u0 + tiles - 1) / per);
+  if (first == last) return;
+  auto at_of = [&](int cta) {
+    return (int64_t)(2 * cta + (cta == first ? 1 : 0)) * kRows + row;
+  };
+  float top = -INFINITY;
+  for (int i = first + lane; i <= last; i += 32) top = fmaxf(top, plan.ml[at_of(i)].x);
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  float sum = 0.f, x[D / 32] = {};
+#pragma unroll 2
+  for (int i = first; i <= last; ++i) {
+    const int64_t at = at_of(i);
+    const float2 ml = plan.ml[at];
+    const float k = top == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+    sum = fmaf(ml.y, k, sum);
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) x[j] = fmaf(plan.o[at * D + j * 32 + lane], k, x[j]);
+  }
+  const float inv = sum == 0.f ? 0.f : exponent_scale(c.v_exp, h, 1) / sum;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + w * D;
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) out[j * 32 + lane] = __float2bfloat16_rn(x[j] * inv);
+  if (a.lse && lane == 0) a.lse[w] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Entries that well-formed offsets can ask for: a unit of rows each, one more per request.
+int64_t max_entries(const View& c, const AttentionArgs& a) {
+  const int64_t rows = (int64_t)a.total_tokens * (a.num_heads / c.kv_heads);
+  return std::min<int64_t>(rows / kRows + a.num_seqs, INT32_MAX - 1);
+}
+
+template <int D>
+size_t layout(const View& c, const AttentionArgs& a, uint8_t* ws, Plan* plan) {
+  const size_t n = (size_t)max_entries(c, a), slots = 2 * (size_t)sm_count();
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = ws + at;
+    at += up256(bytes);
+    return p;
+  };
+  Plan p;
+  p.tiles = reinterpret_cast<unsigned long long*>(take((n + 1) * 8));
+  p.entry = reinterpret_cast<int2*>(take((n + 1) * 8));
+  p.first = reinterpret_cast<int*>(take(((size_t)a.num_seqs + 1) * 4));
+  p.o = reinterpret_cast<float*>(take(slots * kRows * D * 4));
+  p.ml = reinterpret_cast<float2*>(take(slots * kRows * 8));
+  if (plan) *plan = p;
+  return at;
+}
+
+template <int D>
+cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cudaStream_t st) {
+  static PerDeviceInit init;
+  constexpr int kSmem = (int)sizeof(Smem<D>) + 1024;
+  cudaError_t e = init.run([&] {
+    return cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  Plan plan;
+  layout<D>(c, a, static_cast<uint8_t*>(a.workspace), &plan);
+  const int ctas = sm_count();
+  const int q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.q_token_stride % 8 == 0 &&
+                    a.q_head_stride % 8 == 0;
+  plan_kernel<<<1, 1024, 0, st>>>(c, a, range, plan, (int)max_entries(c, a));
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  chunk_kernel<D><<<ctas, kThreads, kSmem, st>>>(c, a, range, plan, q_vec);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.total_tokens * a.num_heads;
+  chunk_join_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(c, a, range, plan, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_chunk_workspace_bytes(const View& c, const AttentionArgs& a) {
+  return a.head_dim == 128 ? layout<128>(c, a, nullptr, nullptr)
+                           : layout<64>(c, a, nullptr, nullptr);
+}
+
+cudaError_t launch_cache_chunk(const View& c, const AttentionArgs& a, const RowRange& range,
+                               cudaStream_t st) {
+  return a.head_dim == 128 ? run<128>(c, a, range, st) : run<64>(c, a, range, st);
+}
+
+}  // namespace kda

@@ -283,6 +283,15 @@ struct AttentionArgs {
 };
 size_t cache_attention_workspace_bytes(const cache::View& c, const AttentionArgs& a);
 cudaError_t launch_cache_attention(const cache::View& c, const AttentionArgs& a, cudaStream_t st);
+// Its kernel for many rows per kv head (kda_cache_chunk.cu, bf16): requests with rows in
+// (range.above, range.up_to]; whether a call may hold such requests, its scratch.
+namespace cache {
+struct RowRange;
+}
+bool cache_chunk_wanted(const cache::View& c, const AttentionArgs& a);
+size_t cache_chunk_workspace_bytes(const cache::View& c, const AttentionArgs& a);
+cudaError_t launch_cache_chunk(const cache::View& c, const AttentionArgs& a,
+                               const cache::RowRange& range, cudaStream_t st);
 
 }  // namespace kda
 
