@@ -262,49 +262,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int see = live ? p.q.kv - p.q.n + (int)(rr / group) + 1 : 0;
       // what every row of the block sees
       const int all_see = p.q.kv - p.q.n + (int)(((int64_t)p.r * kRows + blk * kBlock) / group) + 1;
-      // ---- queries ----
+      // ---- queries: the largest magnitude, then 32 channels at a time ----
       float f;
       {
-        uint32_t w[D / 2];
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
                                    tok * a.q_token_stride + head * a.q_head_stride;
-        if (!live) {
+        auto load32 = [&](int i, uint32_t (&w)[16]) {
+          if (!live) {
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) w[i] = 0;
-        } else if (q_vec) {
+            for (int q = 0; q < 16; ++q) w[q] = 0;
+          } else if (q_vec) {
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
-            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            for (int q = 0; q < 4; ++q) {
+              const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + i) + q);
+              w[4 * q] = u.x, w[4 * q + 1] = u.y, w[4 * q + 2] = u.z, w[4 * q + 3] = u.w;
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              w[q] = __float_as_uint(IO<__nv_bfloat16>::ld(src + i + 2 * q)) >> 16 |
+                     __float_as_uint(IO<__nv_bfloat16>::ld(src + i + 2 * q + 1));
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 2; ++i)
-            w[i] = __float_as_uint(IO<__nv_bfloat16>::ld(src + 2 * i)) >> 16 |
-                   __float_as_uint(IO<__nv_bfloat16>::ld(src + 2 * i + 1));
-        }
+        };
         float top = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t w[16];
+          load32(i, w);
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i)
-          top = fmaxf(top, fmaxf(fabsf(tc::bf16_lo(w[i])), fabsf(tc::bf16_hi(w[i]))));
+          for (int q = 0; q < 16; ++q)
+            top = fmaxf(top, fmaxf(fabsf(tc::bf16_lo(w[q])), fabsf(tc::bf16_hi(w[q]))));
+        }
         const RowScale rs = row_scale(top, a.scale, exponent_scale(c.k_exp, p.h, 1));
         f = rs.f;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t w[16];
+          load32(i, w);
 #pragma unroll
-        for (int i = 0; i < D / 2; ++i)
-          w[i] = tc::pack_f16(tc::bf16_lo(w[i]) * rs.down, tc::bf16_hi(w[i]) * rs.down);
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          uint32_t part[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) part[j] = w[32 * i + j];
-          tc::tmem_st32(tq + 32 * i, part);
+          for (int q = 0; q < 16; ++q)
+            w[q] = tc::pack_f16(tc::bf16_lo(w[q]) * rs.down, tc::bf16_hi(w[q]) * rs.down);
+          tc::tmem_st16u(tq + i / 2, w);
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.q_full[blk]);
       }
-      float neg = 0.f, thr = -INFINITY, l = 0.f;
+      float neg = 0.f, thr = -INFINITY;
+      uint64_t l2[2] = {0, 0};  // the row's sum, in four parts
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         ok = wait(&sm.s_full[blk], s_full.parity);
         if (!ok) break;
@@ -326,9 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kKeys; ++i)
             if (key0 + i >= see || !(valid >> (i / kGroup) & 1)) s[i] = -INFINITY;
         }
-        float top = s[0];
+        float t4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 1; i < kKeys; ++i) top = fmaxf(top, s[i]);
+        for (int i = 4; i < kKeys - 4; i += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) t4[q] = tc::max3(t4[q], s[i + q], s[i + 4 + q]);
+        const float top = fmaxf(tc::max3(t4[0], s[kKeys - 4], s[kKeys - 3]),
+                                tc::max3(tc::max3(t4[1], t4[2], t4[3]), s[kKeys - 2], s[kKeys - 1]));
         if (__any_sync(0xffffffffu, top > thr)) {
           float keep = 1.f;
           if (top > -INFINITY) {
@@ -338,7 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             neg = -m;
             thr = (m + kSlack) / f;
           }
-          l *= keep;
+          const uint64_t keep2 = tc::pack2(keep, keep);
+          l2[0] = tc::fma2(l2[0], keep2, 0);
+          l2[1] = tc::fma2(l2[1], keep2, 0);
           if (j > p.begin) {
             // the product of the tile before has to be in O
             ok = wait(&sm.o_full[blk], o_full.parity);
@@ -356,18 +368,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        uint32_t w[kKeys / 2];
-        float l2 = 0.f;
+        const uint64_t f2 = tc::pack2(f, f), neg2 = tc::pack2(neg, neg);
 #pragma unroll
-        for (int i = 0; i < kKeys / 2; ++i) {
-          const float p0 = ex2_approx(fmaf(s[2 * i], f, neg));
-          const float p1 = ex2_approx(fmaf(s[2 * i + 1], f, neg));
-          l += p0;
-          l2 += p1;
-          w[i] = tc::pack_f16(p0, p1);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int at = half * 32 + 2 * i;
+            float p0, p1;
+            tc::unpack2(tc::fma2(tc::pack2(s[at], s[at + 1]), f2, neg2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            l2[i & 1] = tc::add2(l2[i & 1], tc::pack2(p0, p1));
+            w[i] = tc::pack_f16(p0, p1);
+          }
+          tc::tmem_st16u(ts + half * 16, w);
         }
-        l += l2;
-        tc::tmem_st32(ts, w);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
@@ -380,6 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       o_full.step();
       tc::tc_fence_after();
+      float l, la, lb;
+      tc::unpack2(tc::add2(l2[0], l2[1]), la, lb);
+      l = la + lb;
       const bool whole = p.begin == 0 && p.end == p.tiles;
       const float inv =
           !whole ? 1.f : l == 0.f ? 0.f : exponent_scale(c.v_exp, p.h, 1) / l;
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 12) {
     // ------------------------------------------------------ matrix products ----
-    if (lane == 0) {
+    if (tc::elect_one()) {  // (2048-token chunk over 32768 keys: 869 us; by lane == 0: 1392)
       const uint64_t kd = tc::make_sdesc(tc::smem_u32(sm.k), 0, 1024, tc::kSwizzle128);
       const uint64_t vd = tc::make_sdesc(tc::smem_u32(sm.v), kKeys * 128, 1024, tc::kSwizzle128);
       const uint32_t id_s = tc::make_idesc_f16(128, kKeys, false, false);
