@@ -10,19 +10,21 @@
 // dequantisation of 2 * 64 * D codes: the tensor cores bound it if those two keep
 // out of their way.
 //
-// Operands.  q (halves, a power of two per row taken out, see row_scale) and P stay in
-// tensor memory as A operands; K and V are dequantised to halves in shared memory
-// (code x scale is exact), K as a K-major and V as an MN-major B operand -- the same
-// bytes in both cases: rows of keys, 64 channels to a 128-byte swizzled row.  With A in
-// tensor memory shared memory only feeds B, 64 bytes a cycle of the 128 it has, which
-// leaves room for writing the dequantised tiles.  Tensor memory, 512 columns of 32
-// bits: S 2 x 64 (P overlays S), q 2 x D/2, O 2 x D.
+// Operands.  P and q (halves, a power of two per row taken out, see row_scale) are A
+// operands in tensor memory; K and V are dequantised to halves in shared memory (code x
+// scale is exact), K as a K-major and V as an MN-major B operand -- the same bytes in
+// both cases: rows of keys, 64 channels to a 128-byte swizzled row.  With A in tensor
+// memory shared memory only feeds B, 64 bytes a cycle of the 128 it has, which leaves room
+// for writing the dequantised tiles.  Tensor memory, 512 columns of 32 bits: S 2 x 64,
+// P 2 x 32, q 64, O 2 x D: with D = 128 the second block's q has no room there and is an
+// A operand in shared memory (its 8 score products then take 48 cycles instead of 32).
+// P apart from S is worth that: the next scores are computed while a tile's weights
+// are (with P over S, and both blocks' q in tensor memory, 822 us instead of XXX for
+// 2048 tokens over 32768 keys, 32 heads on 8).
 //
 // Warps.  0-3 and 4-7: softmax of the two blocks, a thread a row; 8-11: dequantisation;
-// 12: issues the matrix products; 13: copies pages into a ring.  The blocks alternate,
-// so that one's products run under the other's softmax.  P of a tile is read by its
-// product with V before the next S of that block overwrites it: both are issued by one
-// thread, in that order.
+// 12: issues the matrix products; 13: copies pages into a ring.  Two threads a row
+// (16 softmax warps of 80 registers) measured slower, 862 us against 822.
 //
 // Work split.  The tiles of all units in one sequence are cut evenly over the CTAs, one
 // per SM; parts of a unit are joined by a second kernel.  Units of one chunk differ in
@@ -161,10 +163,12 @@ struct Smem {
   static constexpr int kRaw = kGroups * Layout<D>::kGroupBytes;
   alignas(1024) uint8_t k[kTileStages][kTile];
   alignas(1024) uint8_t v[kTileStages][kTile];
+  static constexpr bool kQueryHere = D > 64;  // the second block's
+  alignas(1024) uint8_t q[kQueryHere ? kBlock * D * 2 : 16];
   alignas(128) uint8_t raw[kRawStages][kRaw];
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_full[2];
   uint32_t valid[kValidRing];  // groups of a tile that can be read
   uint32_t tmem;
   int failed;
@@ -187,7 +191,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(View c, AttentionArgs a, RowRange range, Plan plan, int q_vec) {
   using L = Layout<D>;
-  constexpr uint32_t TS = 0, TQ = 2 * kKeys, TO = 2 * kKeys + D;  // columns of S, q, O
+  constexpr uint32_t TS = 0, TP = 128, TQ = 192, TO = 256;  // columns of S, P, q, O
+  constexpr bool QS = Smem<D>::kQueryHere;
   extern __shared__ uint8_t raw_smem[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw_smem + (-tc::smem_u32(raw_smem) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -211,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.q_full[i], 4);
       tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.s_free[i], 4);
       tc::mbar_init(&sm.p_full[i], 4);
       tc::mbar_init(&sm.o_full[i], 1);
     }
@@ -241,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blk = warp >> 2;
     const int row = tid & (kBlock - 1);
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lanes + TS + blk * kKeys, tq = lanes + TQ + blk * (D / 2),
-                   to = lanes + TO + blk * D;
+    const uint32_t ts = lanes + TS + blk * kKeys, tp = lanes + TP + blk * (kKeys / 2),
+                   tq = lanes + TQ + blk * (D / 2), to = lanes + TO + blk * D;
     Ring<1> s_full, o_full;
     uint32_t tile_no = 0;  // tiles since the start, over all pieces
     bool ok = true;
@@ -302,9 +308,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             w[q] = tc::pack_f16(tc::bf16_lo(w[q]) * rs.down, tc::bf16_hi(w[q]) * rs.down);
-          tc::tmem_st16u(tq + i / 2, w);
+          if (QS && blk == 1) {
+            uint8_t* dst = sm.q + (i >> 6) * (kBlock * 128) + row * 128;
+            const uint32_t chunk = (i & 63) >> 3;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(dst + (((chunk + q) ^ (row & 7)) << 4)) =
+                  make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          } else {
+            tc::tmem_st16u(tq + i / 2, w);
+          }
         }
-        tc::tmem_st_wait();
+        if (QS && blk == 1)
+          tc::fence_proxy_async_smem();
+        else
+          tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.q_full[blk]);
@@ -325,6 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[i] = h0[i], s[32 + i] = h1[i];
         }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.s_free[blk]);
         const uint32_t valid = *(volatile uint32_t*)&sm.valid[tile_no % kValidRing];
         const int key0 = j * kKeys;
         if (key0 + kKeys > all_see || valid != (1u << kGroups) - 1) {
@@ -339,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) t4[q] = tc::max3(t4[q], s[i + q], s[i + 4 + q]);
         const float top = fmaxf(tc::max3(t4[0], s[kKeys - 4], s[kKeys - 3]),
                                 tc::max3(tc::max3(t4[1], t4[2], t4[3]), s[kKeys - 2], s[kKeys - 1]));
+        bool waited = false;
         if (__any_sync(0xffffffffu, top > thr)) {
           float keep = 1.f;
           if (top > -INFINITY) {
@@ -356,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(&sm.o_full[blk], o_full.parity);
             if (!ok) break;
             tc::tc_fence_after();
+            waited = true;
 #pragma unroll 1
             for (int i = 0; i < D; i += 32) {
               float o[32];
@@ -382,13 +405,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2[i & 1] = tc::add2(l2[i & 1], tc::pack2(p0, p1));
             w[i] = tc::pack_f16(p0, p1);
           }
-          tc::tmem_st16u(ts + half * 16, w);
+          if (half == 0 && j > p.begin) {  // the product before has read its weights
+            ok = waited || wait(&sm.o_full[blk], o_full.parity);
+            o_full.step();
+            if (!ok) break;
+            tc::tc_fence_after();
+          }
+          tc::tmem_st16u(tp + half * 16, w);
         }
+        if (!ok) break;
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.p_full[blk]);
-        if (j > p.begin) o_full.step();  // that product is past by now, waited for or not
       }
       if (!ok) break;
       // ---- end of the piece ----
@@ -510,10 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tc::elect_one()) {  // (2048-token chunk over 32768 keys: 869 us; by lane == 0: 1392)
       const uint64_t kd = tc::make_sdesc(tc::smem_u32(sm.k), 0, 1024, tc::kSwizzle128);
       const uint64_t vd = tc::make_sdesc(tc::smem_u32(sm.v), kKeys * 128, 1024, tc::kSwizzle128);
+      const uint64_t qd = tc::make_sdesc(tc::smem_u32(sm.q), 0, 1024, tc::kSwizzle128);
       const uint32_t id_s = tc::make_idesc_f16(128, kKeys, false, false);
       const uint32_t id_o = tc::make_idesc_f16(128, D, false, true);
       Ring<kTileStages> ks, vs;
       Ring<1> q_full[2], p_full[2];
+      uint32_t free_parity[2] = {1, 1};
       bool ok = true;
       for (unsigned long long x = x0; x < x1 && ok;) {
         Piece p;
@@ -521,51 +552,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         x += p.end - p.begin;
         const int blocks = p.rows() > kBlock ? 2 : 1;
         const int n = p.end - p.begin;
-        auto scores = [&](int blk) {
-          const uint64_t b0 = kd + (uint64_t)(ks.i * Smem<D>::kTile >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ts(tmem + TS + blk * kKeys, tmem + TQ + blk * (D / 2) + kk * 8,
-                       b0 + (uint64_t)(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4), id_s,
-                       kk > 0);
-          tc::mma_commit(&sm.s_full[blk]);
-        };
-        auto next_keys = [&]() {
+        // scores of the next tile, as soon as the softmax has the tile before in registers
+        auto scores = [&]() {
           ok = wait(&sm.k_full[ks.i], ks.parity);
-          tc::tc_fence_after();
-          return ok;
+          const uint64_t b0 = kd + (uint64_t)(ks.i * Smem<D>::kTile >> 4);
+          for (int blk = 0; blk < blocks && ok; ++blk) {
+            ok = wait(&sm.s_free[blk], free_parity[blk]);
+            if (!ok) break;
+            free_parity[blk] ^= 1;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t b1 =
+                  b0 + (uint64_t)(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4);
+              if (QS && blk == 1)
+                tc::mma_bf16_ss(tmem + TS + kKeys,
+                                qd + (uint64_t)(((kk >> 2) * (kBlock * 128) + (kk & 3) * 32) >> 4),
+                                b1, id_s, kk > 0);
+              else
+                tc::mma_ts(tmem + TS + blk * kKeys, tmem + TQ + blk * (D / 2) + kk * 8, b1, id_s,
+                           kk > 0);
+            }
+            tc::mma_commit(&sm.s_full[blk]);
+          }
+          tc::mma_commit(&sm.k_empty[ks.i]);
+          ks.step();
         };
         for (int blk = 0; blk < blocks && ok; ++blk) {
           ok = wait(&sm.q_full[blk], q_full[blk].parity);
           q_full[blk].step();
         }
-        if (!ok || !next_keys()) break;
-        for (int blk = 0; blk < blocks; ++blk) scores(blk);
-        tc::mma_commit(&sm.k_empty[ks.i]);
-        ks.step();
+        if (ok) scores();
         for (int j = 0; j < n && ok; ++j) {
-          ok = wait(&sm.v_full[vs.i], vs.parity);
-          if (!ok) break;
+          if (j + 1 < n) scores();
+          if (ok) ok = wait(&sm.v_full[vs.i], vs.parity);
+          const uint64_t b0 = vd + (uint64_t)(vs.i * Smem<D>::kTile >> 4);
           for (int blk = 0; blk < blocks && ok; ++blk) {
             ok = wait(&sm.p_full[blk], p_full[blk].parity);
             if (!ok) break;
             p_full[blk].step();
             tc::tc_fence_after();
-            const uint64_t b0 = vd + (uint64_t)(vs.i * Smem<D>::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc::mma_ts(tmem + TO + blk * D, tmem + TS + blk * kKeys + kk * 8,
+              tc::mma_ts(tmem + TO + blk * D, tmem + TP + blk * (kKeys / 2) + kk * 8,
                          b0 + (uint64_t)(kk * 2048 >> 4), id_o, j > 0 || kk > 0);
             tc::mma_commit(&sm.o_full[blk]);
-            if (blk == blocks - 1) tc::mma_commit(&sm.v_empty[vs.i]);
-            if (j + 1 < n) {
-              if (blk == 0 && !next_keys()) break;
-              scores(blk);
-              if (blk == blocks - 1) tc::mma_commit(&sm.k_empty[ks.i]);
-            }
           }
+          tc::mma_commit(&sm.v_empty[vs.i]);
           vs.step();
-          if (j + 1 < n) ks.step();
         }
       }
     }
