@@ -335,10 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_full.step();
         tc::tc_fence_after();
         float s[kKeys];
+        const int key0 = j * kKeys;
+        uint32_t valid;
         {
           float h0[32], h1[32];
           tc::tmem_ld32(ts, h0);
           tc::tmem_ld32(ts + 32, h1);
+          valid = *(volatile uint32_t*)&sm.valid[tile_no % kValidRing];
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[i] = h0[i], s[32 + i] = h1[i];
@@ -346,8 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.s_free[blk]);
-        const uint32_t valid = *(volatile uint32_t*)&sm.valid[tile_no % kValidRing];
-        const int key0 = j * kKeys;
         if (key0 + kKeys > all_see || valid != (1u << kGroups) - 1) {
 #pragma unroll
           for (int i = 0; i < kKeys; ++i)
@@ -470,6 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kRawStages> raw;
     Ring<kTileStages> st;
     uint32_t empty_parity = 1;  // a fresh barrier passes for the phase before
+    const int t8 = lane & 7, b4 = lane >> 3;
+    const int kc = L::k_codes(t8, b4), vc = L::v_codes(t8, b4) - L::v_codes(0, 0);
+    const int ks_at = L::k_scale(t8, b4), vs_at = L::v_scale(t8 & 6, b4);
+    // bytes of the scale words that belong to tokens t8 and t8 + 8
+    const uint32_t ks_pick = (ks_at & 3) | (((ks_at & 3) + L::kPer) << 4) | 0x4400;
+    const uint32_t vs_pick = (t8 & 1) | (((t8 & 1) + 2) << 4) | 0x4400;
+    const uint32_t row0 = (dw * kGroup + t8) * 128, chunk0 = ((b4 * 2) ^ t8) << 4;
     uint32_t tile_no = 0;
     bool ok = true;
     for (unsigned long long x = x0; x < x1 && ok;) {
@@ -479,50 +487,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         ok = wait(&sm.raw_full[raw.i], raw.parity);
         if (!ok) break;
-        // warp dw takes group dw of the tile: lane = token of a half (8) x block of 4
+        // Warp dw takes group dw of the tile; a lane the tokens t8 and t8 + 8 of it and block
+        // b4 of every four.  The scales of both tokens lie in one word.
         const uint8_t* g = sm.raw[raw.i] + dw * L::kGroupBytes;
         const bool here = sm.valid[tile_no % kValidRing] >> dw & 1;
         const int left = here ? p.q.kv - j * kKeys - dw * kGroup : 0;  // tokens of the group
-        const int t8 = lane & 7;
-        auto put = [&](uint8_t* tile, int i, int b, uint2 codes, uint32_t scale) {
-          const uint32_t h = e4m3x2_to_f16x2(scale);
-          const uint32_t s2 = __byte_perm(h, 0, 0x1010);
+        auto put = [&](uint8_t* at, uint2 codes, uint32_t s2) {
           uint32_t lo[4], hi[4];
           e2m1x8_to_f16(codes.x, lo);
           e2m1x8_to_f16(codes.y, hi);
 #pragma unroll
           for (int q = 0; q < 4; ++q) lo[q] = mul_f16x2(lo[q], s2), hi[q] = mul_f16x2(hi[q], s2);
-          const uint32_t key = dw * kGroup + i;
-          uint8_t* at = tile + (b >> 2) * (kKeys * 128) + key * 128;
-          const uint32_t chunk = (b & 3) * 2, x7 = key & 7;
-          *reinterpret_cast<uint4*>(at + ((chunk ^ x7) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<uint4*>(at + (((chunk + 1) ^ x7) << 4)) =
-              make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(at + chunk0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(at + (chunk0 ^ 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         };
+        uint2 codes[2][D / 64];
+        uint32_t scales[D / 64];
+#pragma unroll
+        for (int bb = 0; bb < D / 64; ++bb) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::k_codes(half * 8, bb * 4) + kc);
+          scales[bb] = *reinterpret_cast<const uint32_t*>(g + (ks_at & ~3) + bb * 8);
+        }
         ok = wait(&sm.k_empty[st.i], empty_parity);
         if (!ok) break;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int bb = 0; bb < D / 64; ++bb) {
+          const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, ks_pick));
 #pragma unroll
-          for (int bb = 0; bb < D / 64; ++bb) {
-            const int i = half * 8 + t8, b = bb * 4 + (lane >> 3);
-            put(sm.k[st.i], i, b, *reinterpret_cast<const uint2*>(g + L::k_codes(i, b)),
-                g[L::k_scale(i, b)]);
-          }
+          for (int half = 0; half < 2; ++half)
+            put(sm.k[st.i] + row0 + half * 1024 + bb * (kKeys * 128), codes[half][bb],
+                __byte_perm(h, 0, half ? 0x3232 : 0x1010));
+        }
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.k_full[st.i]);
+#pragma unroll
+        for (int bb = 0; bb < D / 64; ++bb) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::v_codes(half * 8, bb * 4) + vc);
+          scales[bb] = *reinterpret_cast<const uint32_t*>(g + vs_at + bb * 64);
+        }
         ok = wait(&sm.v_empty[st.i], empty_parity);
         if (!ok) break;
+        // what lies past the request's length may be anything: its scale becomes 0
+        const uint32_t keep = (t8 < left ? 0x00ffu : 0u) | (t8 + 8 < left ? 0xff00u : 0u);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int bb = 0; bb < D / 64; ++bb) {
+          const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, vs_pick) & keep);
 #pragma unroll
-          for (int bb = 0; bb < D / 64; ++bb) {
-            const int i = half * 8 + t8, b = bb * 4 + (lane >> 3);
-            // what lies past the request's length may be anything: its scale becomes 0
-            put(sm.v[st.i], i, b, *reinterpret_cast<const uint2*>(g + L::v_codes(i, b)),
-                i < left ? g[L::v_scale(i, b)] : 0u);
-          }
+          for (int half = 0; half < 2; ++half)
+            put(sm.v[st.i] + row0 + half * 1024 + bb * (kKeys * 128), codes[half][bb],
+                __byte_perm(h, 0, half ? 0x3232 : 0x1010));
+        }
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
