@@ -763,6 +763,8 @@ kda_status_t kda_cache_read(const kda_cache_t* cache, int32_t io_dtype, int32_t 
  *   lse           device, [total_tokens, num_heads] fp32 or NULL: natural log of
  *                 the sum of exp(scale q . k_j)
  *
+ * total_tokens * num_heads / num_kv_heads < 2^31 (else KDA_ERR_UNSUPPORTED).
+ *
  * desc->max_new is the largest n_b that the caller expects: it sizes the
  * workspace and the launches (a larger n_b gives the same results, slower).
  * Checked on the device: a request whose cu_new or kv_lens is out of range is

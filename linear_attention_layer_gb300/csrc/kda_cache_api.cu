@@ -43,7 +43,8 @@ kda_status_t check_attention(const kda_cache_t* cache, const kda_attention_t* d)
       d->max_blocks < 0 || !known_dtype(d->io_dtype) || !isfinite(d->scale))
     return KDA_ERR_INVALID_ARGUMENT;
   if (d->num_heads % cache->num_kv_heads != 0) return KDA_ERR_INVALID_ARGUMENT;
-  if (d->num_heads / cache->num_kv_heads > 1024) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)d->total_tokens * (d->num_heads / cache->num_kv_heads) > INT32_MAX)
+    return KDA_ERR_UNSUPPORTED;  // rows of one kv head
   if ((d->q_strides[0] == 0) != (d->q_strides[1] == 0)) return KDA_ERR_INVALID_ARGUMENT;
   return KDA_OK;
 }

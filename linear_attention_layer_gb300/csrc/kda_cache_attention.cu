@@ -44,9 +44,9 @@ constexpr int kMaxSeqs = 1024;                   // requests of one launch (thei
 
 // What a launch leaves in the workspace.
 struct Parts {
-  unsigned long long* plan;  // [nseq + 1] tiles before each request, then tiles per warp
-  float* o;                  // [slots][rows][D]
-  float2* ml;                // [slots][rows]
+  OpenUnit* open;  // [ctas]
+  float* o;        // [slots][rows][D]
+  float2* ml;      // [slots][rows]
 };
 
 // Slots: two per warp (part that starts inside its unit, part that starts it but
@@ -68,15 +68,15 @@ struct Cursor {
   int h;  // kv head
   int r;  // row tile
   int tile;
-  int tiles;   // of the unit
-  int64_t rt;  // row tiles of the request
+  int tiles;  // of the unit
+  int rt;     // row tiles of the request
   Request q;
 
   __device__ __forceinline__ bool load(const View& c, const AttentionArgs& a, int seq0,
                                        const RowRange& range, int rows_per_tile) {
     const bool live = load_request(c, a, seq0 + b, range, false, q);
     tiles = tiles_of(q);
-    rt = (q.rows + rows_per_tile - 1) / rows_per_tile;
+    rt = (int)((q.rows + rows_per_tile - 1) / rows_per_tile);
     return live;
   }
   __device__ __forceinline__ void seek(const View& c, const AttentionArgs& a, int seq0, int nseq,
@@ -85,10 +85,17 @@ struct Cursor {
     b = find_last(plan, nseq, x);
     load(c, a, seq0, range, rows_per_tile);
     const unsigned long long off = x - plan[b];
-    const unsigned long long u = off / tiles;
-    tile = (int)(off - u * tiles);
-    h = (int)(u / rt);
-    r = (int)(u - (unsigned long long)h * rt);
+    if (off >> 32 == 0) {
+      const uint32_t u = (uint32_t)off / (uint32_t)tiles;
+      tile = (int)((uint32_t)off - u * tiles);
+      h = (int)(u / (uint32_t)rt);
+      r = (int)(u - (uint32_t)h * (uint32_t)rt);
+    } else {
+      const unsigned long long u = off / tiles;
+      tile = (int)(off - u * tiles);
+      h = (int)(u / rt);
+      r = (int)(u - (unsigned long long)h * rt);
+    }
   }
   // The next tile; returns true when it starts a new unit.  Not past the last one.
   __device__ __forceinline__ bool next(const View& c, const AttentionArgs& a, int seq0, int nseq,
@@ -143,6 +150,12 @@ struct Smem {
   uint64_t full[WARPS][STAGES];
   uint32_t valid[WARPS][STAGES];
   unsigned long long sums[WARPS];
+  // Units that several warps have: [0] the one that enters the CTA, [1 + w] the one that
+  // warp w starts and does not end.  last: the last warp of the launch that has some of it.
+  struct Job {
+    int bos, row0, rows, head;
+    unsigned long long last;
+  } job[WARPS + 1];
 };
 
 template <typename T, int D, int NT, int WARPS, int STAGES, int CTAS>
@@ -165,6 +178,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   const int GP = c.page_size / kGroup;
 
   // ---- the plan: tiles before each request ----
+  if (tid <= WARPS) sm.job[tid].rows = 0;
   if (lane == 0) {
     for (int s = 0; s < STAGES; ++s) tc::mbar_init(&sm.full[warp][s], kTileGroups);
     tc::mbar_fence_init();
@@ -201,10 +215,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   const unsigned long long total = sm.plan[nseq];
   const unsigned long long workers = (unsigned long long)gridDim.x * WARPS;
   const unsigned long long per = (total + workers - 1) / workers;
-  if (blockIdx.x == 0) {
-    for (int i = tid; i <= nseq; i += WARPS * 32) parts.plan[i] = sm.plan[i];
-    if (tid == 0) parts.plan[nseq + 1] = per;
-  }
+  let_next_start();
   const int worker = blockIdx.x * WARPS + warp;
   const unsigned long long x0 = min(per * worker, total), x1 = min(x0 + per, total);
   const Shape shape{(int)gridDim.x, WARPS};
@@ -213,6 +224,13 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
     Cursor ld, cp;
     cp.seek(c, a, seq0, nseq, range, ROWS, sm.plan, x0);
     ld = cp;
+    auto open_job = [&](int i, unsigned long long end) {
+      const int64_t row0 = (int64_t)cp.r * ROWS;
+      if (lane == 0)
+        sm.job[i] = {cp.q.bos, (int)row0, (int)min(cp.q.rows - row0, (int64_t)ROWS), cp.h,
+                     (end - 1) / per};
+    };
+    if (warp == 0 && cp.tile > 0) open_job(0, x0 + (cp.tiles - cp.tile));
     const int count = (int)min(x1 - x0, (unsigned long long)INT32_MAX);
     int issued = 0;
     // Lane i holds the place of group 32 n + i of ld's unit, for the n being loaded, and issues
@@ -618,6 +636,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
           for (int wd = 0; wd < D / 64; ++wd) value_word(v, vs[u], u, wd);
         }
         end_part(ends_unit);
+        if (!ends_unit && seg_tile == 0)
+          open_job(1 + warp, x1 + (cp.tiles - cp.tile - 1));
         if (more) {
           cp.next(c, a, seq0, nseq, range, ROWS);
           start_unit();
@@ -638,117 +658,37 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
 
   // ---- join the parts of units that several warps of this CTA had ----
   __syncthreads();
-  const unsigned long long c0 = min(per * WARPS * blockIdx.x, total),
-                           c1 = min(c0 + per * WARPS, total);
-  // Warp w takes the unit that its own tail starts; warp 0 also the one that enters the CTA.
-  for (int job = warp == 0 ? 0 : 1; job < 2; ++job) {
-    const unsigned long long w0 = min(c0 + per * warp, total), w1 = min(w0 + per, total);
-    if (w0 >= w1) break;
-    Cursor cu;
-    unsigned long long u0, u1;
-    cu.seek(c, a, seq0, nseq, range, ROWS, sm.plan, job == 0 ? w0 : w1 - 1);
-    u0 = (job == 0 ? w0 : w1 - 1) - cu.tile;
-    u1 = u0 + cu.tiles;
-    if (job == 0 ? u0 == w0 : (u0 < w0 || u1 <= w1)) continue;  // no such unit
-    const bool starts = u0 >= c0, ends = u1 <= c1;
-    const unsigned long long p0 = max(u0, c0), p1 = min(u1, c1);
-    const int first = (int)((p0 - c0) / per), last = (int)((p1 - 1 - c0) / per);
-    const int64_t row0 = (int64_t)cu.r * ROWS;
-    const int rows = (int)min((int64_t)cu.q.n * group - row0, (int64_t)ROWS);
-    const float post = exponent_scale(c.v_exp, cu.h, 1);
-    for (int row = 0; row < rows; ++row) {
-      float top = -INFINITY;
-      for (int w = first; w <= last; ++w) {
-        const int slot = 2 * (blockIdx.x * WARPS + w) + (w == first && starts ? 1 : 0);
-        top = fmaxf(top, parts.ml[(int64_t)slot * ROWS + row].x);
-      }
-      float sum = 0.f, x[D / 32] = {};
-      for (int w = first; w <= last; ++w) {
-        const int slot = 2 * (blockIdx.x * WARPS + w) + (w == first && starts ? 1 : 0);
-        const int64_t at = (int64_t)slot * ROWS + row;
-        const float2 ml = parts.ml[at];
-        const float k = top == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-        sum = fmaf(ml.y, k, sum);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) x[i] = fmaf(parts.o[at * D + i * 32 + lane], k, x[i]);
-      }
+  const int w0 = blockIdx.x * WARPS;
+  if (tid == 0) parts.open[blockIdx.x].last = -1;
+  __syncthreads();
+  for (int j = 0; j <= WARPS; ++j) {
+    const auto job = sm.job[j];
+    if (job.rows == 0) continue;
+    const bool starts = j > 0, ends = job.last < w0 + WARPS;
+    const int first = w0 + (starts ? j - 1 : 0);
+    const int last = (int)min(job.last, (unsigned long long)(w0 + WARPS - 1));
+    if (starts && !ends && tid == 0)
+      parts.open[blockIdx.x] = {job.bos, job.row0, job.rows, job.head, (int)(job.last / WARPS)};
+    for (int row = warp; row < job.rows; row += WARPS) {
+      RowSum<D> sum;
+      sum.add(parts.o, parts.ml, first, last, [&](int w) {
+        return (int64_t)(2 * w + (starts && w == first ? 1 : 0)) * ROWS + row;
+      });
       if (starts && ends) {
-        const float inv = sum == 0.f ? 0.f : post / sum;
-        const int64_t rr = row0 + row;
-        const int64_t at = (cu.q.bos + rr / group) * a.num_heads + cu.h * group + rr % group;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          IO<T>::st(static_cast<T*>(a.out) + at * D + i * 32 + lane, x[i] * inv);
-        if (a.lse && lane == 0)
-          a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        const int rr = job.row0 + row;
+        const int64_t at = (int64_t)(job.bos + rr / group) * a.num_heads + job.head * group +
+                           rr % group;
+        sum.store(static_cast<T*>(a.out), a.lse, at, exponent_scale(c.v_exp, job.head, 1));
       } else {
-        const int slot = shape.warp_slots() + 2 * blockIdx.x + (starts ? 1 : 0);
-        const int64_t at = (int64_t)slot * ROWS + row;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) parts.o[at * D + i * 32 + lane] = x[i];
-        if (lane == 0) parts.ml[at] = make_float2(top, sum);
+        sum.store_part(parts.o, parts.ml,
+                       (int64_t)(shape.warp_slots() + 2 * blockIdx.x + (starts ? 1 : 0)) * ROWS +
+                           row);
       }
     }
   }
 }
 
-// Joins the parts of units that several CTAs had: one warp per row.
-template <typename T, int D, int ROWS, int WARPS>
-__global__ void __launch_bounds__(128)
-    join_kernel(View c, AttentionArgs a, int seq0, int nseq, RowRange range, Parts parts,
-                Shape shape) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int group = a.num_heads / c.kv_heads;
-  const int64_t tok = w / a.num_heads;
-  const int hq = (int)(w - tok * a.num_heads);
-  const int32_t* cu = a.cu_new + seq0;
-  if (tok >= a.total_tokens || tok < cu[0] || tok >= cu[nseq]) return;
-  const int b = find_last(cu, nseq, (unsigned long long)tok);
-  Request q;
-  if (!load_request(c, a, seq0 + b, range, false, q) || tok < q.bos || tok >= q.bos + q.n) return;
-  const int tiles = tiles_of(q);
-  const int64_t rt = (q.rows + ROWS - 1) / ROWS;
-  const unsigned long long per = parts.plan[nseq + 1] * WARPS;
-  const int h = hq / group;
-  const int64_t rr = (tok - q.bos) * group + hq % group;
-  const unsigned long long u0 =
-      parts.plan[b] + (unsigned long long)(h * rt + rr / ROWS) * tiles;
-  const int first = (int)(u0 / per), last = (int)((u0 + tiles - 1) / per);
-  if (first == last) return;
-  const int row = (int)(rr % ROWS);
-  auto at_of = [&](int cta) {
-    return (int64_t)(shape.warp_slots() + 2 * cta + (cta == first ? 1 : 0)) * ROWS + row;
-  };
-  float top = -INFINITY;
-  for (int i = first + lane; i <= last; i += 32) top = fmaxf(top, parts.ml[at_of(i)].x);
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  float sum = 0.f, x[D / 32] = {};
-#pragma unroll 4
-  for (int i = first; i <= last; ++i) {
-    const int64_t at = at_of(i);
-    const float2 ml = parts.ml[at];
-    const float k = top == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-    sum = fmaf(ml.y, k, sum);
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) x[j] = fmaf(parts.o[at * D + j * 32 + lane], k, x[j]);
-  }
-  const float inv = sum == 0.f ? 0.f : exponent_scale(c.v_exp, h, 1) / sum;
-  T* out = static_cast<T*>(a.out) + w * D;
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) IO<T>::st(out + j * 32 + lane, x[j] * inv);
-  if (a.lse && lane == 0) a.lse[w] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
-constexpr size_t kPlanBytes = ((kMaxSeqs + 2) * 8 + 255) / 256 * 256;
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // One CTA of `WARPS` warps with `STAGES` tiles in flight each, `CTAS` per SM.
 template <typename T, int D, int NT, int WARPS, int STAGES, int CTAS>
@@ -757,7 +697,7 @@ struct Split {
   static Shape shape() { return Shape{sm_count() * CTAS, WARPS}; }
   static size_t workspace() {
     const size_t slots = shape().slots();
-    return kPlanBytes + slots * ROWS * (D * 4 + 8);
+    return up256(shape().ctas * sizeof(OpenUnit)) + slots * ROWS * (D * 4 + 8);
   }
   static cudaError_t launch(const View& c, const AttentionArgs& a, const RowRange& range,
                             cudaStream_t st) {
@@ -772,21 +712,18 @@ struct Split {
     const Shape sh = shape();
     Parts parts;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    parts.plan = reinterpret_cast<unsigned long long*>(ws);
-    parts.o = reinterpret_cast<float*>(ws + kPlanBytes);
+    parts.open = reinterpret_cast<OpenUnit*>(ws);
+    parts.o = reinterpret_cast<float*>(ws + up256(sh.ctas * sizeof(OpenUnit)));
     parts.ml = reinterpret_cast<float2*>(parts.o + (size_t)sh.slots() * ROWS * D);
     const int64_t es = sizeof(T);
     const int q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 &&
                       a.q_token_stride * es % 16 == 0 && a.q_head_stride * es % 16 == 0;
-    const int64_t rows = (int64_t)a.total_tokens * a.num_heads;
     for (int seq0 = 0; seq0 < a.num_seqs; seq0 += kMaxSeqs) {
       const int nseq = std::min(kMaxSeqs, a.num_seqs - seq0);
       kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, seq0, nseq, range, parts, q_vec);
-      e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-      join_kernel<T, D, ROWS, WARPS>
-          <<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(c, a, seq0, nseq, range, parts, sh);
-      e = cudaGetLastError();
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch_join<T, D, 1>(c, a, parts.open, parts.o, parts.ml, sh.warp_slots(), ROWS, sh.ctas,
+                               st);
       if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -88,5 +88,165 @@ __device__ __forceinline__ RowScale row_scale(float top, float scale, float k_fa
   return r;
 }
 
+// One row of a unit put together from parts i = first .. last, whose (m, l, o[D]) lie at
+// index at(i) of ml and o: by one warp, each lane with D / 32 neighbouring channels.  The
+// loads do not wait for one another.
+template <int D>
+struct RowSum {
+  float top = -INFINITY, sum = 0.f, x[D / 32] = {};
+
+  template <typename At>
+  __device__ __forceinline__ void add(const float* o, const float2* ml, int first, int last,
+                                      At at) {
+    const int lane = threadIdx.x & 31;
+    for (int base = first; base <= last; base += 32) {
+      const int n = min(32, last - base + 1);
+      const float2 mine = lane < n ? ml[at(base + lane)] : make_float2(-INFINITY, 0.f);
+      float next = fmaxf(top, mine.x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, s));
+      const float keep = next == -INFINITY ? 1.f : ex2_approx(top - next);
+      const float k = next == -INFINITY ? 1.f : ex2_approx(mine.x - next);
+      top = next;
+      sum = fmaf(sum, keep, warp_sum(k * mine.y));
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[j] *= keep;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xffffffffu, k, i);
+        float y[D / 32];
+        load(o + at(base + i) * D, y);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) x[j] = fmaf(y[j], w, x[j]);
+      }
+    }
+  }
+  __device__ __forceinline__ static void load(const float* p, float (&y)[D / 32]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (D == 128) {
+      const float4 v = *reinterpret_cast<const float4*>(p + 4 * lane);
+      y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p + 2 * lane);
+      y[0] = v.x, y[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void store_part(float* o, float2* ml, int64_t at) const {
+    const int lane = threadIdx.x & 31;
+    if constexpr (D == 128)
+      *reinterpret_cast<float4*>(o + at * D + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+      *reinterpret_cast<float2*>(o + at * D + 2 * lane) = make_float2(x[0], x[1]);
+    if (lane == 0) ml[at] = make_float2(top, sum);
+  }
+  // The finished row; v_factor is the head's power of two of the values.
+  template <typename T>
+  __device__ __forceinline__ void store(T* out, float* lse, int64_t at, float v_factor) const {
+    const int lane = threadIdx.x & 31;
+    const float inv = sum == 0.f ? 0.f : v_factor / sum;
+    T* p = out + at * D + lane * (D / 32);
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[D / 64];
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) w[j] = tc::pack_bf16(x[2 * j] * inv, x[2 * j + 1] * inv);
+      if constexpr (D == 128)
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+      if constexpr (D == 128)
+        *reinterpret_cast<float4*>(p) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      else
+        *reinterpret_cast<float2*>(p) = make_float2(x[0] * inv, x[1] * inv);
+    }
+    if (lse && lane == 0) lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+};
+
+// A unit that the CTA of this index starts and that CTAs up to `last` carry on (-1: none).
+struct OpenUnit {
+  int bos;   // first new token of its request
+  int row0;  // its first row among the request's (fits: rows of one request < 2^31, checked)
+  int rows;
+  int head;  // kv head
+  int last;
+};
+
+// Programmatic dependent launch: a kernel lets the next one's CTAs start, which wait here
+// until the memory of the one before is complete.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Joins open units: a CTA has PER rows of one, WPR = 4 / PER warps a row.
+template <typename T, int D, int PER>
+__global__ void __launch_bounds__(128)
+    join_kernel(View c, AttentionArgs a, const OpenUnit* units, const float* o, const float2* ml,
+                int slot0, int unit_rows) {
+  constexpr int WPR = 4 / PER;
+  __shared__ RowSum<D> shared_sum[WPR > 1 ? 4 : 1][WPR > 1 ? 32 : 1];
+  wait_for_previous();
+  const int first = blockIdx.x;
+  const OpenUnit u = units[first];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (u.last < 0 || blockIdx.y * PER >= u.rows) return;
+  const int row = blockIdx.y * PER + warp / WPR, part = warp % WPR;
+  const int per = (u.last - first + WPR) / WPR;
+  const int p0 = first + part * per, p1 = min(u.last, p0 + per - 1);
+  RowSum<D> r;
+  if (row < u.rows)
+    r.add(o, ml, p0, p1, [&](int i) {
+      return (int64_t)(slot0 + 2 * i + (i == first ? 1 : 0)) * unit_rows + row;
+    });
+  if constexpr (WPR > 1) {
+    shared_sum[warp][lane] = r;
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      const RowSum<D>& s = shared_sum[warp + w][lane];
+      const float next = fmaxf(r.top, s.top);
+      const float k0 = next == -INFINITY ? 1.f : ex2_approx(r.top - next);
+      const float k1 = next == -INFINITY ? 1.f : ex2_approx(s.top - next);
+      r.top = next;
+      r.sum = r.sum * k0 + s.sum * k1;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) r.x[j] = r.x[j] * k0 + s.x[j] * k1;
+    }
+  }
+  if (row >= u.rows) return;
+  const int group = a.num_heads / c.kv_heads;
+  const int rr = u.row0 + row;
+  const int64_t at = (int64_t)(u.bos + rr / group) * a.num_heads + u.head * group + rr % group;
+  r.store(static_cast<T*>(a.out), a.lse, at, exponent_scale(c.v_exp, u.head, 1));
+}
+
+// Launches it right behind the kernel whose units it joins.
+template <typename T, int D, int PER>
+cudaError_t launch_join(const View& c, const AttentionArgs& a, const OpenUnit* units,
+                        const float* o, const float2* ml, int slot0, int unit_rows, int ctas,
+                        cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, unit_rows / PER);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, PER>, c, a, units, o, ml, slot0, unit_rows);
+}
+
+inline int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
 }  // namespace cache
 }  // namespace kda

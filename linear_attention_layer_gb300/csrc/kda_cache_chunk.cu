@@ -53,6 +53,7 @@ struct Plan {
   unsigned long long* tiles;  // [entries + 1] tiles before each entry (request, row unit)
   int2* entry;                // request, row unit
   int* first;                 // [num_seqs + 1] first entry of each request
+  OpenUnit* open;             // [ctas]
   float* o;                   // [2 * ctas][kRows][D]
   float2* ml;                 // [2 * ctas][kRows]
 };
@@ -228,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
+  let_next_start();
+  if (tid == 0) plan.open[blockIdx.x].last = -1;
   const int entries = plan.first[a.num_seqs];
   const unsigned long long total = entries ? plan.tiles[entries] : 0;
   const unsigned long long per = (total + gridDim.x - 1) / gridDim.x;
@@ -457,6 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
+      if (tid == 0 && p.begin == 0 && !whole)
+        plan.open[blockIdx.x] = {p.q.bos, p.r * kRows, rows, p.h,
+                                 (int)((x + (p.tiles - p.end) - 1) / per)};
       if (live) {
         if (!whole)
           plan.ml[part_at] = make_float2(m, l);
@@ -676,62 +682,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 12) tc::tmem_dealloc(tmem, kCols);
 }
 
-// Joins the parts of units that several CTAs had: one warp per row.
-template <int D>
-__global__ void __launch_bounds__(128)
-    chunk_join_kernel(View c, AttentionArgs a, RowRange range, Plan plan, int ctas) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int group = a.num_heads / c.kv_heads;
-  const int64_t tok = w / a.num_heads;
-  const int hq = (int)(w - tok * a.num_heads);
-  if (tok >= a.total_tokens || tok < a.cu_new[0] || tok >= a.cu_new[a.num_seqs]) return;
-  const int b = find_last(a.cu_new, a.num_seqs, (unsigned long long)tok);
-  Request q;
-  if (!load_request(c, a, b, range, false, q) || tok < q.bos || tok >= q.bos + q.n) return;
-  const int entries = plan.first[a.num_seqs];
-  const unsigned long long total = plan.tiles[entries];
-  const unsigned long long per = (total + ctas - 1) / ctas;
-  const int h = hq / group;
-  const int64_t rr = (tok - q.bos) * group + hq % group;
-  const int r = (int)(rr / kRows), row = (int)(rr % kRows);
-  const int e = plan.first[b] + r;
-  if (e >= entries) return;
-  const int tiles = unit_tiles(q, group, r);
-  const unsigned long long u0 = plan.tiles[e] + (unsigned long long)h * tiles;
-  const int first = (int)(u0 / per), last = (int)((u0 + tiles - 1) / per);
-  if (first == last) return;
-  auto at_of = [&](int cta) {
-    return (int64_t)(2 * cta + (cta == first ? 1 : 0)) * kRows + row;
-  };
-  float top = -INFINITY;
-  for (int i = first + lane; i <= last; i += 32) top = fmaxf(top, plan.ml[at_of(i)].x);
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  float sum = 0.f, x[D / 32] = {};
-#pragma unroll 2
-  for (int i = first; i <= last; ++i) {
-    const int64_t at = at_of(i);
-    const float2 ml = plan.ml[at];
-    const float k = top == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-    sum = fmaf(ml.y, k, sum);
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) x[j] = fmaf(plan.o[at * D + j * 32 + lane], k, x[j]);
-  }
-  const float inv = sum == 0.f ? 0.f : exponent_scale(c.v_exp, h, 1) / sum;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + w * D;
-#pragma unroll
-  for (int j = 0; j < D / 32; ++j) out[j * 32 + lane] = __float2bfloat16_rn(x[j] * inv);
-  if (a.lse && lane == 0) a.lse[w] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Entries that well-formed offsets can ask for: a unit of rows each, one more per request.
@@ -753,6 +703,7 @@ size_t layout(const View& c, const AttentionArgs& a, uint8_t* ws, Plan* plan) {
   p.tiles = reinterpret_cast<unsigned long long*>(take((n + 1) * 8));
   p.entry = reinterpret_cast<int2*>(take((n + 1) * 8));
   p.first = reinterpret_cast<int*>(take(((size_t)a.num_seqs + 1) * 4));
+  p.open = reinterpret_cast<OpenUnit*>(take(slots / 2 * sizeof(OpenUnit)));
   p.o = reinterpret_cast<float*>(take(slots * kRows * D * 4));
   p.ml = reinterpret_cast<float2*>(take(slots * kRows * 8));
   if (plan) *plan = p;
@@ -777,9 +728,7 @@ cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cu
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   chunk_kernel<D><<<ctas, kThreads, kSmem, st>>>(c, a, range, plan, q_vec);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.total_tokens * a.num_heads;
-  chunk_join_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(c, a, range, plan, ctas);
-  return cudaGetLastError();
+  return launch_join<__nv_bfloat16, D, 4>(c, a, plan.open, plan.o, plan.ml, 0, kRows, ctas, st);
 }
 
 }  // namespace

@@ -146,6 +146,12 @@ def test_attention_refuses_descriptor(lib, over):
                                    None) == INVALID
 
 
+def test_attention_too_many_rows(lib):
+    d, n = _desc(total_tokens=1 << 30), ctypes.c_size_t(0)
+    assert lib.kda_cache_attention_workspace_size(ctypes.byref(_cache()), ctypes.byref(d),
+                                                  ctypes.byref(n)) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("args", [
     (None, FAKE, FAKE, FAKE, OUT, None), (FAKE, None, FAKE, FAKE, OUT, None),
     (FAKE, FAKE, None, FAKE, OUT, None), (FAKE, FAKE, FAKE, None, OUT, None),
