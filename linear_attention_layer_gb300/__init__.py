@@ -924,76 +924,35 @@ def cache_empty(num_pages, page_size, num_kv_heads, head_dim, device="cuda"):
                        dtype=torch.uint8, device=device)
 
 
-# The cache calls take microseconds on the GPU, and a decode step makes them once a layer: their
-# checks look at each tensor once and describe what is wrong only when something is.
+# Checks, outputs and the current stream are handled by a native binding
+# (csrc/cache_binding.cpp): a decode step makes these calls once a layer, and each takes the
+# GPU microseconds.
 
-def _bad(name, t, dtype, shape, device):
-    """Raises what is wrong with a tensor that a call's quick check refused."""
-    _check_tensor(name, t, dtype, shape, device)
-    raise ValueError(f"{name} must be {dtype} {tuple(shape)}, contiguous, on {device}")
+_binding = None
 
 
-def _need(name, t, dtype, shape, device):
-    if t is None or t.dtype != dtype or t.shape != shape or t.device != device or \
-            not t.is_contiguous():
-        _bad(name, t, dtype, shape, device)
-    return t.data_ptr()
+def _native():
+    """The native binding (raises if it has not been built)."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    import importlib.util
+    load()
+    path = os.path.join(os.path.dirname(LIB_PATH), "_cache_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"_cache_binding.so not found at {path}; build it with "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`")
+    spec = importlib.util.spec_from_file_location("_cache_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _binding = module
+    return module
 
 
-def _need_rows(name, t, dtype, shape, device):
-    """The same for [T, heads, channels] with strides; only the channels are contiguous."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or \
-            (t.stride(2) != 1 and t.numel()):
-        if t.device == device and t.dtype == dtype and t.shape == shape:
-            raise ValueError(f"{name}'s channels must be contiguous")
-        _bad(name, t, dtype, shape, device)
-    return t.data_ptr()
-
-
-def _cuda_only(name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
-    return t.device
-
-
-class _Launch:
-    """Makes ``device`` current for a call and its allocations, which belong to the stream
-    that the call runs on."""
-    __slots__ = ("handle", "device", "stream")
-
-    def __init__(self, device, stream):
-        self.device = None if device.index == torch.cuda.current_device() else \
-            torch.cuda.device(device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
-        self.handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
-            stream.cuda_stream
-
-    def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
-
-
-def _cache_struct(cache, k_exponent, v_exponent, device):
-    """The kda_cache_t of a cache tensor."""
-    shape = cache.shape
-    if len(shape) != 4 or shape[3] % 18:
-        raise ValueError("cache must be uint8 [num_pages, kv heads, page_size / 16, 18 head_dim], "
-                         f"got {tuple(shape)}")
-    heads = (shape[1],)
-    return KdaCache(
-        _need("cache", cache, torch.uint8, shape, device), shape[0], shape[2] * 16, shape[1],
-        shape[3] // 18,
-        None if k_exponent is None else _need("k_exponent", k_exponent, torch.int32, heads, device),
-        None if v_exponent is None else _need("v_exponent", v_exponent, torch.int32, heads, device))
+def _outputs(result, where):
+    if result.__class__ is int:
+        raise KDAError(result, where)
+    return result
 
 
 def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_range, *,
@@ -1006,56 +965,24 @@ def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_ra
     free_range int64 [2].  Returns (kv_lens [B], cu_new [B + 1], slots
     [max_tokens], free_range_out [2]); kv_lens may be held_lens or seq_lens and
     free_range_out may be free_range, for a loop that updates in place."""
-    lib = load()
-    dev = _cuda_only("held_lens", held_lens)
-    B = held_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    blocks, ring = block_table.shape[1], free_pages.numel()
-    lens, i32, i64 = (B,), torch.int32, torch.int64
-    max_tokens = int(max_tokens)
-    if max_tokens < 0:
-        raise ValueError(f"max_tokens must not be negative, got {max_tokens}")
-    with _Launch(dev, stream) as handle:
-        if kv_lens is None:
-            kv_lens = torch.empty(B, dtype=i32, device=dev)
-        if cu_new is None:
-            cu_new = torch.empty(B + 1, dtype=i32, device=dev)
-        if slots is None:
-            slots = torch.empty(max_tokens, dtype=i64, device=dev)
-        if free_range_out is None:
-            free_range_out = torch.empty(2, dtype=i64, device=dev)
-        st = lib.kda_cache_tables(
-            int(page_size), B, blocks, max_tokens, ring,
-            _need("held_lens", held_lens, i32, lens, dev),
-            _need("seq_lens", seq_lens, i32, lens, dev),
-            _need("new_lens", new_lens, i32, lens, dev),
-            _need("block_table", block_table, i32, (B, blocks), dev),
-            _need("free_pages", free_pages, i32, (ring,), dev),
-            _need("free_range", free_range, i64, (2,), dev),
-            _need("free_range_out", free_range_out, i64, (2,), dev),
-            _need("kv_lens", kv_lens, i32, lens, dev), _need("cu_new", cu_new, i32, (B + 1,), dev),
-            _need("slots", slots, i64, (max_tokens,), dev), handle)
-    if st != KDA_OK:
-        raise KDAError(st, "kda_cache_tables")
-    return kv_lens, cu_new, slots, free_range_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_range,
+                                page_size=page_size, max_tokens=max_tokens, kv_lens=kv_lens,
+                                cu_new=cu_new, slots=slots, free_range_out=free_range_out)
+    return _outputs((_binding or _native()).tables(
+        held_lens, seq_lens, new_lens, block_table, free_pages, free_range, page_size, max_tokens,
+        kv_lens, cu_new, slots, free_range_out), "kda_cache_tables")
 
 
 def cache_append(k, v, slots, cache, *, k_exponent=None, v_exponent=None, stream=None):
     """``kda_cache_append``: quantise k, v [T, kv heads, head_dim] (fp32 or bf16;
     slices of a larger tensor will do, the channels contiguous) into ``cache`` at
     ``slots`` int64 [T] (-1 skips a token)."""
-    lib = load()
-    dev = _cuda_only("cache", cache)
-    c = _cache_struct(cache, k_exponent, v_exponent, dev)
-    T = slots.numel()
-    shape, dtype = (T, c.num_kv_heads, c.head_dim), k.dtype
-    io = _io_code(dtype)
-    kp, vp = _need_rows("k", k, dtype, shape, dev), _need_rows("v", v, dtype, shape, dev)
-    strides = (ctypes.c_int64 * 4)(k.stride(0), k.stride(1), v.stride(0), v.stride(1))
-    with _Launch(dev, stream) as handle:
-        st = lib.kda_cache_append(c, io, T, kp, vp, strides,
-                                  _need("slots", slots, torch.int64, (T,), dev), handle)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_append(k, v, slots, cache, k_exponent=k_exponent, v_exponent=v_exponent)
+    st = (_binding or _native()).append(k, v, slots, cache, k_exponent, v_exponent)
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_append")
 
@@ -1064,42 +991,32 @@ def cache_read(slots, cache, dtype=torch.bfloat16, *, k_exponent=None, v_exponen
                v=None, stream=None):
     """``kda_cache_read``: the values that ``cache`` holds at ``slots`` int64 [T], as
     (k, v) [T, kv heads, head_dim] of ``dtype`` (-1 reads as zeros)."""
-    lib = load()
-    dev = _cuda_only("cache", cache)
-    c = _cache_struct(cache, k_exponent, v_exponent, dev)
-    io = _io_code(dtype)
-    T = slots.numel()
-    shape = (T, c.num_kv_heads, c.head_dim)
-    with _Launch(dev, stream) as handle:
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=dtype, device=dev)
-        st = lib.kda_cache_read(c, io, T, _need("slots", slots, torch.int64, (T,), dev),
-                                _need("k", k, dtype, shape, dev),
-                                _need("v", v, dtype, shape, dev), handle)
-    if st != KDA_OK:
-        raise KDAError(st, "kda_cache_read")
-    return k, v
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_read(slots, cache, dtype, k_exponent=k_exponent, v_exponent=v_exponent,
+                              k=k, v=v)
+    return _outputs((_binding or _native()).read(
+        slots, cache, _io_code(dtype) == KDA_BF16, k_exponent, v_exponent, k, v),
+        "kda_cache_read")
 
 
 def cache_attention_workspace_size(cache, num_seqs, total_tokens, num_heads, max_new, max_blocks,
                                    dtype):
     """Bytes of device scratch that ``cache_attention`` needs for calls of this shape."""
-    dev = _cuda_only("cache", cache)
-    c = _cache_struct(cache, None, None, dev)
-    with _Launch(dev, None):
-        return _attention_workspace(c, KdaAttention(
-            int(num_seqs), int(total_tokens), int(num_heads), int(max_new), int(max_blocks),
-            _io_code(dtype), 1.0))
-
-
-def _attention_workspace(c, d):
+    _check_tensor("cache", cache, torch.uint8, cache.shape, cache.device)
+    if cache.dim() != 4 or cache.shape[3] % 18:
+        raise ValueError("cache must be uint8 [num_pages, kv heads, page_size / 16, 18 head_dim], "
+                         f"got {tuple(cache.shape)}")
+    c = KdaCache(cache.data_ptr(), cache.shape[0], cache.shape[2] * 16, cache.shape[1],
+                 cache.shape[3] // 18)
+    d = KdaAttention(int(num_seqs), int(total_tokens), int(num_heads), int(max_new),
+                     int(max_blocks), _io_code(dtype), 1.0)
     n = ctypes.c_size_t(0)
-    st = load().kda_cache_attention_workspace_size(c, d, ctypes.byref(n))
+    with torch.cuda.device(cache.device):
+        st = load().kda_cache_attention_workspace_size(c, d, ctypes.byref(n))
     if st != KDA_OK:
         raise KDAError(st, "kda_cache_attention_workspace_size")
-    return n.value
+    return int(n.value)
 
 
 def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=None,
@@ -1113,40 +1030,15 @@ def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=No
     head_dim ** -0.5.  Returns out [T, heads, head_dim], with ``return_lse`` also
     the log-sum-exp [T, heads] fp32.  ``workspace``: a uint8 tensor of
     ``cache_attention_workspace_size`` bytes or "auto" (allocated here)."""
-    lib = load()
-    dev = _cuda_only("cache", cache)
-    c = _cache_struct(cache, k_exponent, v_exponent, dev)
-    if q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q must be [T, heads, head_dim] and block_table [B, max_blocks]")
-    shape, dtype = q.shape, q.dtype
-    T, H, D = shape
-    B, blocks = kv_lens.numel(), block_table.shape[1]
-    if D != c.head_dim or H % c.num_kv_heads:
-        raise ValueError(f"q {tuple(shape)} does not fit a cache of {c.num_kv_heads} heads of "
-                         f"{c.head_dim} channels")
-    i32 = torch.int32
-    qp = _need_rows("q", q, dtype, shape, dev)
-    d = KdaAttention(B, T, H, int(max_new), blocks, _io_code(dtype),
-                     D ** -0.5 if scale is None else float(scale))
-    if not q.is_contiguous():
-        d.q_strides[0], d.q_strides[1] = q.stride(0), q.stride(1)
-    with _Launch(dev, stream) as handle:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        if lse is None and return_lse:
-            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        if isinstance(workspace, str):
-            if workspace != "auto":
-                raise ValueError("workspace must be a tensor or 'auto'")
-            workspace = torch.empty(_attention_workspace(c, d), dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            d.workspace_bytes = workspace.numel()
-            d.workspace = _need("workspace", workspace, torch.uint8, (d.workspace_bytes,), dev)
-        st = lib.kda_cache_attention(
-            c, d, qp, _need("block_table", block_table, i32, (B, blocks), dev),
-            _need("kv_lens", kv_lens, i32, (B,), dev), _need("cu_new", cu_new, i32, (B + 1,), dev),
-            _need("out", out, dtype, shape, dev),
-            None if lse is None else _need("lse", lse, torch.float32, (T, H), dev), handle)
-    if st != KDA_OK:
-        raise KDAError(st, "kda_cache_attention")
-    return (out, lse) if return_lse else out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_attention(q, cache, block_table, kv_lens, cu_new, max_new=max_new,
+                                   scale=scale, k_exponent=k_exponent, v_exponent=v_exponent,
+                                   out=out, return_lse=return_lse, lse=lse, workspace=workspace)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be a tensor or 'auto'")
+        workspace = None
+    return _outputs((_binding or _native()).attention(
+        q, cache, block_table, kv_lens, cu_new, max_new, scale, k_exponent, v_exponent, out, lse,
+        bool(return_lse), workspace), "kda_cache_attention")
