@@ -715,7 +715,7 @@ kda_status_t kda_cache_tables(int32_t page_size, int32_t num_seqs, int32_t max_b
  *   k, v       device, [num_tokens, num_kv_heads, head_dim] io dtype; the
  *              channels are contiguous, tokens and heads lie strides[0 .. 3]
  *              elements apart: k's token, k's head, v's token, v's head stride
- *              (NULL: packed).  Any alignment of the dtype; 16-byte aligned
+ *              (32 bits; NULL: packed).  Any alignment of the dtype; 16-byte aligned
  *              rows load faster.
  *   slots      device, [num_tokens] int64, no slot twice; -1 skips a token
  * A slot outside the cache is skipped and sets the device error word.  An

@@ -90,14 +90,17 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// E2M1 codes of (lo, hi), nearest with ties to even, saturating: one byte.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1(float lo, float hi) {
+// E2M1 codes of eight values, nearest with ties to even, saturating: one word.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&x)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 

@@ -136,6 +136,8 @@ kda_status_t kda_cache_append(const kda_cache_t* cache, int32_t io_dtype, int32_
     a.strides[i] = strides ? strides[i]
                    : i % 2 ? (int64_t)cache->head_dim
                            : (int64_t)cache->head_dim * cache->num_kv_heads;
+  for (int64_t x : a.strides)
+    if (x > INT32_MAX || x < INT32_MIN) return KDA_ERR_UNSUPPORTED;
   a.err = kda::device_error();
   if (!a.err) return KDA_ERR_CUDA;
   return status_of(kda::launch_cache_append(a, (cudaStream_t)stream));

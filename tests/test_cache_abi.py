@@ -80,6 +80,12 @@ def test_append_refuses(lib, args):
     assert lib.kda_cache_append(ctypes.byref(_cache()), *args, None) == INVALID
 
 
+def test_append_refuses_long_strides(lib):
+    strides = (ctypes.c_int64 * 4)(256, 128, 1 << 31, 128)
+    assert lib.kda_cache_append(ctypes.byref(_cache()), 1, 3, FAKE, FAKE, strides, FAKE,
+                                None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("args", [
     (7, 3, FAKE, FAKE, OUT), (1, -1, FAKE, FAKE, OUT), (1, 3, None, FAKE, OUT),
     (1, 3, FAKE, None, OUT), (1, 3, FAKE, OUT, None), (1, 3, FAKE, OUT, OUT),
