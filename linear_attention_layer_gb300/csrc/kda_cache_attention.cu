@@ -137,13 +137,7 @@ constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
 template <typename T, int D, int NT, int WARPS, int STAGES>
 struct Smem {
   static constexpr int kStage = kTileGroups * Layout<D>::kGroupBytes;
-#ifndef QT
-#define QT 2
-#define C1 4
-#define C2 3
-#define C3 3
-#endif
-  static constexpr bool kQueriesHere = NT * kTerms<T> > QT;  // else they stay in registers
+  static constexpr bool kQueriesHere = NT * kTerms<T> > 2;  // else they stay in registers
   alignas(128) uint8_t ring[WARPS][STAGES][kStage];
   uint2 q[kQueriesHere ? WARPS : 1][kQueriesHere ? NT * kTerms<T> * (D / 16) * 32 : 1];
   unsigned long long plan[kMaxSeqs + 1];
@@ -730,34 +724,30 @@ struct Split {
   }
 };
 
-// Calls f with the variant for the call's types and expected rows per kv head.
+// Calls f with the variant for the call's types and expected rows per kv head: tiles of 8
+// rows where those are enough, else of 16, more rows taking several passes over the keys
+// (the second finds them in L2).  67 windows of 1 to 5 tokens, 8 query heads on a kv head,
+// 128 channels: 8 rows 191 us, 16 rows 172, 24 rows 186, 32 rows 240 -- the larger tiles'
+// sums leave registers for too few warps.
 template <typename F>
 auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
-  const int64_t rows = (int64_t)a.max_new * (a.num_heads / c.kv_heads);
+  const bool few = (int64_t)a.max_new * (a.num_heads / c.kv_heads) <= 8;
   if (a.bf16) {
     using T = __nv_bfloat16;
-    if (a.head_dim == 128) {
-      if (rows <= 8) return f(Split<T, 128, 1, C1, C2, C3>{});
-      if (rows <= 16) return f(Split<T, 128, 2, 8, 4, 1>{});
-      return f(Split<T, 128, 4, 8, 4, 1>{});
-    }
-    if (rows <= 8) return f(Split<T, 64, 1, 8, 4, 2>{});
-    if (rows <= 16) return f(Split<T, 64, 2, 8, 4, 2>{});
-    return f(Split<T, 64, 4, 8, 4, 1>{});
+    if (a.head_dim == 128)
+      return few ? f(Split<T, 128, 1, 4, 3, 3>{}) : f(Split<T, 128, 2, 8, 4, 1>{});
+    return few ? f(Split<T, 64, 1, 8, 4, 2>{}) : f(Split<T, 64, 2, 8, 4, 1>{});
   }
-  if (a.head_dim == 128) {
-    if (rows <= 8) return f(Split<float, 128, 1, 8, 4, 1>{});
-    return f(Split<float, 128, 2, 8, 4, 1>{});
-  }
-  if (rows <= 8) return f(Split<float, 64, 1, 8, 4, 2>{});
-  return f(Split<float, 64, 2, 8, 4, 1>{});
+  if (a.head_dim == 128)
+    return few ? f(Split<float, 128, 1, 8, 4, 1>{}) : f(Split<float, 128, 2, 8, 4, 1>{});
+  return few ? f(Split<float, 64, 1, 8, 4, 2>{}) : f(Split<float, 64, 2, 8, 4, 1>{});
 }
 
 }  // namespace
 
 // Requests with more rows per kv head than this go to the chunk kernel, whose work for
 // a key is that of 256 rows whatever their number (measured: see kda_cache_chunk.cu).
-constexpr int64_t kSplitRows = 64;
+constexpr int64_t kSplitRows = 48;
 
 size_t cache_attention_workspace_bytes(const View& c, const AttentionArgs& a) {
   const size_t split = dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });

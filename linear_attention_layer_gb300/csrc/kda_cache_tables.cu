@@ -5,8 +5,9 @@
 // tokens, of the pages taken and of the pages given back.  They are few (a
 // thousand requests is one pass of one CTA), so one CTA does the sums and moves
 // the pages: what bounds it is the chain of dependent loads (lengths, ring,
-// table), not their number.  The slots, one per new token, are written by the
-// same CTA when they are few and by a second kernel over the whole GPU otherwise.
+// table) and the barriers, not their number, so the three sums go together.  The
+// slots, one per new token, are written by the same CTA when they are few and by a
+// second kernel over the whole GPU otherwise.
 #include <algorithm>
 
 #include "kda_common.cuh"
@@ -15,45 +16,56 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 512;
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int page) {
   return (int)((tokens + page - 1) / page);
 }
 
-// Inclusive sum over the CTA's threads; `total` gets the CTA's sum.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int64_t& total) {
+// Pages taken, pages given back and new tokens of a request, or their sums.
+struct Counts {
+  int64_t pages;   // taken in the low 32 bits, given back in the high ones: fewer than
+                   // 2^31 each, a pass moves no more than the tables have entries
+  int64_t tokens;
+  Counts() = default;
+  __device__ __forceinline__ Counts(int taken, int freed, int64_t t)
+      : pages((int64_t)((uint64_t)(uint32_t)freed << 32 | (uint32_t)taken)), tokens(t) {}
+  __device__ __forceinline__ int taken() const { return (int)(pages & 0xffffffff); }
+  __device__ __forceinline__ int freed() const { return (int)(pages >> 32); }
+};
+
+// Sums of the CTA's threads before this one; `total` gets the sum of all.
+__device__ __forceinline__ Counts block_scan(Counts x, Counts* warp_sums, Counts& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Counts mine = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int64_t p = __shfl_up_sync(0xffffffffu, x.pages, o);
+    const int64_t t = __shfl_up_sync(0xffffffffu, x.tokens, o);
+    if (lane >= o) x.pages += p, x.tokens += t;
   }
+  __syncthreads();  // the sums of the call before are read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int64_t s = warp_sums[lane];
+  Counts before(0, 0, 0);
+  total = before;
 #pragma unroll
-    for (int o = 1; o < kWarps; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const Counts s = warp_sums[w];
+    if (w < warp) before.pages += s.pages, before.tokens += s.tokens;
+    total.pages += s.pages, total.tokens += s.tokens;
   }
-  __syncthreads();
-  if (warp > 0) x += warp_sums[warp - 1];
-  total = warp_sums[kWarps - 1];
-  __syncthreads();
-  return x;
+  before.pages += x.pages - mine.pages;
+  before.tokens += x.tokens - mine.tokens;
+  return before;
 }
 
-// The request whose tokens hold packed token i (cu[0] = 0 <= i < cu[n]).
-__device__ __forceinline__ int request_of(const int32_t* cu, int n, int i) {
-  int lo = 0, hi = n;  // cu[lo] <= i < cu[hi]
+// The last index i < n with at[i] <= x (at[0] <= x).
+__device__ __forceinline__ int owner(const int32_t* at, int n, int x) {
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= i)
+    if (at[mid] <= x)
       lo = mid;
     else
       hi = mid;
@@ -61,10 +73,8 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int n, int i) {
   return lo;
 }
 
-// Slot of packed token i, whose request's first slot is in place (-1: refused).
-__device__ __forceinline__ int64_t slot_of(const TableArgs& a, int i) {
-  const int b = request_of(a.cu_new, a.num_seqs, i);
-  const int first = a.cu_new[b], n = a.cu_new[b + 1] - first;
+// Slot of packed token i of request b, whose first slot is in place (-1: refused).
+__device__ __forceinline__ int64_t slot_of(const TableArgs& a, int b, int i, int first, int n) {
   if (a.slots[first] < 0) return -1;
   const int pos = a.kv_lens[b] - n + (i - first);
   return (int64_t)a.block_table[(int64_t)b * a.max_blocks + pos / a.page_size] * a.page_size +
@@ -73,26 +83,15 @@ __device__ __forceinline__ int64_t slot_of(const TableArgs& a, int i) {
 
 // Requests of one pass of the CTA, for the page moves that follow their sums.
 struct Pass {
-  int32_t taken_at[kThreads + 1];  // pages taken before each request of the pass
-  int32_t freed_at[kThreads + 1];
-  int32_t from[kThreads];          // first column that changes
+  int32_t taken_at[kThreads];  // pages taken before each request of the pass
+  int32_t freed_at[kThreads];
+  int32_t from[kThreads];      // first column that changes
 };
 
-// The request of the pass that page i belongs to.
-__device__ __forceinline__ int owner(const int32_t* at, int n, int i) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (at[mid] <= i)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
+constexpr int kFew = 8;  // new tokens whose slots the request's own thread writes
 
 __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write_slots) {
-  __shared__ int64_t warp_sums[kWarps];
+  __shared__ Counts warp_sums[kThreads / 32];
   __shared__ Pass ps;
   const int P = a.page_size;
   int64_t head = a.free_range[0], tail = a.free_range[1];
@@ -102,64 +101,77 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write
     if (threadIdx.x == 0) report_error(a.err, kErrDeviceCheck);
   }
   const int64_t avail = tail - head;
+  const int64_t head0 = head % a.ring_size, tail0 = tail % a.ring_size;
+  auto in_ring = [&](int64_t at) {  // at < 2 ring_size as long as the ring does not run over
+    return at < a.ring_size ? at : at % a.ring_size;
+  };
   int64_t tokens = 0, asked = 0, taken = 0, freed = 0;  // of the requests before this pass
+  bool long_ones = false;
   for (int base = 0; base < a.num_seqs; base += kThreads) {
     const int b = base + threadIdx.x;
     const bool in = b < a.num_seqs;
-    const int64_t held = in ? a.held_lens[b] : 0, seq = in ? a.seq_lens[b] : 0;
-    const int64_t fresh = in ? a.new_lens[b] : 0;
+    const int held = in ? a.held_lens[b] : 0, seq = in ? a.seq_lens[b] : 0;
+    const int fresh = in ? a.new_lens[b] : 0;
     const bool sound = held >= 0 && seq >= 0 && seq <= held && fresh >= -1 &&
                        pages_of(held, P) <= a.max_blocks;
     const int64_t add = fresh > 0 ? fresh : 0;
-    const int64_t keep = sound && fresh >= 0 ? seq : 0;
+    const int keep = sound && fresh >= 0 ? seq : 0;
     const int have = sound ? pages_of(held, P) : 0;
     int64_t target = sound ? keep + add : 0;
     bool refused = !sound || pages_of(target, P) > a.max_blocks || target > INT32_MAX;
-    int grow = refused ? 0 : max(0, pages_of(target, P) - have);
-    int64_t sum, pass_taken, pass_freed;
-    int64_t taken_at = block_scan(grow, warp_sums, sum) - grow;
-    pass_taken = sum;
-    if (asked + sum > avail) {  // the ring runs dry in this pass or before
-      if (grow > 0 && asked + taken_at + grow > avail) {
-        refused = true;
-        grow = 0;
-      }
-      taken_at = block_scan(grow, warp_sums, pass_taken) - grow;
-    }
-    asked += sum;
     if (refused) target = keep;
+    Counts sum;
+    Counts at = block_scan(Counts(max(0, pages_of(target, P) - have),
+                                           max(0, have - pages_of(target, P)), add),
+                                    warp_sums, sum);
+    const int64_t all_asked = asked + sum.taken();
+    if (all_asked > avail) {  // the ring runs dry in this pass or before
+      const int grow = max(0, pages_of(target, P) - have);
+      if (grow > 0 && asked + at.taken() + grow > avail) {
+        refused = true;
+        target = keep;
+      }
+      at = block_scan(Counts(max(0, pages_of(target, P) - have),
+                                      max(0, have - pages_of(target, P)), add),
+                               warp_sums, sum);
+    }
+    asked = all_asked;
     if (in && refused && (add > 0 || !sound)) report_error(a.err, kErrDeviceCheck);
     const int want = pages_of(target, P);
-    const int shrink = max(0, have - want);
-    const int64_t freed_at = block_scan(shrink, warp_sums, pass_freed) - shrink;
-    const int64_t first = tokens + block_scan(add, warp_sums, sum) - add;
-    tokens += sum;
-    ps.taken_at[threadIdx.x] = (int32_t)taken_at;
-    ps.freed_at[threadIdx.x] = (int32_t)freed_at;
-    ps.from[threadIdx.x] = grow > 0 ? have : want;
+    const int64_t first = tokens + at.tokens;
+    ps.taken_at[threadIdx.x] = at.taken();
+    ps.freed_at[threadIdx.x] = at.freed();
+    ps.from[threadIdx.x] = min(have, want);
     if (in) {
       a.kv_lens[b] = (int32_t)target;
       a.cu_new[b] = (int32_t)min(first, (int64_t)INT32_MAX);
     }
     __syncthreads();
     // pages change hands, a thread each: what a request gives back may be thousands
-    for (int i = threadIdx.x; i < pass_freed; i += kThreads) {
+    for (int i = threadIdx.x; i < sum.freed(); i += kThreads) {
       const int o = owner(ps.freed_at, kThreads, i);
-      a.free_pages[(tail + freed + i) % a.ring_size] =
+      a.free_pages[in_ring(tail0 + freed + i)] =
           a.block_table[(int64_t)(base + o) * a.max_blocks + ps.from[o] + i - ps.freed_at[o]];
     }
-    for (int i = threadIdx.x; i < pass_taken; i += kThreads) {
+    for (int i = threadIdx.x; i < sum.taken(); i += kThreads) {
       const int o = owner(ps.taken_at, kThreads, i);
       a.block_table[(int64_t)(base + o) * a.max_blocks + ps.from[o] + i - ps.taken_at[o]] =
-          a.free_pages[(head + taken + i) % a.ring_size];
+          a.free_pages[in_ring(head0 + taken + i)];
     }
-    taken += pass_taken;
-    freed += pass_freed;
-    __syncthreads();
-    if (in && add > 0 && first < a.max_tokens)
-      a.slots[first] =
-          refused ? -1
-                  : (int64_t)a.block_table[(int64_t)b * a.max_blocks + keep / P] * P + keep % P;
+    taken += sum.taken();
+    freed += sum.freed();
+    tokens += sum.tokens;
+    long_ones |= __syncthreads_or(in && add > kFew) != 0;
+    // a request's first slot, or all of few, by its own thread
+    if (in && add > 0) {
+      const int n = add <= kFew && write_slots ? (int)add : 1;
+      const int32_t* row = a.block_table + (int64_t)b * a.max_blocks;
+      for (int t = 0; t < n; ++t) {
+        const int64_t i = first + t;
+        const int pos = keep + t;
+        if (i < a.max_tokens) a.slots[i] = refused ? -1 : (int64_t)row[pos / P] * P + pos % P;
+      }
+    }
   }
   if (threadIdx.x == 0) {
     a.cu_new[a.num_seqs] = (int32_t)min(tokens, (int64_t)INT32_MAX);
@@ -169,22 +181,37 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write
       report_error(a.err, kErrDeviceCheck);
   }
   if (!write_slots) return;
-  __syncthreads();  // cu_new, kv_lens, block_table and the first slots are in place
-  for (int i = threadIdx.x; i < a.max_tokens; i += kThreads) {
-    if (i >= tokens)
-      a.slots[i] = -1;
-    else if (a.cu_new[request_of(a.cu_new, a.num_seqs, i)] != i)
-      a.slots[i] = slot_of(a, i);
+  const int live = (int)min(tokens, (int64_t)a.max_tokens);
+  if (long_ones) {
+    __syncthreads();  // cu_new, kv_lens, block_table and the first slots are in place
+    for (int i = threadIdx.x; i < live; i += kThreads) {
+      const int b = owner(a.cu_new, a.num_seqs, i);
+      const int first = a.cu_new[b], n = a.cu_new[b + 1] - first;
+      if (n > kFew && i != first) a.slots[i] = slot_of(a, b, i, first, n);
+    }
   }
+  for (int i = live + threadIdx.x; i < a.max_tokens; i += kThreads) a.slots[i] = -1;
 }
 
+constexpr int kOffsets = 4096;  // offsets that the slot kernel keeps in shared memory
+
 __global__ void __launch_bounds__(256) slots_kernel(TableArgs a) {
-  const int tokens = a.cu_new[a.num_seqs];
+  __shared__ int32_t cu[kOffsets + 1];
+  const bool here = a.num_seqs <= kOffsets;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // of the kernel before
+  if (here)
+    for (int i = threadIdx.x; i <= a.num_seqs; i += 256) cu[i] = a.cu_new[i];
+  __syncthreads();
+  const int32_t* offsets = here ? cu : a.cu_new;
+  const int tokens = offsets[a.num_seqs];
   for (int i = blockIdx.x * 256 + threadIdx.x; i < a.max_tokens; i += gridDim.x * 256) {
-    if (i >= tokens)
+    if (i >= tokens) {
       a.slots[i] = -1;
-    else if (a.cu_new[request_of(a.cu_new, a.num_seqs, i)] != i)
-      a.slots[i] = slot_of(a, i);
+      continue;
+    }
+    const int b = owner(offsets, a.num_seqs, i);
+    const int first = offsets[b];
+    if (i != first) a.slots[i] = slot_of(a, b, i, first, offsets[b + 1] - first);
   }
 }
 
@@ -201,8 +228,16 @@ cudaError_t launch_cache_tables(const TableArgs& a, cudaStream_t st) {
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  slots_kernel<<<std::min((a.max_tokens + 255) / 256, 8 * sms), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min((a.max_tokens + 255) / 256, 4 * sms));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, slots_kernel, a);
 }
 
 }  // namespace kda
