@@ -655,6 +655,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   const int w0 = blockIdx.x * WARPS;
   if (tid == 0) parts.open[blockIdx.x].last = -1;
   __syncthreads();
+  int dealt = 0;  // rows dealt out to the warps in turn, over all jobs
   for (int j = 0; j <= WARPS; ++j) {
     const auto job = sm.job[j];
     if (job.rows == 0) continue;
@@ -663,7 +664,9 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
     const int last = (int)min(job.last, (unsigned long long)(w0 + WARPS - 1));
     if (starts && !ends && tid == 0)
       parts.open[blockIdx.x] = {job.bos, job.row0, job.rows, job.head, (int)(job.last / WARPS)};
-    for (int row = warp; row < job.rows; row += WARPS) {
+    const int row_first = (warp - dealt % WARPS + WARPS) % WARPS;
+    dealt += job.rows;
+    for (int row = row_first; row < job.rows; row += WARPS) {
       RowSum<D> sum;
       sum.add(parts.o, parts.ml, first, last, [&](int w) {
         return (int64_t)(2 * w + (starts && w == first ? 1 : 0)) * ROWS + row;
