@@ -6,8 +6,9 @@
 // usual running maximum m and sum l of a softmax,
 //     p_j = 2^(s_j - m),  l = sum p_j,  o = sum p_j v_j,   s = scale log2(e) q . k,
 // partial (m, l, o) of parts of a unit's keys being joined by rescaling to the
-// common maximum.  m is moved (and o, l rescaled) only when some score passes it
-// by more than 8, so p <= 2^8: any reference gives the same quotient o / l.
+// common maximum.  m is set 7 below the largest score and moved (and o, l rescaled)
+// only when some score passes it by more than 15, so p <= 2^15: any reference gives
+// the same quotient o / l.
 //
 // Products.  mma.sync m16n8k16 on halves with the cache as the 16-row operand:
 // scores^T = K q^T (16 keys x 8 rows), o^T += V^T p^T (16 channels x 8 rows).
@@ -17,7 +18,7 @@
 // the bytes of a group (the layout in include/kda.h is the fragments' order), a
 // conversion instruction makes two halves of each byte, and one half2 product
 // applies the E4M3 scale: code x scale has 6 significant bits, exact in a half.
-// q is scaled to [1/2, 1] by a power of two per row and rounded to halves: bf16
+// q is scaled by a power of two per row (row_scale) and rounded to halves: bf16
 // fits exactly, fp32 goes in as two halves.  p is rounded to a half (2^-11, below
 // the output's own 2^-8), for fp32 outputs to two.  All sums are fp32.
 //
@@ -460,15 +461,31 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         }
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int n = 0; n < NT; ++n) {
+        if constexpr (TERMS == 1) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < TERMS; ++e) {
-            const uint2 q = query(n, 2 * w + j, e);
+          for (int j = 0; j < 2; ++j) {
+            const uint2 q = query(n, 2 * w + j, 0);
 #pragma unroll
             for (int u = 0; u < kTileGroups; ++u) tc::mma_16816_f16(s[u][n], af[u][j], q.x, q.y);
           }
+        } else {  // short sums, second halves first: see value_word
+          float part[kTileGroups][4] = {};
+#pragma unroll
+          for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint2 q = query(n, 2 * w + j, e);
+#pragma unroll
+              for (int u = 0; u < kTileGroups; ++u)
+                tc::mma_16816_f16(part[u], af[u][j], q.x, q.y);
+            }
+#pragma unroll
+          for (int u = 0; u < kTileGroups; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][n][i] += part[u][i];
+        }
+      }
     };
     struct Values {
       uint32_t c0[2][D / 64], c1[2][D / 64];  // [token][word] of tokens 2t.., 2t + 8..
@@ -502,10 +519,21 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         const uint32_t af[4] = {mul_f16x2(e0[j], s0), mul_f16x2(d0[j], s0), mul_f16x2(e1[j], s1),
                                 mul_f16x2(d1[j], s1)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (TERMS == 1) {
+            tc::mma_16816_f16(o[wd * 4 + j][n], af, pf[u][n][0][0], pf[u][n][0][1]);
+          } else {
+            // The tensor cores cut off what they add up; over a long row that drifts towards
+            // zero (9000 keys: 5e-6 of an fp32 output).  Sums of 16 keys are added here, rounded;
+            // the weights' second halves go first, where what is cut off is little.
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < TERMS; ++e)
-            tc::mma_16816_f16(o[wd * 4 + j][n], af, pf[u][n][e][0], pf[u][n][e][1]);
+            for (int e = TERMS - 1; e >= 0; --e)
+              tc::mma_16816_f16(part, af, pf[u][n][e][0], pf[u][n][e][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[wd * 4 + j][n][i] += part[i];
+          }
+        }
       }
     };
 
@@ -578,10 +606,10 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             if (top > -INFINITY) {
               const float before = thr[n][e] == -INFINITY ? -INFINITY : -neg[n][e];
-              const float m = fmaxf(before, top * sf[n][e]);
+              const float m = fmaxf(before, top * sf[n][e] - kLift);
               const float keep = ex2_approx(before - m);
               neg[n][e] = -m;
-              thr[n][e] = (m + kSlack) / sf[n][e];
+              thr[n][e] = (m + (kLift + kSlack)) / sf[n][e];
               l[n][e] *= keep;
 #pragma unroll
               for (int i2 = 0; i2 < KM; ++i2) {

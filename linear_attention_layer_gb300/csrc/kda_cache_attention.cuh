@@ -9,7 +9,10 @@
 namespace kda {
 namespace cache {
 
-constexpr float kSlack = 8.f;  // log2 head room of a weight over the reference maximum
+// Weights are 2^(s - m) with a reference m below the largest score seen by kLift at least and
+// kLift + kSlack at most: up to 2^15, within a half's range, and as far from the end of its
+// small numbers as that allows.
+constexpr float kSlack = 8.f, kLift = 7.f;
 constexpr long long kWaitCycles = 2000000000ll;  // about a second: a wait gives up after it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -71,7 +74,8 @@ __device__ __forceinline__ int find_last(const P* plan, int n, unsigned long lon
   return lo;
 }
 
-// Power of two that brings a row with this largest magnitude into [1, 2): the row's
+// Power of two that brings a row with this largest magnitude into [2^10, 2^11) -- again
+// far from a half's smallest numbers, where its second half would lose bits: the row's
 // factors down (applied to it, with the sign of the score factor) and f (of its raw
 // scores, log2 units; kept positive and finite, so that a masked score stays -infinity).
 struct RowScale {
@@ -82,6 +86,7 @@ __device__ __forceinline__ RowScale row_scale(float top, float scale, float k_fa
   int e = ((__float_as_int(top) >> 23) & 255) - 127;
   e = e == 128 ? 0 : max(-126, min(e, 126));
   RowScale r;
+  e = max(e - 10, -126);
   r.down = copysignf(__int_as_float((127 - e) << 23), scale);
   r.f = fminf(fmaxf(fabsf(scale) * kLog2e * k_factor * __int_as_float((127 + e) << 23), 1.2e-38f),
               3.e38f);

@@ -5,7 +5,7 @@
 // that share it, as two blocks of 128 rows.  Its keys are walked in tiles of 64,
 //     S = q K^T,   P = 2^(S f - m),   l += row sums of P,   O += P V,
 // with the running reference m of kda_cache_attention.cu (moved, and O rescaled,
-// only when a score passes it by more than 8).  4 * 64 * 128 * D flops a block and
+// only when a score passes it by more than 15).  4 * 64 * 128 * D flops a block and
 // tile stand against the softmax of 128 x 64 scores and, shared by the blocks, the
 // dequantisation of 2 * 64 * D codes: the tensor cores bound it if those two keep
 // out of their way.
@@ -369,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float keep = 1.f;
           if (top > -INFINITY) {
             const float before = thr == -INFINITY ? -INFINITY : -neg;
-            const float m = fmaxf(before, top * f);
+            const float m = fmaxf(before, top * f - kLift);
             keep = ex2_approx(before - m);
             neg = -m;
-            thr = (m + kSlack) / f;
+            thr = (m + (kLift + kSlack)) / f;
           }
           const uint64_t keep2 = tc::pack2(keep, keep);
           l2[0] = tc::fma2(l2[0], keep2, 0);

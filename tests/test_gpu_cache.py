@@ -322,6 +322,20 @@ def test_chunks(dtype, D, Hq, Hk, P, kv, new):
     p.check(*p.call())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv,new", [([40, 700], [100, 300]), ([2000], [90]), ([257, 5, 64], [256, 5, 60])])
+def test_chunks_of_many_rows(D, kv, new):
+    """More rows than a unit has, contexts shorter than the chunk, contexts cut over CTAs."""
+    p = Problem(kv, new, 8, 1, D, 48, torch.bfloat16, seed=D + sum(kv))
+    p.check(*p.call())
+
+
+@pytest.mark.parametrize("rows", [8, 9, 16, 17, 47, 48, 49, 128, 129, 256, 257])
+def test_row_counts_at_the_kernels_borders(rows):
+    p = Problem([300, 310], [rows, 1], 1, 1, 64, 16, torch.bfloat16, seed=rows)
+    p.check(*p.call())
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_one_long_request(dtype):
     p = Problem([4100], [2], 4, 2, 128, 64, dtype, seed=3)
