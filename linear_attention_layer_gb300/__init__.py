@@ -2,7 +2,7 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``_lib/libkda.so``, reached through its C ABI (``include/kda.h``)
-with ctypes.  PyTorch supplies device memory and streams.  There is no CPU
+with ctypes (the cache calls: with a native module, ``csrc/cache_binding.cpp``).  PyTorch supplies device memory and streams.  There is no CPU
 fallback: if the library is missing or a call fails, these functions raise.
 
 Entry points (same names as the C ABI, without the ``kda_`` prefix):

@@ -19,16 +19,23 @@
 // P 2 x 32, q 64, O 2 x D: with D = 128 the second block's q has no room there and is an
 // A operand in shared memory (its 8 score products then take 48 cycles instead of 32).
 // P apart from S is worth that: the next scores are computed while a tile's weights
-// are (with P over S, and both blocks' q in tensor memory, 822 us instead of XXX for
-// 2048 tokens over 32768 keys, 32 heads on 8).
+// are (2048 new tokens at the end of 32768 keys, 32 heads on 8: with P over S, and both
+// blocks' q in tensor memory, 822 us; apart, 779).
 //
 // Warps.  0-3 and 4-7: softmax of the two blocks, a thread a row; 8-11: dequantisation;
-// 12: issues the matrix products; 13: copies pages into a ring.  Two threads a row
-// (16 softmax warps of 80 registers) measured slower, 862 us against 822.
+// 12: issues the matrix products; 13: copies pages into a ring.  Measured slower: two
+// threads a row (16 softmax warps of 80 registers, 862 us against 822), eight warps for the
+// dequantisation with registers moved to the softmax (876 against 746), and, for up to 128
+// rows, the two blocks on alternate tiles of the same rows (no faster than one block).
 //
 // Work split.  The tiles of all units in one sequence are cut evenly over the CTAs, one
 // per SM; parts of a unit are joined by a second kernel.  Units of one chunk differ in
 // length (causality), so a planner kernel sums them first.
+//
+// Measured: the chunk above takes 740 us, 1.44 PFLOP/s, 0.76 of the measured bf16 rate (this
+// kernel 714, the launches around it the rest); tensor pipe 64% busy.  A tile of both blocks
+// takes about 1600 cycles: 1152 of products, the rest waits for the softmax, whose two
+// warps a quadrant take about 1500 (64 exponentials a row and warp alone 256).
 #include <math.h>
 
 #include <algorithm>

@@ -5,7 +5,10 @@
 // thread's own registers, its codes are one 8-byte store, and nothing is shared
 // between threads.  Both calls read and write each value once and are bound by
 // HBM as long as a value costs few enough instructions (about six; HBM's rate
-// leaves 11), which decides how the rounding below is done.
+// leaves 11), which decides how the rounding below is done.  Measured for 270336 tokens x 8
+// heads x 128 channels of bf16, 1.42 GB each way: append 283 us (0.75 of the measured HBM
+// rate; 175 warp instructions a block, most of the wait for the loads of CTAs that live
+// for one of them), read 240 us (0.88).
 //
 // A CTA takes 8 tokens of K or of V, a thread one token and block and every so many
 // heads: where the token's slot lies is worked out once, the heads are strides.  Lanes

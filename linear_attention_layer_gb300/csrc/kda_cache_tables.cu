@@ -16,6 +16,8 @@
 namespace kda {
 namespace {
 
+// 256 requests' decode step / 37 with up to 1800 pages given back / 64 prompts, host included:
+// 9.6 / 12.3 / 14.3 us; with 256 threads 10.2 / 13.7 / 16.4, with 1024 10.3 / 12.3 / 14.5.
 constexpr int kThreads = 512;
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int page) {
@@ -215,7 +217,8 @@ __global__ void __launch_bounds__(256) slots_kernel(TableArgs a) {
   }
 }
 
-// Up to this many slots are written by the first kernel.
+// Up to this many slots are written by the first kernel: a few passes of its CTA, which
+// cost less than a second launch (2 to 3 us).
 constexpr int kOneLaunchTokens = 4096;
 
 }  // namespace
