@@ -708,7 +708,6 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   __syncthreads();
   const int w0 = blockIdx.x * WARPS;
   if (tid == 0) parts.open[blockIdx.x].last = -1;
-  __syncthreads();
   int dealt = 0;  // rows dealt out to the warps in turn, over all jobs
   for (int j = 0; j <= WARPS; ++j) {
     const auto job = sm.job[j];
@@ -773,7 +772,7 @@ struct Split {
       const int nseq = std::min(kMaxSeqs, a.num_seqs - seq0);
       kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, seq0, nseq, range, parts, q_vec);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      e = launch_join<T, D, 1>(c, a, parts.open, parts.o, parts.ml, sh.warp_slots(), ROWS, sh.ctas,
+      e = launch_join<T, D, 1, 4>(c, a, parts.open, parts.o, parts.ml, sh.warp_slots(), ROWS, sh.ctas,
                                st);
       if (e != cudaSuccess) return e;
     }

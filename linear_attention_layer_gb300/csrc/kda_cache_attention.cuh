@@ -186,13 +186,13 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Joins open units: a CTA has PER rows of one, WPR = 4 / PER warps a row.
-template <typename T, int D, int PER>
-__global__ void __launch_bounds__(128)
+// Joins open units: a CTA has PER rows of one, WPR warps a row.
+template <typename T, int D, int PER, int WPR>
+__global__ void __launch_bounds__(32 * PER * WPR)
     join_kernel(View c, AttentionArgs a, const OpenUnit* units, const float* o, const float2* ml,
                 int slot0, int unit_rows) {
-  constexpr int WPR = 4 / PER;
-  __shared__ RowSum<D> shared_sum[WPR > 1 ? 4 : 1][WPR > 1 ? 32 : 1];
+  constexpr int kFields = 2 + D / 32;
+  __shared__ float shared_sum[WPR > 1 ? PER * WPR : 1][kFields][32];
   wait_for_previous();
   const int first = blockIdx.x;
   const OpenUnit u = units[first];
@@ -207,19 +207,22 @@ __global__ void __launch_bounds__(128)
       return (int64_t)(slot0 + 2 * i + (i == first ? 1 : 0)) * unit_rows + row;
     });
   if constexpr (WPR > 1) {
-    shared_sum[warp][lane] = r;
+    shared_sum[warp][0][lane] = r.top;
+    shared_sum[warp][1][lane] = r.sum;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) shared_sum[warp][2 + j][lane] = r.x[j];
     __syncthreads();
     if (part != 0) return;
 #pragma unroll
     for (int w = 1; w < WPR; ++w) {
-      const RowSum<D>& s = shared_sum[warp + w][lane];
-      const float next = fmaxf(r.top, s.top);
+      const float(*s)[32] = shared_sum[warp + w];
+      const float next = fmaxf(r.top, s[0][lane]);
       const float k0 = next == -INFINITY ? 1.f : ex2_approx(r.top - next);
-      const float k1 = next == -INFINITY ? 1.f : ex2_approx(s.top - next);
+      const float k1 = next == -INFINITY ? 1.f : ex2_approx(s[0][lane] - next);
       r.top = next;
-      r.sum = r.sum * k0 + s.sum * k1;
+      r.sum = r.sum * k0 + s[1][lane] * k1;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) r.x[j] = r.x[j] * k0 + s.x[j] * k1;
+      for (int j = 0; j < D / 32; ++j) r.x[j] = r.x[j] * k0 + s[2 + j][lane] * k1;
     }
   }
   if (row >= u.rows) return;
@@ -230,20 +233,20 @@ __global__ void __launch_bounds__(128)
 }
 
 // Launches it right behind the kernel whose units it joins.
-template <typename T, int D, int PER>
+template <typename T, int D, int PER, int WPR>
 cudaError_t launch_join(const View& c, const AttentionArgs& a, const OpenUnit* units,
                         const float* o, const float2* ml, int slot0, int unit_rows, int ctas,
                         cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, unit_rows / PER);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * PER * WPR);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, PER>, c, a, units, o, ml, slot0, unit_rows);
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, PER, WPR>, c, a, units, o, ml, slot0, unit_rows);
 }
 
 inline int sm_count() {

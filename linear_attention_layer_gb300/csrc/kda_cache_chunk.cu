@@ -735,7 +735,7 @@ cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cu
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   chunk_kernel<D><<<ctas, kThreads, kSmem, st>>>(c, a, range, plan, q_vec);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<__nv_bfloat16, D, 4>(c, a, plan.open, plan.o, plan.ml, 0, kRows, ctas, st);
+  return launch_join<__nv_bfloat16, D, 4, 1>(c, a, plan.open, plan.o, plan.ml, 0, kRows, ctas, st);
 }
 
 }  // namespace
