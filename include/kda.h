@@ -754,7 +754,8 @@ kda_status_t kda_cache_read(const kda_cache_t* cache, int32_t io_dtype, int32_t 
  *
  *   q             device, [total_tokens, num_heads, head_dim] io dtype, tokens
  *                 and heads q_strides[0], q_strides[1] elements apart (both 0:
- *                 packed; one of them 0 is refused), channels contiguous
+ *                 packed; one of them 0 is refused: a broadcast query has no
+ *                 form here), channels contiguous
  *   block_table   device, [num_seqs][max_blocks] int32
  *   kv_lens       device, [num_seqs] int32
  *   cu_new        device, [num_seqs + 1] int32

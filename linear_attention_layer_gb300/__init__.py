@@ -1023,7 +1023,8 @@ def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=No
                     k_exponent=None, v_exponent=None, out=None, return_lse=False, lse=None,
                     workspace="auto", stream=None):
     """``kda_cache_attention``: causal attention of the new tokens q [T, heads,
-    head_dim] (packed over the requests by cu_new int32 [B + 1]; their keys are in
+    head_dim] (slices of a larger tensor will do, the channels contiguous, but no
+    broadcast; packed over the requests by cu_new int32 [B + 1]; their keys are in
     the cache already) over ``cache`` through block_table int32 [B, max_blocks] and
     kv_lens int32 [B], the lengths with the new tokens.  ``max_new``: new tokens of
     the longest request (1 for a decode step).  ``scale``: of the scores, default

@@ -82,6 +82,19 @@ const Tensor& rows(PyObject* o, const char* name, ScalarType type, IntArrayRef s
   return t;
 }
 
+// Token and head stride of q [T, heads, channels].  Zeros mean "packed" to the C call, so a q
+// broadcast over tokens or heads is refused: it would be read as the T heads channels elements
+// that it does not have.  The stride of a dimension of one element says nothing (torch leaves any
+// number there, 0 too) and gives way to the packed one.
+void query_strides(const Tensor& q, int64_t (&strides)[2]) {
+  if (q.numel() == 0) return;  // not read
+  strides[0] = q.size(0) == 1 ? q.size(1) * q.size(2) : q.stride(0);
+  strides[1] = q.size(1) == 1 ? q.size(2) : q.stride(1);
+  if (strides[0] == 0 || strides[1] == 0)
+    REFUSE("q must not be broadcast over tokens or heads, got strides " << q.strides()
+           << " of shape " << q.sizes());
+}
+
 int64_t integer(PyObject* o, const char* name) {
   const int64_t v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw python_error();
@@ -217,11 +230,13 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arity(n, 13);
-  kda_cache_t c;
-  const c10::Device dev = cache_struct(a[1], a[7], a[8], c);
   const Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "block_table");
   if (q.dim() != 3 || table.dim() != 2)
     REFUSE("q must be [T, heads, head_dim] and block_table [B, max_blocks]");
+  kda_attention_t d = {};
+  query_strides(q, d.q_strides);
+  kda_cache_t c;
+  const c10::Device dev = cache_struct(a[1], a[7], a[8], c);
   const int64_t T = q.size(0), H = q.size(1), D = q.size(2), blocks = table.size(1),
                 B = tensor(a[3], "kv_lens").numel();
   if (D != c.head_dim || c.num_kv_heads <= 0 || H % c.num_kv_heads != 0)
@@ -233,7 +248,6 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 lse_shape[] = {T, H};
   const ScalarType type = q.scalar_type();
   constexpr ScalarType I = ScalarType::Int;
-  kda_attention_t d = {};
   d.io_dtype = io_code(type);
   rows(a[0], "q", type, shape, dev);
   d.num_seqs = (int32_t)B;
@@ -247,10 +261,6 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double s = PyFloat_AsDouble(a[6]);
     if (s == -1.0 && PyErr_Occurred()) throw python_error();
     d.scale = (float)s;
-  }
-  if (!q.is_contiguous()) {
-    d.q_strides[0] = q.stride(0);
-    d.q_strides[1] = q.stride(1);
   }
   const int32_t* table_p = need<int32_t>(a[2], "block_table", I, table_shape, dev);
   const int32_t* kv_p = need<int32_t>(a[3], "kv_lens", I, lens, dev);

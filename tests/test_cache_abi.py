@@ -191,3 +191,14 @@ def test_binding_refuses():
         kda.cache_attention(x, cache, torch.zeros(1, 1, dtype=torch.int32),
                             torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                             max_new=1)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 64), (5, 1, 64), (1, 4, 64)])
+def test_binding_refuses_broadcast_queries(lib, shape):
+    """Stride 0 over more than one token or head: two such would be taken for packed, and read
+    past the end.  Refused before anything else is looked at."""
+    q = torch.zeros(shape).expand(5, 4, 64)
+    cache = kda.cache_empty(1, 16, 2, 64, device="cpu")
+    lens, cu = torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="broadcast"):
+        kda.cache_attention(q, cache, lens[None], lens, cu, max_new=1)
