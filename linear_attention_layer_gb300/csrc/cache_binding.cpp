@@ -82,14 +82,18 @@ const Tensor& rows(PyObject* o, const char* name, ScalarType type, IntArrayRef s
   return t;
 }
 
-// Token and head stride of q [T, heads, channels].  Zeros mean "packed" to the C call, so a q
-// broadcast over tokens or heads is refused: it would be read as the T heads channels elements
-// that it does not have.  The stride of a dimension of one element says nothing (torch leaves any
-// number there, 0 too) and gives way to the packed one.
+// Token and head stride of t [T, heads, channels].  The stride of a dimension of one element
+// says nothing (torch leaves any number there) and gives way to the packed one.
+void outer_strides(const Tensor& t, int64_t* strides) {
+  strides[0] = t.size(0) == 1 ? t.size(1) * t.size(2) : t.stride(0);
+  strides[1] = t.size(1) == 1 ? t.size(2) : t.stride(1);
+}
+
+// The same of q.  Zeros mean "packed" to the C call, so a q broadcast over tokens or heads is
+// refused: it would be read as the T heads channels elements that it does not have.
 void query_strides(const Tensor& q, int64_t (&strides)[2]) {
   if (q.numel() == 0) return;  // not read
-  strides[0] = q.size(0) == 1 ? q.size(1) * q.size(2) : q.stride(0);
-  strides[1] = q.size(1) == 1 ? q.size(2) : q.stride(1);
+  outer_strides(q, strides);
   if (strides[0] == 0 || strides[1] == 0)
     REFUSE("q must not be broadcast over tokens or heads, got strides " << q.strides()
            << " of shape " << q.sizes());
@@ -196,7 +200,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t io = io_code(type);
   const Tensor &k = rows(a[0], "k", type, shape, dev), &v = rows(a[1], "v", type, shape, dev);
   const int64_t* slots = need<int64_t>(a[2], "slots", ScalarType::Long, slots_shape, dev);
-  const int64_t strides[] = {k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+  int64_t strides[4];
+  outer_strides(k, strides);
+  outer_strides(v, strides + 2);
   const c10::cuda::CUDAGuard guard(dev);
   return status_object(kda_cache_append(&c, io, (int32_t)T, k.data_ptr(), v.data_ptr(), strides,
                                         slots, stream_of(dev)));

@@ -24,3 +24,29 @@ def test_strides_of_single_tokens_and_heads_say_nothing(dtype, T, H, strides):
     assert q.stride()[:2] == strides and not q.is_contiguous()
     for a, b in zip(base, p.call(q=q)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,H,strides", [(1, 3, (0, 160)), (1, 3, (1 << 40, 160)),
+                                         (5, 1, (200, 0)), (5, 1, (200, 1 << 40))])
+def test_append_strides_of_single_tokens_and_heads_say_nothing(dtype, T, H, strides):
+    x = torch.randn((2, T, H, 128), device=DEV).to(dtype)
+    room = torch.full((2, 2000), 9.0, dtype=dtype, device=DEV)
+    k, v = (room[i].as_strided((T, H, 128), strides + (1,)) for i in range(2))
+    k.copy_(x[0]), v.copy_(x[1])
+    slots = torch.arange(3, 3 + T, device=DEV)
+    caches = [torch.zeros((1, H, 1, 18 * 128), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    kda.cache_append(x[0], x[1], slots, caches[0])
+    kda.cache_append(k, v, slots, caches[1])
+    assert torch.equal(*caches)
+
+
+def test_append_takes_broadcast_rows():
+    """One key and value for every token: stride 0 is what it says."""
+    x = torch.randn((2, 1, 2, 64), device=DEV)
+    slots = torch.arange(20, device=DEV)
+    caches = [torch.zeros((2, 2, 1, 18 * 64), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    wide = x.expand(2, 20, 2, 64)
+    kda.cache_append(wide[0], wide[1], slots, caches[0])
+    kda.cache_append(wide[0].contiguous(), wide[1].contiguous(), slots, caches[1])
+    assert torch.equal(*caches)
