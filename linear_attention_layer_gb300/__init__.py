@@ -818,8 +818,9 @@ def get_device_error(stream=None) -> int:
 
 
 def testing_inject_wait_timeout(launches: int = 1) -> None:
-    """Make the next `launches` tensor-core prefill launches of this thread hit
-    an expired device wait (``kda_testing_inject_wait_timeout``)."""
+    """Make the next `launches` tensor-core prefill launches or ``cache_attention``
+    calls of this thread hit an expired device wait
+    (``kda_testing_inject_wait_timeout``)."""
     load().kda_testing_inject_wait_timeout(int(launches))
 
 

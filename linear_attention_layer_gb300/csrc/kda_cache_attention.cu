@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   // ---- the plan: tiles before each request ----
   if (tid <= WARPS) sm.job[tid].rows = 0;
   if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) tc::mbar_init(&sm.full[warp][s], kTileGroups);
+    for (int s = 0; s < STAGES; ++s)
+      tc::mbar_init(&sm.full[warp][s], kTileGroups + (s == 0 ? a.withheld : 0));
     tc::mbar_fence_init();
   }
   {
@@ -222,7 +223,6 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   const unsigned long long x0 = min(per * worker, total), x1 = min(x0 + per, total);
   const Shape shape{(int)gridDim.x, WARPS};
 
-  bool timed_out = false;
   if (x0 < x1) {
     Cursor ld, cp;
     cp.seek(c, a, seq0, nseq, range, ROWS, sm.plan, x0);
@@ -548,7 +548,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
     int stage = 0;
     uint32_t parity = 0;
     auto wait = [&](int st, uint32_t par) {
-      const bool ok = wait_phase(&sm.full[warp][st], par, nullptr);
+      const bool ok = __all_sync(
+          0xffffffffu, wait_phase(&sm.full[warp][st], par, a.wait_cycles, nullptr));
       if (!ok && lane == 0) report_error(a.err, kErrTimeout);
       return ok;
     };
@@ -563,7 +564,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) score_word(k, w);
     }
-    for (int i = 0; i < count && fed; ++i) {
+    int i = 0;
+    for (; i < count && fed; ++i) {
       // s holds the raw scores of tile i
       const uint8_t* const base = sm.ring[warp][stage];
       const uint32_t valid = sm.valid[warp][stage];
@@ -700,11 +702,14 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
       stage = next;
       parity = next_parity;
     }
-    timed_out = !fed;
+    if (!fed) {  // the copies under way, of tiles i on, land before the shared memory goes away
+      if (lane < a.withheld) tc::mbar_arrive(&sm.full[warp][0]);
+      for (; i < issued; ++i)
+        wait_phase(&sm.full[warp][i % STAGES], i / STAGES & 1, a.wait_cycles, nullptr);
+    }
   }
 
   // ---- join the parts of units that several warps of this CTA had ----
-  if (timed_out) __nanosleep(1000000);  // let the copies under way land
   __syncthreads();
   const int w0 = blockIdx.x * WARPS;
   if (tid == 0) parts.open[blockIdx.x].last = -1;
@@ -821,7 +826,12 @@ bool cache_chunk_wanted(const View& c, const AttentionArgs& a) {
   return a.bf16 && (int64_t)a.max_new * (a.num_heads / c.kv_heads) > kSplitRows;
 }
 
-cudaError_t launch_cache_attention(const View& c, const AttentionArgs& a, cudaStream_t st) {
+cudaError_t launch_cache_attention(const View& c, const AttentionArgs& args, cudaStream_t st) {
+  AttentionArgs a = args;
+  if (take_injected_timeout()) {
+    a.wait_cycles = kInjectedWaitCycles;
+    a.withheld = 1;
+  }
   const bool chunk = cache_chunk_wanted(c, a);
   // without the second kernel the first takes every request, whatever max_new said
   const RowRange few{0, chunk ? kSplitRows : INT64_MAX}, many{kSplitRows, INT64_MAX};

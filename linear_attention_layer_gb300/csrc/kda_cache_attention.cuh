@@ -13,18 +13,20 @@ namespace cache {
 // kLift + kSlack at most: up to 2^15, within a half's range, and as far from the end of its
 // small numbers as that allows.
 constexpr float kSlack = 8.f, kLift = 7.f;
-constexpr long long kWaitCycles = 2000000000ll;  // about a second: a wait gives up after it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Waits for a phase of the barrier; false when it took kWaitCycles or `*failed` (another
-// warp's wait that gave up; may be null) was set.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed) {
+// Waits for a phase of the barrier; false when it took `limit` cycles or `*failed` (another wait
+// that gave up; may be null) was set.  Each thread has its own answer: before code that needs a
+// whole warp the answers have to be brought together by a vote, or some of its threads could
+// leave and the others wait for them.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t limit,
+                                           volatile int* failed) {
   if (tc::mbar_try_wait(bar, parity)) return true;
-  const long long start = clock64();
+  const uint32_t start = (uint32_t)clock();  // 32 bits: 2 s, and a register less
   for (uint32_t i = 1;; ++i) {
     if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((i & 15) == 0 && ((failed && *failed) || clock64() - start > kWaitCycles)) return false;
+    if ((i & 15) == 0 && ((failed && *failed) || (uint32_t)clock() - start > limit)) return false;
   }
 }
 

@@ -176,9 +176,10 @@ struct Smem {
   alignas(128) uint8_t raw[kRawStages][kRaw];
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
-  uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_full[2], issued;
   uint32_t valid[kValidRing];  // groups of a tile that can be read
   uint32_t tmem;
+  uint32_t copied;  // tiles whose pages were asked for
   int failed;
 };
 
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < kRawStages; ++i) {
-      tc::mbar_init(&sm.raw_full[i], kGroups);
+      tc::mbar_init(&sm.raw_full[i], kGroups + (i == 0 ? a.withheld : 0));
       tc::mbar_init(&sm.raw_empty[i], 4);
     }
     for (int i = 0; i < kTileStages; ++i) {
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sm.p_full[i], 4);
       tc::mbar_init(&sm.o_full[i], 1);
     }
+    tc::mbar_init(&sm.issued, 1);
     sm.failed = 0;
     tc::mbar_fence_init();
   }
@@ -243,14 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long per = (total + gridDim.x - 1) / gridDim.x;
   const unsigned long long x0 = min(per * blockIdx.x, total), x1 = min(x0 + per, total);
 
-  // A wait that gives up tells the other warps, who give up as well.
+  // A wait that gives up tells the other warps, who give up as well.  A warp leaves its tiles
+  // when a vote, one a tile, finds a thread whose wait gave up; until then that thread goes on
+  // with whatever is there (a vote after each wait: 786 us for the chunk above).
   volatile int* failed = &sm.failed;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (wait_phase(bar, parity, failed)) return true;
+    if (wait_phase(bar, parity, a.wait_cycles, failed)) return true;
     *failed = 1;
     report_error(a.err, kErrTimeout);
     return false;
   };
+  auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax ----
@@ -340,8 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float neg = 0.f, thr = -INFINITY;
       uint64_t l2[2] = {0, 0};  // the row's sum, in four parts
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
-        ok = wait(&sm.s_full[blk], s_full.parity);
-        if (!ok) break;
+        ok &= wait(&sm.s_full[blk], s_full.parity);
         s_full.step();
         tc::tc_fence_after();
         float s[kKeys];
@@ -372,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = fmaxf(tc::max3(t4[0], s[kKeys - 4], s[kKeys - 3]),
                                 tc::max3(tc::max3(t4[1], t4[2], t4[3]), s[kKeys - 2], s[kKeys - 1]));
         bool waited = false;
-        if (__any_sync(0xffffffffu, top > thr)) {
+        if (__any_sync(0xffffffffu, top > thr || !ok)) {
+          ok = all_ok(ok);
+          if (!ok) break;
           float keep = 1.f;
           if (top > -INFINITY) {
             const float before = thr == -INFINITY ? -INFINITY : -neg;
@@ -387,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > p.begin) {
             // the product of the tile before has to be in O
             ok = wait(&sm.o_full[blk], o_full.parity);
-            if (!ok) break;
             tc::tc_fence_after();
             waited = true;
 #pragma unroll 1
@@ -417,22 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[i] = tc::pack_f16(p0, p1);
           }
           if (half == 0 && j > p.begin) {  // the product before has read its weights
-            ok = waited || wait(&sm.o_full[blk], o_full.parity);
+            if (!waited) ok &= wait(&sm.o_full[blk], o_full.parity);
             o_full.step();
-            if (!ok) break;
             tc::tc_fence_after();
           }
           tc::tmem_st16u(tp + half * 16, w);
         }
-        if (!ok) break;
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.p_full[blk]);
       }
-      if (!ok) break;
       // ---- end of the piece ----
-      ok = wait(&sm.o_full[blk], o_full.parity);
+      ok = all_ok(ok && wait(&sm.o_full[blk], o_full.parity));
       if (!ok) break;
       o_full.step();
       tc::tc_fence_after();
@@ -484,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kRawStages> raw;
     Ring<kTileStages> st;
     uint32_t empty_parity = 1;  // a fresh barrier passes for the phase before
+    uint32_t tile_no = 0;
     const int t8 = lane & 7, b4 = lane >> 3;
     const int kc = L::k_codes(t8, b4), vc = L::v_codes(t8, b4) - L::v_codes(0, 0);
     const int ks_at = L::k_scale(t8, b4), vs_at = L::v_scale(t8 & 6, b4);
@@ -491,7 +494,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ks_pick = (ks_at & 3) | (((ks_at & 3) + L::kPer) << 4) | 0x4400;
     const uint32_t vs_pick = (t8 & 1) | (((t8 & 1) + 2) << 4) | 0x4400;
     const uint32_t row0 = (dw * kGroup + t8) * 128, chunk0 = ((b4 * 2) ^ t8) << 4;
-    uint32_t tile_no = 0;
     bool ok = true;
     for (unsigned long long x = x0; x < x1 && ok;) {
       Piece p;
@@ -499,7 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       x += p.end - p.begin;
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         ok = wait(&sm.raw_full[raw.i], raw.parity);
-        if (!ok) break;
         // Warp dw takes group dw of the tile; a lane the tokens t8 and t8 + 8 of it and block
         // b4 of every four.  The scales of both tokens lie in one word.
         const uint8_t* g = sm.raw[raw.i] + dw * L::kGroupBytes;
@@ -523,8 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::k_codes(half * 8, bb * 4) + kc);
           scales[bb] = *reinterpret_cast<const uint32_t*>(g + (ks_at & ~3) + bb * 8);
         }
-        ok = wait(&sm.k_empty[st.i], empty_parity);
-        if (!ok) break;
+        ok &= wait(&sm.k_empty[st.i], empty_parity);
 #pragma unroll
         for (int bb = 0; bb < D / 64; ++bb) {
           const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, ks_pick));
@@ -543,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::v_codes(half * 8, bb * 4) + vc);
           scales[bb] = *reinterpret_cast<const uint32_t*>(g + vs_at + bb * 64);
         }
-        ok = wait(&sm.v_empty[st.i], empty_parity);
-        if (!ok) break;
+        ok &= wait(&sm.v_empty[st.i], empty_parity);
         // what lies past the request's length may be anything: its scale becomes 0
         const uint32_t keep = (t8 < left ? 0x00ffu : 0u) | (t8 + 8 < left ? 0xff00u : 0u);
 #pragma unroll
@@ -561,6 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mbar_arrive(&sm.v_full[st.i]);
           tc::mbar_arrive(&sm.raw_empty[raw.i]);
         }
+        ok = all_ok(ok);
+        if (!ok) break;
         raw.step();
         st.step();
         if (st.i == 0) empty_parity ^= 1;
@@ -634,6 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           vs.step();
         }
       }
+      if (!ok) {  // products may be under way: they end before the tensor memory is given back
+        tc::mma_commit(&sm.issued);
+        wait_phase(&sm.issued, 0, a.wait_cycles, nullptr);
+      }
     }
     __syncwarp();
   } else {
@@ -660,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           src = c.pages + (((int64_t)page * c.kv_heads + p.h) * GP + gi % GP) * L::kGroupBytes;
           present = __ballot_sync(0xffffffffu, in && sound);
         }
-        ok = wait(&sm.raw_empty[raw.i], empty_parity);
+        ok = all_ok(wait(&sm.raw_empty[raw.i], empty_parity));
         if (!ok) break;
         if ((lane ^ first) < kGroups) {
           const int u = lane ^ first;
@@ -680,12 +685,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (raw.i == 0) empty_parity ^= 1;
       }
     }
+    if (lane == 0) sm.copied = tile_no;
   }
-  // After a wait gave up, copies and products may be under way: let them land.
-  if (*failed) __nanosleep(1000000);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  if (*failed && warp == 13) {  // the copies under way, of the last tiles, land
+    if (lane < a.withheld) tc::mbar_arrive(&sm.raw_full[0]);
+    const uint32_t n = sm.copied;
+    for (uint32_t i = n - min(n, (uint32_t)kRawStages); i < n; ++i)
+      wait_phase(&sm.raw_full[i % kRawStages], i / kRawStages & 1, a.wait_cycles, nullptr);
+  }
   if (warp == 12) tc::tmem_dealloc(tmem, kCols);
 }
 

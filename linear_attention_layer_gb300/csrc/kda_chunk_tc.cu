@@ -1675,10 +1675,9 @@ struct TcLaunch {
     prm.num_seqs = p.num_seqs;
     prm.spin_cycles = 4000000000LL;  // ~2 s at 2 GHz
     prm.inject_timeout = 0;
-    if (g_inject_wait_timeout > 0) {  // testing aid, see kda_testing_inject_wait_timeout
-      --g_inject_wait_timeout;
+    if (take_injected_timeout()) {
       prm.inject_timeout = 1;
-      prm.spin_cycles = 20000000LL;  // ~10 ms
+      prm.spin_cycles = kInjectedWaitCycles;
     }
     prm.conv_w = a.conv_w;
     prm.conv_wq = a.conv_wq;
@@ -1898,6 +1897,12 @@ cudaError_t launch_chunk_tc_summary(const Problem& p, const Args& a, const int32
   if (e != cudaSuccess) return e;
   return launch_state_fold(kD, kD, p.num_heads, w, w, nullptr, m_out, 1, fm.data(),
                            (int)fm.size(), st);
+}
+
+bool take_injected_timeout() {
+  if (tcp::g_inject_wait_timeout == 0) return false;
+  --tcp::g_inject_wait_timeout;
+  return true;
 }
 
 }  // namespace kda

@@ -122,6 +122,11 @@ cudaError_t launch_recurrent_small(const Problem& p, const Args& a, cudaStream_t
 // Chunked prefill on CUDA cores in fp32 (any supported size, fp32 or bf16 io).
 cudaError_t launch_chunk_simt(const Problem& p, const Args& a, cudaStream_t stream);
 
+// Whether a device wait of this thread's next launch is to run out (testing aid, see
+// kda_testing_inject_wait_timeout); counts the launch.
+bool take_injected_timeout();
+constexpr uint32_t kInjectedWaitCycles = 20000000u;  // about 10 ms
+
 // Chunked prefill on the tensor cores (bf16 io, dk = dv = 128, 16-byte
 // aligned buffers).  cu_host (optional) orders the work longest-first and,
 // with workspace (256-byte aligned), lets long sequences be split across SMs
@@ -280,6 +285,8 @@ struct AttentionArgs {
   float* lse = nullptr;  // may be null
   void* workspace = nullptr;
   int* err = nullptr;
+  uint32_t wait_cycles = 2000000000u;  // about a second: a device wait gives up after it
+  int withheld = 0;  // testing: arrivals that the first barriers wait for in vain
 };
 size_t cache_attention_workspace_bytes(const cache::View& c, const AttentionArgs& a);
 cudaError_t launch_cache_attention(const cache::View& c, const AttentionArgs& a, cudaStream_t st);

@@ -50,3 +50,24 @@ def test_append_takes_broadcast_rows():
     kda.cache_append(wide[0], wide[1], slots, caches[0])
     kda.cache_append(wide[0].contiguous(), wide[1].contiguous(), slots, caches[1])
     assert torch.equal(*caches)
+
+
+# ------------------------------------------------- waits that run out ---
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kv,new", [([70, 2000, 33], [1, 1, 1]), ([70, 2000, 33], [3, 5, 0]),
+                                    ([700, 333, 90], [200, 1, 40])])
+def test_expired_wait_reports_timeout_and_recovers(dtype, kv, new):
+    """An input wait made to run out by the testing hook, in a decode step, windows and (bf16)
+    the chunk kernel: the calls end with KDA_ERR_TIMEOUT in the error word, and the next one on
+    the same context is right."""
+    p = Problem(kv, new, 8, 2, 128, 32, dtype, seed=21)
+    base = p.call()
+    kda.testing_inject_wait_timeout(1)
+    p.call()
+    assert kda.get_device_error() == 4
+    again = p.call()
+    assert kda.get_device_error() == 0
+    for a, b in zip(base, again):
+        assert torch.equal(a, b)
+    p.check(*again)
