@@ -85,6 +85,12 @@ kda_status_t kda_cache_tables(int32_t page_size, int32_t num_seqs, int32_t max_b
     return KDA_ERR_INVALID_ARGUMENT;
   if (num_seqs > 0 && max_blocks > 0 && !block_table) return KDA_ERR_INVALID_ARGUMENT;
   if (max_tokens > 0 && !slots) return KDA_ERR_INVALID_ARGUMENT;
+  const void* words[] = {held_lens, seq_lens, new_lens, block_table, free_pages, kv_lens, cu_new};
+  const void* longs[] = {free_range, free_range_out, slots};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return KDA_ERR_INVALID_ARGUMENT;
+  for (const void* p : longs)
+    if (!aligned(p, 8)) return KDA_ERR_INVALID_ARGUMENT;
   const void* in[] = {held_lens, seq_lens, new_lens};
   const void* out[] = {cu_new, slots, block_table, free_pages, free_range_out};
   for (const void* o : out)
@@ -185,7 +191,9 @@ kda_status_t kda_cache_attention(const kda_cache_t* cache, const kda_attention_t
   if (!q || !kv_lens || !cu_new || !out || q == out) return KDA_ERR_INVALID_ARGUMENT;
   if (desc->max_blocks > 0 && !block_table) return KDA_ERR_INVALID_ARGUMENT;
   const uintptr_t size = desc->io_dtype == KDA_BF16 ? 2 : 4;
-  if (!aligned(q, size) || !aligned(out, 16) || !aligned(lse, 4)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, size) || !aligned(out, 16)) return KDA_ERR_INVALID_ARGUMENT;
+  if (!aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(cu_new, 4) || !aligned(lse, 4))
+    return KDA_ERR_INVALID_ARGUMENT;
   kda::AttentionArgs a;
   fill_attention(cache, desc, a);
   a.q = q;

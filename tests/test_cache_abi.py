@@ -202,3 +202,19 @@ def test_binding_refuses_broadcast_queries(lib, shape):
     lens, cu = torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="broadcast"):
         kda.cache_attention(q, cache, lens[None], lens, cu, max_new=1)
+
+
+@pytest.mark.parametrize("name,address", [
+    ("held", 0x1002), ("seq", 0x1002), ("new", 0x3001), ("table", 0x4002), ("free", 0x5002),
+    ("span", 0x6004), ("span_out", 0x6004), ("kv", 0x7002), ("cu", 0x8002), ("slots", 0x9004)])
+def test_tables_refuses_misaligned(lib, name, address):
+    assert _tables(lib, **{name: address}) == INVALID
+
+
+@pytest.mark.parametrize("which", [1, 2, 3])
+def test_attention_refuses_misaligned_tables(lib, which):
+    args = [FAKE, FAKE, FAKE, FAKE, OUT, None]
+    args[which] = ctypes.c_void_p(0x10002)
+    room = _desc(workspace=1 << 30, workspace_bytes=1 << 40)
+    assert lib.kda_cache_attention(ctypes.byref(_cache()), ctypes.byref(room), *args,
+                                   None) == INVALID
