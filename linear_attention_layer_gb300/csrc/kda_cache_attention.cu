@@ -773,9 +773,9 @@ struct Split {
     const int64_t es = sizeof(T);
     const int q_vec = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 &&
                       a.q_token_stride * es % 16 == 0 && a.q_head_stride * es % 16 == 0;
-    for (int seq0 = 0; seq0 < a.num_seqs; seq0 += kMaxSeqs) {
-      const int nseq = std::min(kMaxSeqs, a.num_seqs - seq0);
-      kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, seq0, nseq, range, parts, q_vec);
+    for (int64_t seq0 = 0; seq0 < a.num_seqs; seq0 += kMaxSeqs) {
+      const int nseq = (int)std::min<int64_t>(kMaxSeqs, a.num_seqs - seq0);
+      kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, (int)seq0, nseq, range, parts, q_vec);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
       e = launch_join<T, D, 1, 4>(c, a, parts.open, parts.o, parts.ml, sh.warp_slots(), ROWS, sh.ctas,
                                st);

@@ -67,7 +67,7 @@ template <typename P>
 __device__ __forceinline__ int find_last(const P* plan, int n, unsigned long long x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);
     if ((unsigned long long)plan[mid] <= x)
       lo = mid;
     else

@@ -104,13 +104,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(View c, AttentionArgs a, Row
   __shared__ unsigned long long sums[32];
   const int group = a.num_heads / c.kv_heads;
   unsigned long long at = 0, total;
-  for (int base = 0; base < a.num_seqs; base += 1024) {
-    const int b = base + threadIdx.x;
+  for (uint32_t base = 0; base < (uint32_t)a.num_seqs; base += 1024) {
+    const uint32_t b = base + threadIdx.x;
+    const bool in = b < (uint32_t)a.num_seqs;
     Request q;
-    const bool live = b < a.num_seqs && load_request(c, a, b, range, false, q);
+    const bool live = in && load_request(c, a, b, range, false, q);
     const unsigned long long n = live ? (q.rows + kRows - 1) / kRows : 0;
     const unsigned long long incl = scan1024(n, sums, total);
-    if (b < a.num_seqs) plan.first[b] = (int)min(at + incl - n, (unsigned long long)max_entries);
+    if (in) plan.first[b] = (int)min(at + incl - n, (unsigned long long)max_entries);
     at += total;
   }
   // ranges that overlap (malformed offsets) could ask for more entries than there is room for
@@ -118,10 +119,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(View c, AttentionArgs a, Row
   if (threadIdx.x == 0) plan.first[a.num_seqs] = entries;
   __syncthreads();
   unsigned long long tiles = 0;
-  for (int base = 0; base < entries; base += 1024) {
-    const int e = base + threadIdx.x;
+  for (uint32_t base = 0; base < (uint32_t)entries; base += 1024) {
+    const uint32_t e = base + threadIdx.x;
+    const bool in = e < (uint32_t)entries;
     unsigned long long n = 0;
-    if (e < entries) {
+    if (in) {
       const int b = find_last(plan.first, a.num_seqs, e);
       Request q;
       load_request(c, a, b, range, false, q);
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(View c, AttentionArgs a, Row
       plan.entry[e] = make_int2(b, r);
     }
     const unsigned long long incl = scan1024(n, sums, total);
-    if (e < entries) plan.tiles[e] = tiles + incl - n;
+    if (in) plan.tiles[e] = tiles + incl - n;
     tiles += total;
   }
   if (threadIdx.x == 0) plan.tiles[entries] = tiles;

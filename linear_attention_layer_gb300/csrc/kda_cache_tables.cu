@@ -16,6 +16,9 @@
 namespace kda {
 namespace {
 
+// Counters that step through the caller's sizes (each below 2^31) are unsigned: the step past the
+// last one does not fit 31 bits.
+
 // 256 requests' decode step / 37 with up to 1800 pages given back / 64 prompts, host included:
 // 9.6 / 12.3 / 14.3 us; with 256 threads 10.2 / 13.7 / 16.4, with 1024 10.3 / 12.3 / 14.5.
 constexpr int kThreads = 512;
@@ -66,7 +69,7 @@ __device__ __forceinline__ Counts block_scan(Counts x, Counts* warp_sums, Counts
 __device__ __forceinline__ int owner(const int32_t* at, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
+    const int mid = lo + ((hi - lo) >> 1);
     if (at[mid] <= x)
       lo = mid;
     else
@@ -109,9 +112,9 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write
   };
   int64_t tokens = 0, asked = 0, taken = 0, freed = 0;  // of the requests before this pass
   bool long_ones = false;
-  for (int base = 0; base < a.num_seqs; base += kThreads) {
-    const int b = base + threadIdx.x;
-    const bool in = b < a.num_seqs;
+  for (uint32_t base = 0; base < (uint32_t)a.num_seqs; base += kThreads) {
+    const uint32_t b = base + threadIdx.x;
+    const bool in = b < (uint32_t)a.num_seqs;
     const int held = in ? a.held_lens[b] : 0, seq = in ? a.seq_lens[b] : 0;
     const int fresh = in ? a.new_lens[b] : 0;
     const bool sound = held >= 0 && seq >= 0 && seq <= held && fresh >= -1 &&
@@ -150,12 +153,12 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(TableArgs a, int write
     }
     __syncthreads();
     // pages change hands, a thread each: what a request gives back may be thousands
-    for (int i = threadIdx.x; i < sum.freed(); i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < (uint32_t)sum.freed(); i += kThreads) {
       const int o = owner(ps.freed_at, kThreads, i);
       a.free_pages[in_ring(tail0 + freed + i)] =
           a.block_table[(int64_t)(base + o) * a.max_blocks + ps.from[o] + i - ps.freed_at[o]];
     }
-    for (int i = threadIdx.x; i < sum.taken(); i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < (uint32_t)sum.taken(); i += kThreads) {
       const int o = owner(ps.taken_at, kThreads, i);
       a.block_table[(int64_t)(base + o) * a.max_blocks + ps.from[o] + i - ps.taken_at[o]] =
           a.free_pages[in_ring(head0 + taken + i)];
@@ -206,14 +209,15 @@ __global__ void __launch_bounds__(256) slots_kernel(TableArgs a) {
   __syncthreads();
   const int32_t* offsets = here ? cu : a.cu_new;
   const int tokens = offsets[a.num_seqs];
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < a.max_tokens; i += gridDim.x * 256) {
-    if (i >= tokens) {
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < (uint32_t)a.max_tokens;
+       i += gridDim.x * 256) {
+    if (i >= (uint32_t)tokens) {
       a.slots[i] = -1;
       continue;
     }
     const int b = owner(offsets, a.num_seqs, i);
     const int first = offsets[b];
-    if (i != first) a.slots[i] = slot_of(a, b, i, first, offsets[b + 1] - first);
+    if (i != (uint32_t)first) a.slots[i] = slot_of(a, b, i, first, offsets[b + 1] - first);
   }
 }
 
@@ -232,7 +236,7 @@ cudaError_t launch_cache_tables(const TableArgs& a, cudaStream_t st) {
   if (cudaGetDevice(&dev) == cudaSuccess)
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min((a.max_tokens + 255) / 256, 4 * sms));
+  cfg.gridDim = dim3(std::min((a.max_tokens - 1) / 256 + 1, 4 * sms));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -71,3 +71,21 @@ def test_expired_wait_reports_timeout_and_recovers(dtype, kv, new):
     for a, b in zip(base, again):
         assert torch.equal(a, b)
     p.check(*again)
+
+
+# ------------------------------------------------------ 31-bit borders ---
+
+def test_tables_with_room_for_the_most_tokens():
+    """max_tokens = 2^31 - 1: counters that step past it do not wrap."""
+    P, most = 64, 2 ** 31 - 1
+    table = torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
+    ring = torch.tensor([4, 2, 0, 1, 3], dtype=torch.int32, device=DEV)
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    kv, cu, slots, span = kda.cache_tables(
+        zero, zero, torch.tensor([70, 9], dtype=torch.int32, device=DEV), table, ring,
+        torch.tensor([0, 5], device=DEV), page_size=P, max_tokens=most)
+    assert kv.tolist() == [70, 9] and cu.tolist() == [0, 70, 79] and span.tolist() == [3, 5]
+    want = list(range(4 * P, 5 * P)) + list(range(2 * P, 2 * P + 6)) + list(range(9))
+    assert slots.numel() == most and slots[:79].tolist() == want
+    for part in slots[79:].split(1 << 28):
+        assert bool((part == -1).all())
