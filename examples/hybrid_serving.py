@@ -63,7 +63,7 @@ class Server:
 
     def step(self, x, new, keep=None):
         """x [T, width]: the new tokens of the requests one after another, ``new`` of each
-        (-1: the request is over).  ``keep``: tokens of each that stay (default: all; fewer
+        (-1: the request is over, its slot free for another).  ``keep``: tokens of each that stay (default: all; fewer
         after drafts were rejected -- the KDA states are then the caller's to restore).
         Returns the outputs [T, width]."""
         m = self.model
@@ -77,6 +77,11 @@ class Server:
         offsets = [0]
         for n in count:
             offsets.append(offsets[-1] + n)
+        over = [b for b, n in enumerate(new) if n < 0]
+        if over:  # pages go back in cache_tables; a state stays until it is cleared
+            for states in self.states:
+                for state in states:
+                    state[over] = 0
         for layers, states, att, cache in zip(m.kda, self.states, m.attention, self.caches):
             for w, state in zip(layers, states):
                 x = x + self._kda(w, state, _norm(x), cu, offsets)

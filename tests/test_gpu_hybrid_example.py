@@ -54,3 +54,26 @@ def test_chunks_and_single_tokens_give_what_whole_prompts_give():
         y = torch.cat(got[b])
         rel = (y - want[b]).norm() / want[b].norm()
         assert rel <= 4e-2, (b, float(rel))
+
+
+def test_a_slot_is_clean_for_its_next_request():
+    """A request ends and another starts in its slot: its outputs are those of a server on which
+    the slot was never used, bit for bit: the same calls on the same values, in other pages."""
+    ex = _module()
+    model = ex.HybridModel(blocks=1)
+
+    def tokens(n):
+        return torch.randn((n, 512), device="cuda").to(torch.bfloat16)
+
+    first, other, second = tokens(50), [tokens(n) for n in (20, 1, 1, 1)], [tokens(33), tokens(1)]
+    used, fresh = (ex.Server(model, slots=2, pages=12, page_size=16, max_blocks=8)
+                   for _ in range(2))
+    used.step(torch.cat([first, other[0]]), [50, 20])
+    used.step(other[1], [-1, 1])
+    fresh.step(other[0], [0, 20])
+    fresh.step(other[1], [0, 1])
+    for i, n in enumerate((33, 1)):
+        a, b = (s.step(torch.cat([second[i], other[2 + i]]), [n, 1])[:n] for s in (used, fresh))
+        assert torch.equal(a, b), i
+    assert used.held.tolist() == fresh.held.tolist() == [34, 23]
+    assert kda.get_device_error() == 0
