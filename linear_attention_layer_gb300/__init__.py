@@ -950,6 +950,14 @@ def _native():
     return module
 
 
+def _on(stream, name, t):
+    """The context of a caller's stream, which has to be of the device that t is on (the
+    native calls take that device's current stream)."""
+    if stream.device != t.device:
+        raise ValueError(f"stream is of {stream.device}, {name} on {t.device}")
+    return torch.cuda.stream(stream)
+
+
 def _outputs(result, where):
     if result.__class__ is int:
         raise KDAError(result, where)
@@ -967,7 +975,7 @@ def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_ra
     [max_tokens], free_range_out [2]); kv_lens may be held_lens or seq_lens and
     free_range_out may be free_range, for a loop that updates in place."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, "held_lens", held_lens):
             return cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_range,
                                 page_size=page_size, max_tokens=max_tokens, kv_lens=kv_lens,
                                 cu_new=cu_new, slots=slots, free_range_out=free_range_out)
@@ -981,7 +989,7 @@ def cache_append(k, v, slots, cache, *, k_exponent=None, v_exponent=None, stream
     slices of a larger tensor will do, the channels contiguous) into ``cache`` at
     ``slots`` int64 [T] (-1 skips a token)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, "cache", cache):
             return cache_append(k, v, slots, cache, k_exponent=k_exponent, v_exponent=v_exponent)
     st = (_binding or _native()).append(k, v, slots, cache, k_exponent, v_exponent)
     if st != KDA_OK:
@@ -993,7 +1001,7 @@ def cache_read(slots, cache, dtype=torch.bfloat16, *, k_exponent=None, v_exponen
     """``kda_cache_read``: the values that ``cache`` holds at ``slots`` int64 [T], as
     (k, v) [T, kv heads, head_dim] of ``dtype`` (-1 reads as zeros)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, "cache", cache):
             return cache_read(slots, cache, dtype, k_exponent=k_exponent, v_exponent=v_exponent,
                               k=k, v=v)
     return _outputs((_binding or _native()).read(
@@ -1033,7 +1041,7 @@ def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=No
     the log-sum-exp [T, heads] fp32.  ``workspace``: a uint8 tensor of
     ``cache_attention_workspace_size`` bytes or "auto" (allocated here)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, "cache", cache):
             return cache_attention(q, cache, block_table, kv_lens, cu_new, max_new=max_new,
                                    scale=scale, k_exponent=k_exponent, v_exponent=v_exponent,
                                    out=out, return_lse=return_lse, lse=lse, workspace=workspace)

@@ -218,3 +218,22 @@ def test_attention_refuses_misaligned_tables(lib, which):
     room = _desc(workspace=1 << 30, workspace_bytes=1 << 40)
     assert lib.kda_cache_attention(ctypes.byref(_cache()), ctypes.byref(room), *args,
                                    None) == INVALID
+
+
+def test_binding_refuses_a_stream_of_another_device(lib):
+    """The calls run on the current stream of their tensors' device: a stream of another one
+    would be passed over without a word."""
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    cache = kda.cache_empty(1, 16, 2, 64, device="cpu")
+    lens, cu = torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    slots, x = torch.zeros(1, dtype=torch.int64), torch.zeros(1, 2, 64)
+    for call in (lambda s: kda.cache_tables(lens, lens, lens, lens[None], lens, slots,
+                                            page_size=16, max_tokens=1, stream=s),
+                 lambda s: kda.cache_append(x, x, slots, cache, stream=s),
+                 lambda s: kda.cache_read(slots, cache, stream=s),
+                 lambda s: kda.cache_attention(x, cache, lens[None], lens, cu, max_new=1,
+                                               stream=s)):
+        with pytest.raises(ValueError, match="stream is of cuda:1"):
+            call(Elsewhere())
