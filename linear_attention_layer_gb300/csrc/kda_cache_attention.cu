@@ -20,7 +20,8 @@
 // applies the E4M3 scale: code x scale has 6 significant bits, exact in a half.
 // q is scaled by a power of two per row (row_scale) and rounded to halves: bf16
 // fits exactly, fp32 goes in as two halves.  p is rounded to a half (2^-11, below
-// the output's own 2^-8), for fp32 outputs to two.  All sums are fp32.
+// the output's own 2^-8), for fp32 outputs to two, the second held 2^11 times
+// larger.  All sums are fp32.
 //
 // Work split.  The tiles of all units in one sequence are cut evenly over the
 // warps of the whole GPU, wherever that falls in a unit: lengths of any mix fill
@@ -141,6 +142,11 @@ __device__ __forceinline__ void store_row(T* p, const float (&x)[D / 8]) {
 // Halves of a query or weight: two for fp32 outputs, one for bf16.
 template <typename T>
 constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
+
+// The second half of a weight is held 2^11 times larger: 2^15 at most, and where the first half
+// has run out of exponent the second still has 2^-36, 2^-43 of the row's largest weight (held as
+// it is it ended at 2^-25: 40000 weights of 2^-33 behind one large one were lost).
+constexpr float kSecond = 2048.f;
 
 template <typename T, int D, int NT, int WARPS, int STAGES>
 struct Smem {
@@ -535,9 +541,10 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
             // zero (9000 keys: 5e-6 of an fp32 output).  Sums of 16 keys are added here, rounded;
             // the weights' second halves go first, where what is cut off is little.
             float part[4] = {0.f, 0.f, 0.f, 0.f};
+            tc::mma_16816_f16(part, af, pf[u][n][1][0], pf[u][n][1][1]);
 #pragma unroll
-            for (int e = TERMS - 1; e >= 0; --e)
-              tc::mma_16816_f16(part, af, pf[u][n][e][0], pf[u][n][e][1]);
+            for (int i = 0; i < 4; ++i) part[i] *= 1.f / kSecond;
+            tc::mma_16816_f16(part, af, pf[u][n][0][0], pf[u][n][0][1]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[wd * 4 + j][n][i] += part[i];
           }
@@ -644,8 +651,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
             pf[u][n][0][j] = tc::movmatrix_trans(hi);
             if constexpr (TERMS == 2) {
               const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-              pf[u][n][1][j] =
-                  tc::movmatrix_trans(tc::pack_f16(s[u][n][2 * j] - b.x, s[u][n][2 * j + 1] - b.y));
+              pf[u][n][1][j] = tc::movmatrix_trans(tc::pack_f16(
+                  (s[u][n][2 * j] - b.x) * kSecond, (s[u][n][2 * j + 1] - b.y) * kSecond));
             }
           }
         }

@@ -1,9 +1,11 @@
 """GPU tests of the 4-bit paged cache where a call is easily answered wrongly: unusual strides,
 long fp32 rows, weights far below the largest, hidden pages, waits that run out."""
+import numpy as np
 import pytest
 import torch
 
 import linear_attention_layer_gb300 as kda
+from oracle import paged_cache as pc
 from tests.test_gpu_cache import DEV, DTYPES, Problem, _device  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +91,46 @@ def test_tables_with_room_for_the_most_tokens():
     assert slots.numel() == most and slots[:79].tolist() == want
     for part in slots[79:].split(1 << 28):
         assert bool((part == -1).all())
+
+
+# ------------------------------------------------------- fp32 outputs ---
+
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 1), (64, 5), (128, 5)])
+def test_fp32_keeps_weights_far_below_the_largest(D, new):
+    """40000 keys of weight e^-23 = 2^-33.2 behind a dominant one whose values are zero in half of
+    the channels.  A weight is held in two halves, the second 2^11 times larger: 2^-11 of it, or
+    2^-36 where the row's largest has 2^7 at least, 2^-43 of it."""
+    L, Hq = 40000, 4
+    p = Problem([L], [new], Hq, 1, D, 64, torch.float32, seed=D)
+    k, v = np.zeros((L, 1, D)), np.ones((L, 1, D))
+    k[777, 0, 0] = 6.0  # an exact code
+    v[777, 0, : D // 2] = 0.0
+    raw = p.cache.cpu().numpy()
+    pos = np.arange(L)
+    pc.store(raw, p.table[0, pos // 64] * 64 + pos % 64, k, v)
+    p.cache = torch.tensor(raw, device=DEV)
+    v = pc.dequantise(*pc.quantise(v))
+    q = np.zeros((new, Hq, D))
+    q[..., 0] = 23.0 / 6.0 * D ** 0.5
+    p.q = torch.tensor(q, device=DEV).float()
+    out, lse = p.call()
+    want, z, mass, flat, size = pc.attention(p.q.double().cpu().numpy(), k, v, D ** -0.5)
+    assert (want[..., 0] > 4e-6).all() and (want[..., -1] > 0.9).all()
+    tol = 2.0 ** -24 * want + mass * (2.0 ** -21 + size[..., None] * 2.0 ** -16) + flat * 2.0 ** -43
+    worst = float((np.abs(out.double().cpu().numpy() - want) / tol).max())
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("D,new,Hq,Hk", [(128, 1, 4, 1), (64, 1, 3, 3), (128, 6, 2, 1), (64, 3, 8, 1)])
+def test_fp32_sums_of_a_long_row(D, new, Hq, Hk):
+    """The error of a whole request's outputs over 9000 keys, by its norm.  Weights are off by
+    2^-22 (two halves) and by their score's error, about 2^-24 of the magnitudes that it adds up
+    (its sums are rounded every 32 products): independent of the values' signs, so the outputs
+    are off by no more than that.  Sums left to the tensor cores, which cut off, were off by 6e-6,
+    queries or weights in one half by 5e-4."""
+    p = Problem([9001], [new], Hq, Hk, D, 64, torch.float32, seed=D + new)
+    out, lse = p.call()
+    p.check(out, lse)
+    want, z, mass, flat, size = pc.attention(p.q.double().cpu().numpy(), p.ks[0], p.vs[0], D ** -0.5)
+    err = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= 2.0 ** -22 + size.mean() * 2.0 ** -24, err
