@@ -749,8 +749,10 @@ kda_status_t kda_cache_read(const kda_cache_t* cache, int32_t io_dtype, int32_t 
  * Query head h reads kv head h / (num_heads / num_kv_heads).  One new token per
  * request is a decode step, a few are a drafted window, many a prefill chunk.
  * A row that sees no token (kv_lens[b] < n_b) gives zeros and the log-sum-exp
- * -infinity.  Scores, softmax statistics and sums are fp32; see the kernels for
- * the operands' types.  Bytes of a page past the request's length are not used,
+ * -infinity.  Scores, softmax statistics and sums are fp32 (scores of magnitude
+ * 2^27 or more, where fp32 steps by 8, give undefined outputs).  Weights enter
+ * the product with v as one fp16 for bf16 outputs -- 2^-11 of a weight, 2^-32 of
+ * the row's largest -- and as two for fp32 outputs, 2^-22 and 2^-43.  Bytes of a page past the request's length are not used,
  * whatever they are.
  *
  *   q             device, [total_tokens, num_heads, head_dim] io dtype, tokens

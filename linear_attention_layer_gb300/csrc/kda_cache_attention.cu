@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
               const float m = fmaxf(before, top * sf[n][e] - kLift);
               const float keep = ex2_approx(before - m);
               neg[n][e] = -m;
-              thr[n][e] = (m + (kLift + kSlack)) / sf[n][e];
+              thr[n][e] = score_limit(m, sf[n][e]);
               l[n][e] *= keep;
 #pragma unroll
               for (int i2 = 0; i2 < KM; ++i2) {

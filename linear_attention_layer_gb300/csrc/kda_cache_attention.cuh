@@ -95,6 +95,12 @@ __device__ __forceinline__ RowScale row_scale(float top, float scale, float k_fa
   return r;
 }
 
+// The raw score up to which a weight 2^(s f - m) stays within 2^(kLift + kSlack): rounded down, or
+// beside a reference of 2^24 and more a weight could pass a half's largest value.
+__device__ __forceinline__ float score_limit(float m, float f) {
+  return __fdiv_rd(__fadd_rd(m, kLift + kSlack), f);
+}
+
 // One row of a unit put together from parts i = first .. last, whose (m, l, o[D]) lie at
 // index at(i) of ml and o: by one warp, each lane with D / 32 neighbouring channels.  The
 // loads do not wait for one another.

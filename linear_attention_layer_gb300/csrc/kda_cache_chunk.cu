@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float m = fmaxf(before, top * f - kLift);
             keep = ex2_approx(before - m);
             neg = -m;
-            thr = (m + (kLift + kSlack)) / f;
+            thr = score_limit(m, f);
           }
           const uint64_t keep2 = tc::pack2(keep, keep);
           l2[0] = tc::fma2(l2[0], keep2, 0);

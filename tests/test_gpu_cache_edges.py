@@ -134,3 +134,36 @@ def test_fp32_sums_of_a_long_row(D, new, Hq, Hk):
     want, z, mass, flat, size = pc.attention(p.q.double().cpu().numpy(), p.ks[0], p.vs[0], D ** -0.5)
     err = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
     assert err <= 2.0 ** -22 + size.mean() * 2.0 ** -24, err
+
+
+# ------------------------------------------------------- large scores ---
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [1, 4, 60])
+def test_scores_of_tens_of_millions(dtype, new):
+    """Two keys whose scores lie 12 (in powers of two) apart at 3.4e7, where fp32 steps by 2 to
+    4, in different tiles of every request: beside a reference of this size the limit up to
+    which weights fit a half has to be rounded down.  The scores' common factor is off by 2^-23,
+    their difference with it."""
+    B, Hk, G, D, P, L, scale = 1000 if new < 60 else 64, 4, 2, 64, 64, 192, 22711.783203125
+    k, v = np.zeros((L, Hk, D)), np.zeros((L, Hk, D))
+    k[3, :, 0], k[100, :, 0] = 1536.0, 1536.0
+    k[100, :, 16], k[100, :, 17] = 3.0, 6.0  # the latter for the block's scale
+    v[3], v[100], v[50] = 6.0, 3.0, -6.0
+    v[100, :, ::16] = 6.0
+    raw = np.zeros((3, Hk, P // 16, 18 * D), np.uint8)
+    pos = np.arange(L)
+    pc.store(raw, pos, k, v)
+    q = torch.zeros((B * new, G * Hk, D), dtype=dtype, device=DEV)
+    q[..., 0], q[..., 16] = 1.0, 2.0 ** -13
+    ints = dict(dtype=torch.int32, device=DEV)
+    out = kda.cache_attention(
+        q, torch.tensor(raw, device=DEV), torch.tensor([[0, 1, 2]] * B, **ints),
+        torch.full((B,), L, **ints), torch.arange(0, (B + 1) * new, new, **ints), max_new=new,
+        scale=scale)
+    p = np.exp(-scale * 3 * 2.0 ** -13)
+    want = (p * v[3, 0] + v[100, 0]) / (1 + p)
+    step = 2.0 ** -8 + 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -24 + 2.0 ** -21
+    tol = want * (step + 12 * 2.0 ** -23)
+    worst = float((np.abs(out.double().cpu().numpy() - want) / tol).max())
+    assert worst <= 1, worst
