@@ -760,7 +760,7 @@ kda_status_t kda_cache_read(const kda_cache_t* cache, int32_t io_dtype, int32_t 
  *                 packed; one of them 0 is refused: a broadcast query has no
  *                 form here), channels contiguous
  *   block_table   device, [num_seqs][max_blocks] int32
- *   kv_lens       device, [num_seqs] int32
+ *   kv_lens       device, [num_seqs] int32, below 2^31 - 127
  *   cu_new        device, [num_seqs + 1] int32
  *   out           device, [total_tokens, num_heads, head_dim] io dtype, 16-byte
  *                 aligned; tokens past cu_new[num_seqs] are not written

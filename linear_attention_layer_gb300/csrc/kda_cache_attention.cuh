@@ -36,6 +36,9 @@ struct RowRange {
   int64_t above, up_to;
 };
 
+// Longest request: key numbers are rounded up to whole tiles in 31 bits.
+constexpr int kMostKeys = INT32_MAX - 127;
+
 // A request of the launch.
 struct Request {
   int kv, n, bos;
@@ -52,7 +55,7 @@ __device__ __forceinline__ bool load_request(const View& c, const AttentionArgs&
   r.rows = 0;
   r.n = 0;
   if (!ok) return false;
-  if (r.kv < 0 || r.kv > (int64_t)a.max_blocks * c.page_size) {
+  if (r.kv < 0 || r.kv > (int64_t)a.max_blocks * c.page_size || r.kv > kMostKeys) {
     if (report) report_error(a.err, kErrDeviceCheck);
     return false;
   }

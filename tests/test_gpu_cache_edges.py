@@ -93,6 +93,21 @@ def test_tables_with_room_for_the_most_tokens():
         assert bool((part == -1).all())
 
 
+@pytest.mark.parametrize("new", [1, 60])
+def test_lengths_that_round_up_past_31_bits_are_refused(new):
+    """A table of one page over and over may claim them; such a request is skipped."""
+    p = Problem([100], [new], 4, 2, 64, 32, torch.bfloat16)
+    cache = torch.zeros((1, 2, 256, 18 * 64), dtype=torch.uint8, device=DEV)
+    table = torch.zeros((1, 1 << 19), dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, new], dtype=torch.int32, device=DEV)
+    for kv in (2 ** 31 - 1, 2 ** 31 - 127):
+        out = torch.full_like(p.q, 3.0)
+        kda.cache_attention(p.q, cache, table, torch.tensor([kv], dtype=torch.int32, device=DEV),
+                            cu, max_new=new, out=out)
+        assert kda.get_device_error() == 5
+        assert bool((out == 3.0).all())
+
+
 # ------------------------------------------------------- fp32 outputs ---
 
 @pytest.mark.parametrize("D,new", [(64, 1), (128, 1), (64, 5), (128, 5)])
