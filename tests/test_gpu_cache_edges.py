@@ -182,3 +182,83 @@ def test_scores_of_tens_of_millions(dtype, new):
     tol = want * (step + 12 * 2.0 ** -23)
     worst = float((np.abs(out.double().cpu().numpy() - want) / tol).max())
     assert worst <= 1, worst
+
+
+# ------------------------------------------------- pages, workspaces, many ---
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [1, 5, 40])
+@pytest.mark.parametrize("page", [-1, 1 << 20])
+def test_rows_see_what_a_hidden_page_leaves(dtype, new, page):
+    """Values, row by row, of a request one page of which is not in the cache: a row sees the
+    tokens up to its own but for that page's."""
+    p = Problem([100, 90], [new, 1], 8, 2, 128, 32, dtype, seed=14)
+    table = p.table.copy()
+    table[0, 2] = page  # tokens 64 .. 95
+    out, lse = p.call(table=table)
+    assert kda.get_device_error() == 5
+    p.check(out, lse, only={1})
+    rows = Problem([1] * new, [1] * new, 8, 2, 128, 32, dtype)  # its check, a request a row
+    rows.q, ks, vs = p.q[:new], p.ks[0], p.vs[0]
+    keep = [np.r_[0:64, 96:100][: sum(t <= 100 - new + i for t in np.r_[0:64, 96:100])]
+            for i in range(new)]
+    rows.ks, rows.vs = [ks[k] for k in keep], [vs[k] for k in keep]
+    rows.kv = [len(k) for k in keep]
+    rows.check(out[:new], lse[:new])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_callers_workspace(new):
+    p = Problem([300, 70], [new, new], 8, 2, 128, 32, torch.bfloat16, seed=5)
+    base = p.call()
+    size = kda.cache_attention_workspace_size(p.cache, 2, 2 * new, 8, new, p.table.shape[1],
+                                              torch.bfloat16)
+    room = torch.full((size + 512,), 255, dtype=torch.uint8, device=DEV)
+    for a, b in zip(base, p.call(workspace=room[:size])):
+        assert torch.equal(a, b)
+    assert bool((room[size:] == 255).all())
+    for bad in (room[:size - 1], room[1:size + 1]):  # short; not 256-byte aligned
+        with pytest.raises(kda.KDAError):
+            p.call(workspace=bad)
+    for bad in (room[:size].view(torch.int8), room[::2], "none"):
+        with pytest.raises(ValueError):
+            p.call(workspace=bad)
+
+
+def test_many_requests_of_many_rows():
+    """More requests, and units of rows, than one pass of the chunk kernel's planner takes."""
+    rng = np.random.RandomState(4)
+    kv = list(map(int, rng.randint(0, 70, 1100)))
+    p = Problem(kv, [9] * len(kv), 32, 1, 64, 16, torch.bfloat16, seed=8)
+    p.check(*p.call(), only=set(range(0, 1100, 53)) | {1023, 1024, 1025, 1099})
+
+
+# -------------------------------------------------------------- rounding ---
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_every_bf16_value_under_every_scale(dtype):
+    """For each E4M3 scale, a block's largest value that gives it and all bf16 values up to that
+    one (from 2^-3 of the smallest code's border on; both signs), codes against fp64."""
+    bits = np.arange(0x7f80, dtype=np.uint32) << 16
+    every = bits.view(np.float32).astype(np.float64)
+    scale = pc.nearest(pc.E4M3, every / 6)
+    blocks = []
+    for sb in range(1, 127):
+        tops = every[scale == sb]
+        x = every[(every <= tops.max()) & (every >= pc.E4M3[sb] / 32)]
+        x = np.pad(x, (0, -len(x) % 14)).reshape(-1, 14)
+        top = np.resize(tops, len(x))
+        x = np.minimum(x, top[:, None])
+        blocks.append(np.concatenate([top[:, None], x, -x[:, :1]], 1))
+    blocks = np.concatenate(blocks)
+    blocks = np.pad(blocks, ((0, -len(blocks) % 4), (0, 0)))
+    blocks[:, 1::2] *= -1
+    k = blocks.reshape(-1, 1, 64)
+    slots = torch.arange(len(k), device=DEV)
+    cache = kda.cache_empty(-(-len(k) // 16), 16, 1, 64, DEV)
+    t = torch.tensor(k, device=DEV).to(dtype)
+    assert np.array_equal(t.double().cpu().numpy(), k)
+    kda.cache_append(t, -t, slots, cache)
+    kr, vr = kda.cache_read(slots, cache, dtype)
+    want = pc.dequantise(*pc.quantise(k))
+    assert np.array_equal(kr.double().cpu().numpy(), want) and torch.equal(kr, -vr)
