@@ -36,13 +36,6 @@ struct Layout {
   }
 };
 
-// First byte of the group that holds a slot's token.
-template <int D>
-__device__ __forceinline__ uint8_t* group_of(const View& c, int64_t page, int token, int head) {
-  const int64_t g = (page * c.kv_heads + head) * (c.page_size / kGroup) + token / kGroup;
-  return c.pages + g * Layout<D>::kGroupBytes;
-}
-
 // 2^e for a head's exponent, held to the documented range.
 __device__ __forceinline__ float exponent_scale(const int32_t* e, int head, int sign) {
   if (!e) return 1.f;

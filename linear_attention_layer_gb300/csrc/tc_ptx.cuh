@@ -210,16 +210,6 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uin
       : "memory");
 }
 
-// Registers a thread of this warpgroup, raised or lowered; all four warps call it.
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // True in one lane of a converged warp.  The compiler knows what follows it to run in a
 // single lane and keeps the operands of tcgen05.mma in uniform registers; under a plain
 // test of the lane number it moves them there with a loop over the lanes each time.
