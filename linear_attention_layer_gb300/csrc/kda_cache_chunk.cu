@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned long long x0 = min(per * blockIdx.x, total), x1 = min(x0 + per, total);
 
   // A wait that gives up tells the other warps, who give up as well.  A warp leaves its tiles
-  // when a vote, one a tile, finds a thread whose wait gave up; until then that thread goes on
-  // with whatever is there (a vote after each wait: 786 us for the chunk above).
+  // by a vote, at one place in a tile; until then a thread whose wait gave up goes on with
+  // whatever is there (a vote after each wait: 786 us for the chunk above).
   volatile int* failed = &sm.failed;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (wait_phase(bar, parity, a.wait_cycles, failed)) return true;
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float neg = 0.f, thr = -INFINITY;
       uint64_t l2[2] = {0, 0};  // the row's sum, in four parts
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
-        ok &= wait(&sm.s_full[blk], s_full.parity);
+        // a wait that gives up lowers the limit, so that the vote below is taken
+        if (!wait(&sm.s_full[blk], s_full.parity)) thr = -INFINITY;
         s_full.step();
         tc::tc_fence_after();
         float s[kKeys];
@@ -378,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = fmaxf(tc::max3(t4[0], s[kKeys - 4], s[kKeys - 3]),
                                 tc::max3(tc::max3(t4[1], t4[2], t4[3]), s[kKeys - 2], s[kKeys - 1]));
         bool waited = false;
-        if (__any_sync(0xffffffffu, top > thr || !ok)) {
-          ok = all_ok(ok);
+        if (__any_sync(0xffffffffu, top > thr)) {
+          ok = all_ok(!*failed);
           if (!ok) break;
           float keep = 1.f;
           if (top > -INFINITY) {
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2[1] = tc::fma2(l2[1], keep2, 0);
           if (j > p.begin) {
             // the product of the tile before has to be in O
-            ok = wait(&sm.o_full[blk], o_full.parity);
+            if (!wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY;
             tc::tc_fence_after();
             waited = true;
 #pragma unroll 1
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[i] = tc::pack_f16(p0, p1);
           }
           if (half == 0 && j > p.begin) {  // the product before has read its weights
-            if (!waited) ok &= wait(&sm.o_full[blk], o_full.parity);
+            if (!waited && !wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY;
             o_full.step();
             tc::tc_fence_after();
           }
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&sm.p_full[blk]);
       }
       // ---- end of the piece ----
-      ok = all_ok(ok && wait(&sm.o_full[blk], o_full.parity));
+      ok = all_ok(ok && wait(&sm.o_full[blk], o_full.parity) && !*failed);
       if (!ok) break;
       o_full.step();
       tc::tc_fence_after();
@@ -637,10 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           vs.step();
         }
       }
-      if (!ok) {  // products may be under way: they end before the tensor memory is given back
-        tc::mma_commit(&sm.issued);
-        wait_phase(&sm.issued, 0, a.wait_cycles, nullptr);
-      }
     }
     __syncwarp();
   } else {
@@ -692,12 +689,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (*failed && warp == 13) {  // the copies under way, of the last tiles, land
+  // After a wait gave up, what is under way ends before its memory goes away: the products (of
+  // the thread that elect.sync elects each time) and the copies of the last tiles.
+  if (*failed && warp == 12 && tc::elect_one()) {
+    tc::mma_commit(&sm.issued);
+    wait_phase(&sm.issued, 0, a.wait_cycles, nullptr);
+  }
+  if (*failed && warp == 13) {
     if (lane < a.withheld) tc::mbar_arrive(&sm.raw_full[0]);
     const uint32_t n = sm.copied;
     for (uint32_t i = n - min(n, (uint32_t)kRawStages); i < n; ++i)
       wait_phase(&sm.raw_full[i % kRawStages], i / kRawStages & 1, a.wait_cycles, nullptr);
   }
+  __syncwarp();
   if (warp == 12) tc::tmem_dealloc(tmem, kCols);
 }
 
