@@ -538,8 +538,8 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
             tc::mma_16816_f16(o[wd * 4 + j][n], af, pf[u][n][0][0], pf[u][n][0][1]);
           } else {
             // The tensor cores cut off what they add up; over a long row that drifts towards
-            // zero (9000 keys: 5e-6 of an fp32 output).  Sums of 16 keys are added here, rounded;
-            // the weights' second halves go first, where what is cut off is little.
+            // zero (9001 keys: 1e-5 of an fp32 output, so 5e-7).  Sums of 16 keys are added here,
+            // rounded; the weights' second halves go first, where what is cut off is little.
             float part[4] = {0.f, 0.f, 0.f, 0.f};
             tc::mma_16816_f16(part, af, pf[u][n][1][0], pf[u][n][1][1]);
 #pragma unroll

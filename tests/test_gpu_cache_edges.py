@@ -136,19 +136,25 @@ def test_fp32_keeps_weights_far_below_the_largest(D, new):
     assert worst <= 1, worst
 
 
-@pytest.mark.parametrize("D,new,Hq,Hk", [(128, 1, 4, 1), (64, 1, 3, 3), (128, 6, 2, 1), (64, 3, 8, 1)])
+@pytest.mark.parametrize("D,new,Hq,Hk", [(128, 1, 4, 2), (64, 1, 6, 3), (128, 6, 4, 2), (64, 3, 8, 2)])
 def test_fp32_sums_of_a_long_row(D, new, Hq, Hk):
-    """The error of a whole request's outputs over 9000 keys, by its norm.  Weights are off by
-    2^-22 (two halves) and by their score's error, about 2^-24 of the magnitudes that it adds up
-    (its sums are rounded every 32 products): independent of the values' signs, so the outputs
-    are off by no more than that.  Sums left to the tensor cores, which cut off, were off by 6e-6,
-    queries or weights in one half by 5e-4."""
+    """The error of a request's outputs over 9001 keys, by its norm, in a batch of 1000 (of one
+    request's tokens and queries over and over), where a warp adds up whole rows.  Weights are
+    off by 2^-22 (two halves) and by their score's error, about 2^-24 of the magnitudes that it
+    adds up (its sums are rounded every 32 products): independent of the values' signs, so the
+    outputs are off by no more than that.  Sums left to the tensor cores, which cut off, or
+    queries or weights in one half are off by more."""
+    B = 1000
     p = Problem([9001], [new], Hq, Hk, D, 64, torch.float32, seed=D + new)
-    out, lse = p.call()
-    p.check(out, lse)
     want, z, mass, flat, size = pc.attention(p.q.double().cpu().numpy(), p.ks[0], p.vs[0], D ** -0.5)
-    err = np.linalg.norm(out.double().cpu().numpy() - want) / np.linalg.norm(want)
-    assert err <= 2.0 ** -22 + size.mean() * 2.0 ** -24, err
+    ints = dict(dtype=torch.int32, device=DEV)
+    out = kda.cache_attention(p.q.repeat(B, 1, 1), p.cache,
+                              torch.tensor(p.table, **ints).repeat(B, 1),
+                              torch.full((B,), 9001, **ints),
+                              torch.arange(0, (B + 1) * new, new, **ints), max_new=new)
+    err = (out.double() - torch.tensor(want, device=DEV).repeat(B, 1, 1)).reshape(B, -1).norm(dim=1)
+    worst = float(err.max()) / np.linalg.norm(want)
+    assert worst <= 2.0 ** -22 + size.mean() * 2.0 ** -24, worst
 
 
 # ------------------------------------------------------- large scores ---
