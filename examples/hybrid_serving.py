@@ -1,4 +1,4 @@
-"""Serving a small hybrid model: three KDA layers, then one full-attention layer.
+"""Serving a small hybrid model: three KDA layers, then one layer of grouped-query attention.
 
 A KDA layer's memory of a request is a state of fixed size (fp32, updated in place); the
 attention layer's is the 4-bit paged cache.  One step of the server, whatever each request

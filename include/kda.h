@@ -622,12 +622,17 @@ kda_status_t kda_state_scan(const kda_desc_t* desc, int32_t count, const float* 
 /*
  * The 4-bit paged cache of the full-attention layers.
  *
- * The architecture puts one full-attention layer after every three KDA layers
- * (blog.higcp.com "猜想：K3 可能是最适合 TPU 的 MoE 架构", section "第七重").  A
- * KDA layer keeps a state of fixed size; an attention layer keeps the keys and
- * values of every token.  The calls below hold those in 4 bits -- E2M1 values
- * with one E4M3 scale per 16 channels, the main-KV format that
- * lishengnan.com/aichip names -- in pages handed out on the GPU:
+ * A hybrid model puts a full-attention layer after every few KDA layers.  A KDA
+ * layer keeps a state of fixed size; an attention layer keeps the keys and
+ * values of every token.  The calls below hold those of grouped-query attention
+ * with heads of 64 or 128 channels in 4 bits -- E2M1 values with one E4M3 scale
+ * per 16 channels -- in pages handed out on the GPU.  (The model of the pages
+ * that this library was built from interleaves its KDA layers three to one with
+ * Gated MLA, which caches a latent vector instead: blog.higcp.com "猜想：K3
+ * 可能是最适合 TPU 的 MoE 架构", section "第七重".  That layer is not built here.
+ * The format is the one that lishengnan.com/aichip names for another model's
+ * main KV cache.)
+ *
  *
  *   kda_cache_tables      block tables and slots from the requests' lengths
  *   kda_cache_append      new k, v quantised into their slots

@@ -2,15 +2,17 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``_lib/libkda.so``, reached through its C ABI (``include/kda.h``)
-with ctypes (the cache calls: with a native module, ``csrc/cache_binding.cpp``).  PyTorch supplies device memory and streams.  There is no CPU
-fallback: if the library is missing or a call fails, these functions raise.
+with ctypes (the cache calls: with a native module, ``csrc/cache_binding.cpp``).
+PyTorch supplies device memory and streams.  There is no CPU fallback: if the
+library is missing or a call fails, these functions raise.
 
 Entry points (same names as the C ABI, without the ``kda_`` prefix):
     chunk_fwd      -- chunked prefill over a packed variable-length batch
     recurrent_fwd  -- token-by-token prefill (the GPU reference path)
     decode_step    -- one token for each live request, state updated in place
     cache_tables, cache_append, cache_read, cache_attention
-                   -- the full-attention layers' 4-bit paged cache
+                   -- a 4-bit paged key/value cache for attention layers
+                      beside the KDA layers
 """
 from __future__ import annotations
 

@@ -31,11 +31,11 @@
 // second kernel.
 //
 // Measured (GB300; 32 query heads on 8 kv heads of 128, bf16).  256 requests of 256 to
-// 8192 tokens: 262 us for 1.27 GB, 0.73 of the measured HBM rate; 1 x 262144 tokens 70 us
-// (0.65), 1 x 2048 tokens 12.5 us.  What bounds it: the copies alone take 217 us, the
-// arithmetic alone 267.  A tile is 560 warp instructions and about 1000 cycles of a
-// quadrant: 128 conversions and 100 other integer instructions of 2 cycles, 128 half2
-// products of 2 beside them, and 32 products of 8 that do not run beside either.
+// 8192 tokens: 257 us for 1.27 GB, 0.74 of the measured HBM rate; 1 x 262144 tokens 68 us
+// (0.66), 1 x 2048 tokens 12.5 us.  What bounds it: the copies alone took 217 us, the
+// arithmetic alone 267 (the whole 262 then).  A tile is 560 warp instructions and about
+// 1000 cycles of a quadrant: 128 conversions and 100 other integer instructions of 2 cycles,
+// 128 half2 products of 2 beside them, and 32 products of 8 that do not run beside either.
 #include <math.h>
 
 #include <algorithm>
@@ -794,7 +794,7 @@ struct Split {
   }
 };
 
-// 12 warps of 160 registers a SM (three CTAs of four): the decode step above takes 262 us; 16
+// 12 warps of 160 registers a SM (three CTAs of four): the decode step above takes 257 us; 16
 // warps of 128 registers 278 to 281 (they spill), 8 warps 375.  Values of one tile and scores
 // of the next are interleaved in the source; without that 16 warps were as fast, not faster.
 //
@@ -823,7 +823,8 @@ auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
 // key is that of 128 rows, or 256, whatever their number.  67 windows with up to 40 rows,
 // three passes here: 172 us, with the requests of more than 32 rows over there 203 (they
 // are a fifth of the keys, and the second set of launches costs 15 us); a pass over all of
-// these keys takes 95 us here, the chunk kernel's only one 200, so four passes lose.
+// these keys takes 95 us here, the chunk kernel's only one 200, so four passes lose.  Measured
+// with 8 query heads on a kv head and 128 channels; other shapes go by the same number.
 constexpr int64_t kSplitRows = 48;
 
 size_t cache_attention_workspace_bytes(const View& c, const AttentionArgs& a) {

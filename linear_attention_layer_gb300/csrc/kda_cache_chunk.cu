@@ -32,8 +32,8 @@
 // per SM; parts of a unit are joined by a second kernel.  Units of one chunk differ in
 // length (causality), so a planner kernel sums them first.
 //
-// Measured: the chunk above takes 740 us, 1.44 PFLOP/s, 0.76 of the measured bf16 rate (this
-// kernel 714, the launches around it the rest); tensor pipe 64% busy.  A tile of both blocks
+// Measured: the chunk above takes 742 us, 1.44 PFLOP/s, 0.76 of the measured bf16 rate (this
+// kernel 722, the launches around it the rest); tensor pipe 63% busy.  A tile of both blocks
 // takes about 1600 cycles: 1152 of products, the rest waits for the softmax, whose two
 // warps a quadrant take about 1500 (64 exponentials a row and warp alone 256).
 #include <math.h>
