@@ -31,7 +31,7 @@
 // second kernel.
 //
 // Measured (GB300; 32 query heads on 8 kv heads of 128, bf16).  256 requests of 256 to
-// 8192 tokens: 257 us for 1.27 GB, 0.74 of the measured HBM rate; 1 x 262144 tokens 68 us
+// 8192 tokens: 257 to 260 us for 1.27 GB, 0.73 of the measured HBM rate; 1 x 262144 tokens 68 us
 // (0.66), 1 x 2048 tokens 12.5 us.  What bounds it: the copies alone took 217 us, the
 // arithmetic alone 267 (the whole 262 then).  A tile is 560 warp instructions and about
 // 1000 cycles of a quadrant: 128 conversions and 100 other integer instructions of 2 cycles,
