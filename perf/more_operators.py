@@ -386,10 +386,10 @@ def run(state):
     if own:
         import linear_attention_layer_gb300 as kda
         if op == "append8":
-            kda.cache8_append(state["k"], state["v"], state["slots"], state["cache"])
-            return kda.cache8_read(state["check"], state["cache"], state["k"].dtype)
+            kda.byte_cache_append(state["k"], state["v"], state["slots"], state["cache"])
+            return kda.byte_cache_read(state["check"], state["cache"], state["k"].dtype)
         if op == "attend8":
-            return kda.cache8_attention(state["q"], state["cache"], state["table"], state["kv"],
+            return kda.byte_cache_attention(state["q"], state["cache"], state["table"], state["kv"],
                                         state["cu"], max_new=state["max_new"], return_lse=True)
         if op == "fork":
             kv, table, copies, span = kda.cache_fork(
