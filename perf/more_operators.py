@@ -389,8 +389,9 @@ def run(state):
             kda.byte_cache_append(state["k"], state["v"], state["slots"], state["cache"])
             return kda.byte_cache_read(state["check"], state["cache"], state["k"].dtype)
         if op == "attend8":
-            return kda.byte_cache_attention(state["q"], state["cache"], state["table"], state["kv"],
-                                        state["cu"], max_new=state["max_new"], return_lse=True)
+            return kda.byte_cache_attention(
+                state["q"], state["cache"], state["table"], state["kv"], state["cu"],
+                max_new=state["max_new"], return_lse=True)
         if op == "fork":
             kv, table, copies, span = kda.cache_fork(
                 state["held"], state["table"], state["parents"], state["keep"], state["ring"],
