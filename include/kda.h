@@ -803,6 +803,184 @@ kda_status_t kda_cache_attention(const kda_cache_t* cache, const kda_attention_t
 kda_status_t kda_cache_attention_workspace_size(const kda_cache_t* cache,
                                                 const kda_attention_t* desc, size_t* bytes);
 
+/*
+ * The 8-bit form of that cache, for models that 4 bits are too few for.
+ *
+ *   kda_byte_cache_append     new k, v quantised into their slots
+ *   kda_byte_cache_read       the values at given slots
+ *   kda_byte_cache_attention  causal attention of new queries over the cache
+ *
+ * Block tables and slots are kda_cache_tables' and the same for both forms.
+ *
+ * Format.  A block is 16 neighbouring tokens of a kv head (slots 16 n .. 16 n + 15),
+ * its keys and its values apart: an exponent e and a code e4m3(x 2^-e) for each
+ * channel, rounded to nearest with ties to even, that stands for code * 2^e.  e is
+ * the least, from -100 to 119, with |x| <= 448 2^e for every x appended to the block
+ * (larger ones saturate); it rises as tokens come in, and the codes that the block
+ * holds are then taken along, e4m3(code 2^(e - e')), which changes a value only where
+ * it runs into E4M3's smallest numbers (below 2^-6 2^e').  A token at a block's first
+ * place begins it anew.
+ *
+ * Layout.  pages is [num_pages][num_kv_heads][page_size / 16][32 * head_dim + 16]
+ * bytes, D = head_dim.  A block's bytes, for token i = 0 .. 15 and channel c:
+ *     K code     byte  (c % (D/4)) / 16 * 1024 + 64 i + c / (D/4) * 16 + c % 16
+ *     V code     byte  16 D + (i/8*2 + i%2) 4 D + c / (D/8) * D/2 + (i%8)/2 * D/8 + c % (D/8)
+ *     exponents  byte  32 D: that of K plus 127; 32 D + 1: that of V plus 127
+ * and 14 bytes that are not used.
+ */
+typedef struct {
+  void* pages;          /* device, 16-byte aligned                      */
+  int32_t num_pages;    /* >= 0; num_pages * page_size < 2^31           */
+  int32_t page_size;    /* tokens per page: a multiple of 16, <= 4096   */
+  int32_t num_kv_heads; /* 1 .. 4096                                    */
+  int32_t head_dim;     /* 64 or 128                                    */
+} kda_byte_cache_t;
+
+/*
+ * kda_byte_cache_append -- k, v of num_tokens tokens, quantised into the cache.
+ *
+ *   k, v       device, [num_tokens, num_kv_heads, head_dim] io dtype; the
+ *              channels are contiguous, tokens and heads lie strides[0 .. 3]
+ *              elements apart: k's token, k's head, v's token, v's head stride
+ *              (32 bits; NULL: packed).  Any alignment of the dtype; 16-byte aligned
+ *              rows load faster.
+ *   slots      device, [num_tokens] int64, no slot twice; -1 skips a token.  The
+ *              tokens of one block stand next to one another in the batch, in any
+ *              order (kda_cache_tables gives a request's in rising order)
+ * A slot outside the cache is skipped and sets the device error word.  An
+ * infinity does not count for the exponent and is stored as the block's largest
+ * value of its sign, a NaN as zero; either sets the error word.
+ */
+kda_status_t kda_byte_cache_append(const kda_byte_cache_t* cache, int32_t io_dtype, int32_t num_tokens,
+                               const void* k, const void* v, const int64_t* strides,
+                               const int64_t* slots, kda_stream_t stream);
+
+/*
+ * kda_byte_cache_read -- the values that the cache holds at slots, written packed to k,
+ * v [num_tokens, num_kv_heads, head_dim] (io dtype, 16-byte aligned).  They have at
+ * most 4 significant bits, so bf16 holds them exactly.  Slot -1 reads as zeros; one
+ * outside the cache too, and sets the device error word.
+ */
+kda_status_t kda_byte_cache_read(const kda_byte_cache_t* cache, int32_t io_dtype, int32_t num_tokens,
+                             const int64_t* slots, void* k, void* v, kda_stream_t stream);
+
+/*
+ * kda_byte_cache_attention -- kda_cache_attention over the 8-bit cache: the same
+ * arguments, rows, masks, checks and outputs.  Scores, softmax statistics and sums
+ * are fp32.  A weight enters the product with v times 2^(e - E), e its block's
+ * exponent and E the largest of the request's that the row's part has met, as one
+ * fp16 for bf16 outputs (2^-11 of it, 2^-32 of the row's largest weight under E) and
+ * as two for fp32 outputs (2^-22 and 2^-43).  Values of magnitude below 2^80.
+ */
+kda_status_t kda_byte_cache_attention(const kda_byte_cache_t* cache, const kda_attention_t* desc,
+                                  const void* q, const int32_t* block_table,
+                                  const int32_t* kv_lens, const int32_t* cu_new, void* out,
+                                  float* lse, kda_stream_t stream);
+
+/* Bytes of device scratch that kda_byte_cache_attention needs for this descriptor
+ * (on the current device; the workspace fields are not read). */
+kda_status_t kda_byte_cache_attention_workspace_size(const kda_byte_cache_t* cache,
+                                                 const kda_attention_t* desc, size_t* bytes);
+
+/*
+ * Pages that several requests hold (several answers to one prompt, beams, a kept
+ * prefix), and pages moved.  The calls work on block tables as kda_cache_tables
+ * keeps them and on either form of the cache; who holds a page follows from the
+ * tables alone.  kda_cache_tables gives back pages whoever else holds them: end or
+ * cut requests that may share pages with kda_cache_fork.
+ *
+ *   kda_cache_fork      new rows from rows of the table; what nobody holds goes back
+ *   kda_cache_compact   the pages in use moved to the lowest numbers
+ *   kda_cache_copy      the copies that these two ask for, in every layer's cache
+ */
+
+/*
+ * kda_cache_fork -- a table whose rows continue rows of another.
+ *
+ * New row b holds the first keep_lens[b] <= held_lens[p] tokens of old row p =
+ * parents[b], in the same pages (parents[b] = -1: none).  A row may have any number
+ * of children, and one that has none ends.  Only an unfinished last page is written
+ * again: where keep_lens[b] ends inside a page that other new rows hold as well, the
+ * lowest of the rows that end inside it keeps it -- none, if some row holds more of it
+ * as a whole page -- and each other one gets a page from free_pages, in row order, and
+ * a copy to be made.  Pages that old rows held and no new row holds go back to
+ * free_pages, in rising order.
+ *
+ *   held_lens        device, [old_seqs] int32
+ *   block_table      device, [old_seqs][max_blocks] int32
+ *   parents, keep_lens   device, [num_seqs] int32
+ *   free_pages       device, [ring_size] int32, a ring as for kda_cache_tables, updated;
+ *                    ring_size >= num_pages
+ *   free_range       device, [2] int64
+ *   free_range_out   device, [2] int64, written; may be free_range
+ *   kv_lens          device, [num_seqs] int32, written: keep_lens[b]; may be held_lens,
+ *                    parents or keep_lens
+ *   block_table_out  device, [num_seqs][max_blocks] int32, written, -1 past a row's pages
+ *   copies           device, [num_seqs][3] int32, written: for row b the page to copy
+ *                    from, the page to copy to and the tokens in use, or -1, -1, 0
+ *   workspace        device, 256-byte aligned, kda_cache_fork_workspace_size bytes
+ *
+ * Checked on the device (KDA_ERR_DEVICE_CHECK in the error word): a row whose parent
+ * or length is out of range keeps nothing; one that no page is left for (and those
+ * after it that need one) ends with its last whole page.  An old row of negative
+ * length or of more tokens than its row has room for keeps its pages and has no
+ * children; a page index outside the cache is passed on as it is.
+ * old_seqs * max_blocks and num_seqs * max_blocks < 2^31 (else KDA_ERR_UNSUPPORTED).
+ */
+kda_status_t kda_cache_fork(int32_t page_size, int32_t num_pages, int32_t old_seqs,
+                            int32_t num_seqs, int32_t max_blocks, int32_t ring_size,
+                            const int32_t* held_lens, const int32_t* block_table,
+                            const int32_t* parents, const int32_t* keep_lens, int32_t* free_pages,
+                            const int64_t* free_range, int64_t* free_range_out, int32_t* kv_lens,
+                            int32_t* block_table_out, int32_t* copies, void* workspace,
+                            size_t workspace_bytes, kda_stream_t stream);
+kda_status_t kda_cache_fork_workspace_size(int32_t num_pages, int32_t num_seqs, size_t* bytes);
+
+/*
+ * kda_cache_compact -- the pages that rows hold, L of them, moved to 0 .. L - 1, so
+ * that a cache can go on in fewer pages.
+ *
+ * Pages below L that are in use stay; the i-th one in use from L on moves to the i-th
+ * free one below L.  All other pages are free afterwards: the ring holds L ..
+ * num_pages - 1, in order, from its first entry on.
+ *
+ *   held_lens        device, [num_seqs] int32
+ *   block_table      device, [num_seqs][max_blocks] int32
+ *   block_table_out  device, the same shape, written, -1 past a row's pages; may be
+ *                    block_table
+ *   copies           device, [num_pages / 2][3] int32, written: the moves (from, to,
+ *                    page_size), then -1, -1, 0
+ *   free_pages       device, [ring_size] int32, written; ring_size >= num_pages
+ *   free_range_out   device, [2] int64, written: 0, num_pages - L
+ *   workspace        device, 256-byte aligned, kda_cache_compact_workspace_size bytes
+ *
+ * Checked on the device: a row of negative length or of more tokens than it has room
+ * for holds nothing; a page index outside the cache is passed on as it is.
+ */
+kda_status_t kda_cache_compact(int32_t page_size, int32_t num_pages, int32_t num_seqs,
+                               int32_t max_blocks, int32_t ring_size, const int32_t* held_lens,
+                               const int32_t* block_table, int32_t* block_table_out,
+                               int32_t* copies, int32_t* free_pages, int64_t* free_range_out,
+                               void* workspace, size_t workspace_bytes, kda_stream_t stream);
+kda_status_t kda_cache_compact_workspace_size(int32_t num_pages, size_t* bytes);
+
+/*
+ * kda_cache_copy -- pages copied inside each of num_layers caches of one shape, of
+ * either form: for every (from, to, tokens) of copies the first tokens of page from,
+ * rounded up to 16, to page to.  A from of -1 or no tokens: nothing.  No page may be
+ * copied to twice, or both to and from.
+ *
+ *   pages        host array of num_layers device pointers, 16-byte aligned
+ *   group_bytes  bytes of 16 tokens of a kv head: 18 * head_dim (4 bits) or
+ *                32 * head_dim + 16 (8 bits)
+ *   copies       device, [num_copies][3] int32
+ * A copy with a page or a number of tokens out of range is skipped and sets the
+ * device error word.
+ */
+kda_status_t kda_cache_copy(int32_t num_layers, void* const* pages, int32_t num_pages,
+                            int32_t num_kv_heads, int32_t page_size, int32_t group_bytes,
+                            int32_t num_copies, const int32_t* copies, kda_stream_t stream);
+
 const char* kda_status_string(kda_status_t status);
 
 /* Synchronise `stream`, then read and clear the device error word of the

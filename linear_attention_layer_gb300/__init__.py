@@ -13,6 +13,10 @@ Entry points (same names as the C ABI, without the ``kda_`` prefix):
     cache_tables, cache_append, cache_read, cache_attention
                    -- a 4-bit paged key/value cache for attention layers
                       beside the KDA layers
+    byte_cache_append, byte_cache_read, byte_cache_attention
+                   -- its 8-bit form
+    cache_fork, cache_compact, cache_copy
+                   -- pages that several requests hold, and pages moved
 """
 from __future__ import annotations
 
@@ -31,8 +35,10 @@ __all__ = ["chunk_fwd", "chunk_fwd_noalloc", "recurrent_fwd", "decode_step",
            "chunk_fwd_summary_workspace_size", "state_scan", "decode_step_fused",
            "decode_replay_window_fused", "chunk_fwd_fused", "chunk_bwd",
            "chunk_bwd_workspace_size", "cache_empty", "cache_tables", "cache_append",
-           "cache_read", "cache_attention", "cache_attention_workspace_size",
-           "EXPORTED_SYMBOLS"]
+           "cache_read", "cache_attention", "cache_attention_workspace_size", "byte_cache_empty",
+           "byte_cache_append", "byte_cache_read", "byte_cache_attention", "byte_cache_attention_workspace_size",
+           "cache_fork", "cache_fork_workspace_size", "cache_compact",
+           "cache_compact_workspace_size", "cache_copy", "EXPORTED_SYMBOLS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libkda.so")
 
@@ -53,7 +59,11 @@ EXPORTED_SYMBOLS = ("kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_recurr
                     "kda_decode_replay_window_fused", "kda_chunk_fwd_fused", "kda_chunk_bwd",
                     "kda_chunk_bwd_workspace_size", "kda_cache_tables", "kda_cache_append",
                     "kda_cache_read", "kda_cache_attention",
-                    "kda_cache_attention_workspace_size")
+                    "kda_cache_attention_workspace_size", "kda_byte_cache_append",
+                    "kda_byte_cache_read", "kda_byte_cache_attention",
+                    "kda_byte_cache_attention_workspace_size", "kda_cache_fork",
+                    "kda_cache_fork_workspace_size", "kda_cache_compact",
+                    "kda_cache_compact_workspace_size", "kda_cache_copy")
 
 #: Size of the library's own scratch array used by chunk_fwd_noalloc
 #: (KDA_NOALLOC_SCRATCH_BYTES in include/kda.h).
@@ -88,6 +98,12 @@ class KdaCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("k_exponent", ctypes.c_void_p),
                 ("v_exponent", ctypes.c_void_p)]
+
+
+class KdaByteCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 class KdaAttention(ctypes.Structure):
@@ -162,6 +178,25 @@ def load() -> ctypes.CDLL:
         lib.kda_cache_attention_workspace_size.restype = ctypes.c_int
         lib.kda_cache_attention_workspace_size.argtypes = [cp, ap,
                                                            ctypes.POINTER(ctypes.c_size_t)]
+        cp8, size_p = ctypes.POINTER(KdaByteCache), ctypes.POINTER(ctypes.c_size_t)
+        lib.kda_byte_cache_append.restype = ctypes.c_int
+        lib.kda_byte_cache_append.argtypes = [cp8, i32, i32] + [vp] * 5
+        lib.kda_byte_cache_read.restype = ctypes.c_int
+        lib.kda_byte_cache_read.argtypes = [cp8, i32, i32] + [vp] * 4
+        lib.kda_byte_cache_attention.restype = ctypes.c_int
+        lib.kda_byte_cache_attention.argtypes = [cp8, ap] + [vp] * 7
+        lib.kda_byte_cache_attention_workspace_size.restype = ctypes.c_int
+        lib.kda_byte_cache_attention_workspace_size.argtypes = [cp8, ap, size_p]
+        lib.kda_cache_fork.restype = ctypes.c_int
+        lib.kda_cache_fork.argtypes = [i32] * 6 + [vp] * 11 + [ctypes.c_size_t, vp]
+        lib.kda_cache_fork_workspace_size.restype = ctypes.c_int
+        lib.kda_cache_fork_workspace_size.argtypes = [i32, i32, size_p]
+        lib.kda_cache_compact.restype = ctypes.c_int
+        lib.kda_cache_compact.argtypes = [i32] * 5 + [vp] * 7 + [ctypes.c_size_t, vp]
+        lib.kda_cache_compact_workspace_size.restype = ctypes.c_int
+        lib.kda_cache_compact_workspace_size.argtypes = [i32, size_p]
+        lib.kda_cache_copy.restype = ctypes.c_int
+        lib.kda_cache_copy.argtypes = [i32, ctypes.POINTER(vp)] + [i32] * 5 + [vp, vp]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_status_string.argtypes = [ctypes.c_int]
         lib.kda_testing_inject_wait_timeout.restype = None
@@ -1054,3 +1089,155 @@ def cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=No
     return _outputs((_binding or _native()).attention(
         q, cache, block_table, kv_lens, cu_new, max_new, scale, k_exponent, v_exponent, out, lse,
         bool(return_lse), workspace), "kda_cache_attention")
+
+
+# ------------------------------------------------- the 8-bit paged cache ---
+
+def byte_cache_empty(num_pages, page_size, num_kv_heads, head_dim, device="cuda"):
+    """A cache of the 8-bit form for one attention layer: uint8 [num_pages,
+    num_kv_heads, page_size / 16, 32 * head_dim + 16] (byte layout in
+    include/kda.h): E4M3 codes and a power of two for the keys and for the values
+    of each 16 tokens and head.  The contents are undefined until appended."""
+    if page_size <= 0 or page_size % 16 or page_size > 4096:
+        raise ValueError(f"page_size must be a multiple of 16 up to 4096, got {page_size}")
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    return torch.empty((num_pages, num_kv_heads, page_size // 16, 32 * head_dim + 16),
+                       dtype=torch.uint8, device=device)
+
+
+def byte_cache_append(k, v, slots, cache, *, stream=None):
+    """``kda_byte_cache_append``: quantise k, v [T, kv heads, head_dim] (fp32 or bf16;
+    slices of a larger tensor will do, the channels contiguous) into ``cache`` at
+    ``slots`` int64 [T] (-1 skips a token).  Tokens of the same 16 slots stand next
+    to one another, as ``cache_tables`` gives them; one that raises its block's
+    exponent takes the codes along that the block holds."""
+    if stream is not None:
+        with _on(stream, "cache", cache):
+            return byte_cache_append(k, v, slots, cache)
+    st = (_binding or _native()).append8(k, v, slots, cache)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_byte_cache_append")
+
+
+def byte_cache_read(slots, cache, dtype=torch.bfloat16, *, k=None, v=None, stream=None):
+    """``kda_byte_cache_read``: the values that ``cache`` holds at ``slots`` int64 [T], as
+    (k, v) [T, kv heads, head_dim] of ``dtype`` (-1 reads as zeros)."""
+    if stream is not None:
+        with _on(stream, "cache", cache):
+            return byte_cache_read(slots, cache, dtype, k=k, v=v)
+    return _outputs((_binding or _native()).read8(slots, cache, _io_code(dtype) == KDA_BF16, k, v),
+                    "kda_byte_cache_read")
+
+
+def byte_cache_attention_workspace_size(cache, num_seqs, total_tokens, num_heads, max_new, max_blocks,
+                                    dtype):
+    """Bytes of device scratch that ``byte_cache_attention`` needs for calls of this shape."""
+    _check_tensor("cache", cache, torch.uint8, cache.shape, cache.device)
+    if cache.dim() != 4 or cache.shape[3] % 32 != 16:
+        raise ValueError("cache must be uint8 [num_pages, kv heads, page_size / 16, "
+                         f"32 head_dim + 16], got {tuple(cache.shape)}")
+    c = KdaByteCache(cache.data_ptr(), cache.shape[0], cache.shape[2] * 16, cache.shape[1],
+                  cache.shape[3] // 32)
+    d = KdaAttention(int(num_seqs), int(total_tokens), int(num_heads), int(max_new),
+                     int(max_blocks), _io_code(dtype), 1.0)
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(cache.device):
+        st = load().kda_byte_cache_attention_workspace_size(c, d, ctypes.byref(n))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_byte_cache_attention_workspace_size")
+    return int(n.value)
+
+
+def byte_cache_attention(q, cache, block_table, kv_lens, cu_new, *, max_new, scale=None, out=None,
+                     return_lse=False, lse=None, workspace="auto", stream=None):
+    """``kda_byte_cache_attention``: ``cache_attention`` over a cache of the 8-bit form."""
+    if stream is not None:
+        with _on(stream, "cache", cache):
+            return byte_cache_attention(q, cache, block_table, kv_lens, cu_new, max_new=max_new,
+                                    scale=scale, out=out, return_lse=return_lse, lse=lse,
+                                    workspace=workspace)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be a tensor or 'auto'")
+        workspace = None
+    return _outputs((_binding or _native()).attention8(
+        q, cache, block_table, kv_lens, cu_new, max_new, scale, out, lse, bool(return_lse),
+        workspace), "kda_byte_cache_attention")
+
+
+# ------------------------------------------- pages that several rows hold ---
+
+def cache_fork(held_lens, block_table, parents, keep_lens, free_pages, free_range, *, page_size,
+               num_pages, kv_lens=None, block_table_out=None, copies=None, free_range_out=None,
+               workspace=None, stream=None):
+    """``kda_cache_fork``: rows that continue rows of ``block_table`` int32 [B,
+    max_blocks], which hold held_lens int32 [B] tokens.  New row b keeps the first
+    keep_lens[b] tokens of row parents[b] (int32 [R]; -1: an empty row) in the same
+    pages; pages that no new row holds go back to ``free_pages`` (int32, updated).
+    Returns (kv_lens [R], block_table [R, max_blocks], copies [R, 3],
+    free_range_out [2]): ``cache_copy(caches, copies)`` then fills the pages of rows
+    that would go on writing into a page that another row holds.  Serves for
+    several answers to a prompt, beams, kept prefixes, and to end or cut requests
+    that share pages.  ``workspace``: a uint8 tensor of
+    ``cache_fork_workspace_size`` bytes, else allocated here."""
+    if stream is not None:
+        with _on(stream, "held_lens", held_lens):
+            return cache_fork(held_lens, block_table, parents, keep_lens, free_pages, free_range,
+                              page_size=page_size, num_pages=num_pages, kv_lens=kv_lens,
+                              block_table_out=block_table_out, copies=copies,
+                              free_range_out=free_range_out, workspace=workspace)
+    return _outputs((_binding or _native()).fork(
+        held_lens, block_table, parents, keep_lens, free_pages, free_range, page_size, num_pages,
+        kv_lens, block_table_out, copies, free_range_out, workspace), "kda_cache_fork")
+
+
+def cache_fork_workspace_size(num_pages, num_seqs):
+    """Bytes of device scratch that ``cache_fork`` needs for so many pages and new rows."""
+    n = ctypes.c_size_t(0)
+    st = load().kda_cache_fork_workspace_size(int(num_pages), int(num_seqs), ctypes.byref(n))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_fork_workspace_size")
+    return int(n.value)
+
+
+def cache_compact(held_lens, block_table, free_pages, *, page_size, num_pages,
+                  block_table_out=None, copies=None, free_range_out=None, workspace=None,
+                  stream=None):
+    """``kda_cache_compact``: the L pages that the rows of ``block_table`` int32 [B,
+    max_blocks] hold (held_lens int32 [B] tokens) moved to 0 .. L - 1; all others
+    are free afterwards and fill ``free_pages`` (int32) from its first entry on.
+    Returns (block_table, copies [num_pages / 2, 3], free_range [2]), the moves to
+    be made by ``cache_copy(caches, copies)``; block_table_out may be block_table.
+    ``workspace``: a uint8 tensor of ``cache_compact_workspace_size`` bytes, else
+    allocated here."""
+    if stream is not None:
+        with _on(stream, "held_lens", held_lens):
+            return cache_compact(held_lens, block_table, free_pages, page_size=page_size,
+                                 num_pages=num_pages, block_table_out=block_table_out,
+                                 copies=copies, free_range_out=free_range_out, workspace=workspace)
+    return _outputs((_binding or _native()).compact(
+        held_lens, block_table, free_pages, page_size, num_pages, block_table_out, copies,
+        free_range_out, workspace), "kda_cache_compact")
+
+
+def cache_compact_workspace_size(num_pages):
+    """Bytes of device scratch that ``cache_compact`` needs for so many pages."""
+    n = ctypes.c_size_t(0)
+    st = load().kda_cache_compact_workspace_size(int(num_pages), ctypes.byref(n))
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_compact_workspace_size")
+    return int(n.value)
+
+
+def cache_copy(caches, copies, *, stream=None):
+    """``kda_cache_copy``: the copies int32 [n, 3] (from, to, tokens) of ``cache_fork``
+    or ``cache_compact``, made in each of ``caches``: one cache of either form or a
+    list of the layers', all of one shape."""
+    if stream is not None:
+        with _on(stream, "copies", copies):
+            return cache_copy(caches, copies)
+    st = (_binding or _native()).copy(
+        (caches,) if isinstance(caches, torch.Tensor) else tuple(caches), copies)
+    if st != KDA_OK:
+        raise KDAError(st, "kda_cache_copy")

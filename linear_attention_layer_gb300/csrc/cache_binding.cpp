@@ -13,6 +13,7 @@
 
 #include <cmath>
 #include <sstream>
+#include <vector>
 
 #include "../../include/kda.h"
 
@@ -297,11 +298,261 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A cache of the 8-bit form.
+c10::Device byte_cache_struct(PyObject* cache, kda_byte_cache_t& c) {
+  const Tensor& t = tensor(cache, "cache");
+  if (!t.is_cuda()) REFUSE("cache must be on a CUDA device, got " << t.device());
+  if (t.dim() != 4 || t.size(3) % 32 != 16)
+    REFUSE("cache must be uint8 [num_pages, kv heads, page_size / 16, 32 head_dim + 16], got "
+           << t.sizes());
+  for (int i = 0; i < 4; ++i)
+    if (t.size(i) > (1 << 30)) REFUSE("cache is too large: " << t.sizes());
+  c.pages = need<void>(cache, "cache", ScalarType::Byte, t.sizes(), t.device());
+  c.num_pages = (int32_t)t.size(0);
+  c.num_kv_heads = (int32_t)t.size(1);
+  c.page_size = (int32_t)(t.size(2) > 4096 ? -1 : t.size(2) * 16);
+  c.head_dim = (int32_t)(t.size(3) / 32);
+  return t.device();
+}
+
+// k, v, slots, cache
+PyObject* append8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 4);
+  kda_byte_cache_t c;
+  const c10::Device dev = byte_cache_struct(a[3], c);
+  const int64_t T = tensor(a[2], "slots").numel();
+  const int64_t shape[] = {T, c.num_kv_heads, c.head_dim}, slots_shape[] = {T};
+  if (T > INT32_MAX) REFUSE("more tokens than 32 bits count");
+  const ScalarType type = tensor(a[0], "k").scalar_type();
+  const int32_t io = io_code(type);
+  const Tensor &k = rows(a[0], "k", type, shape, dev), &v = rows(a[1], "v", type, shape, dev);
+  const int64_t* slots = need<int64_t>(a[2], "slots", ScalarType::Long, slots_shape, dev);
+  int64_t strides[4];
+  outer_strides(k, strides);
+  outer_strides(v, strides + 2);
+  const c10::cuda::CUDAGuard guard(dev);
+  return status_object(kda_byte_cache_append(&c, io, (int32_t)T, k.data_ptr(), v.data_ptr(), strides,
+                                         slots, stream_of(dev)));
+  END_HANDLE_TH_ERRORS
+}
+
+// slots, cache, is_bf16, k, v
+PyObject* read8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 5);
+  kda_byte_cache_t c;
+  const c10::Device dev = byte_cache_struct(a[1], c);
+  const ScalarType type = a[2] == Py_True ? ScalarType::BFloat16 : ScalarType::Float;
+  const int64_t T = tensor(a[0], "slots").numel();
+  if (T > INT32_MAX) REFUSE("more tokens than 32 bits count");
+  const int64_t shape[] = {T, c.num_kv_heads, c.head_dim}, slots_shape[] = {T};
+  const int64_t* slots = need<int64_t>(a[0], "slots", ScalarType::Long, slots_shape, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  Tensor k, v;
+  void* kp = output<void>(a[3], "k", type, shape, dev, k);
+  void* vp = output<void>(a[4], "v", type, shape, dev, v);
+  const kda_status_t st =
+      kda_byte_cache_read(&c, io_code(type), (int32_t)T, slots, kp, vp, stream_of(dev));
+  if (st != KDA_OK) return status_object(st);
+  return tuple_of({k, v});
+  END_HANDLE_TH_ERRORS
+}
+
+// Device scratch: the caller's, or new when it gave none.
+void* scratch(PyObject* o, size_t bytes, c10::Device dev, Tensor& keep, size_t& have) {
+  if (o == Py_None) {
+    const int64_t size[] = {(int64_t)bytes};
+    keep = at::detail::empty_cuda(size, ScalarType::Byte, dev, std::nullopt);
+  } else {
+    keep = tensor(o, "workspace");
+    const int64_t size[] = {keep.numel()};
+    need<void>(o, "workspace", ScalarType::Byte, size, dev);
+  }
+  have = (size_t)keep.numel();
+  return keep.data_ptr();
+}
+
+// The same over the 8-bit form: q, cache, block_table, kv_lens, cu_new, max_new, scale (or None),
+// out, lse, want_lse, workspace (None: allocated here)
+PyObject* attention8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 11);
+  const Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "block_table");
+  if (q.dim() != 3 || table.dim() != 2)
+    REFUSE("q must be [T, heads, head_dim] and block_table [B, max_blocks]");
+  kda_attention_t d = {};
+  query_strides(q, d.q_strides);
+  kda_byte_cache_t c;
+  const c10::Device dev = byte_cache_struct(a[1], c);
+  const int64_t T = q.size(0), H = q.size(1), D = q.size(2), blocks = table.size(1),
+                B = tensor(a[3], "kv_lens").numel();
+  if (D != c.head_dim || c.num_kv_heads <= 0 || H % c.num_kv_heads != 0)
+    REFUSE("q " << q.sizes() << " does not fit a cache of " << c.num_kv_heads << " heads of "
+                << c.head_dim << " channels");
+  if (T > INT32_MAX || H > INT32_MAX || B > INT32_MAX || blocks > INT32_MAX)
+    REFUSE("more tokens, heads, requests or columns than 32 bits count");
+  const int64_t shape[] = {T, H, D}, table_shape[] = {B, blocks}, lens[] = {B}, cu_shape[] = {B + 1},
+                lse_shape[] = {T, H};
+  const ScalarType type = q.scalar_type();
+  constexpr ScalarType I = ScalarType::Int;
+  d.io_dtype = io_code(type);
+  rows(a[0], "q", type, shape, dev);
+  d.num_seqs = (int32_t)B;
+  d.total_tokens = (int32_t)T;
+  d.num_heads = (int32_t)H;
+  d.max_new = (int32_t)integer(a[5], "max_new");
+  d.max_blocks = (int32_t)blocks;
+  if (a[6] == Py_None) {
+    d.scale = (float)(1.0 / std::sqrt((double)D));
+  } else {
+    const double s = PyFloat_AsDouble(a[6]);
+    if (s == -1.0 && PyErr_Occurred()) throw python_error();
+    d.scale = (float)s;
+  }
+  const int32_t* table_p = need<int32_t>(a[2], "block_table", I, table_shape, dev);
+  const int32_t* kv_p = need<int32_t>(a[3], "kv_lens", I, lens, dev);
+  const int32_t* cu_p = need<int32_t>(a[4], "cu_new", I, cu_shape, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  size_t bytes = 0;
+  kda_status_t st = kda_byte_cache_attention_workspace_size(&c, &d, &bytes);
+  if (st != KDA_OK) return status_object(st);
+  Tensor out, lse, ws;
+  void* out_p = output<void>(a[7], "out", type, shape, dev, out);
+  const bool with_lse = a[9] == Py_True || a[8] != Py_None;
+  float* lse_p =
+      with_lse ? output<float>(a[8], "lse", ScalarType::Float, lse_shape, dev, lse) : nullptr;
+  d.workspace = scratch(a[10], bytes, dev, ws, d.workspace_bytes);
+  st = kda_byte_cache_attention(&c, &d, q.data_ptr(), table_p, kv_p, cu_p, out_p, lse_p, stream_of(dev));
+  if (st != KDA_OK) return status_object(st);
+  if (a[9] == Py_True) return tuple_of({out, lse});
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// held_lens, block_table, parents, keep_lens, free_pages, free_range, page_size, num_pages,
+// kv_lens, block_table_out, copies, free_range_out, workspace (None: allocated here)
+PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 13);
+  const Tensor& held = tensor(a[0], "held_lens");
+  if (!held.is_cuda()) REFUSE("held_lens must be on a CUDA device, got " << held.device());
+  const c10::Device dev = held.device();
+  const Tensor &table = tensor(a[1], "block_table"), &ring = tensor(a[4], "free_pages");
+  if (table.dim() != 2) REFUSE("block_table must be [B, max_blocks]");
+  const int64_t B = held.numel(), R = tensor(a[2], "parents").numel(), blocks = table.size(1),
+                cap = ring.numel();
+  if (B > INT32_MAX || R > INT32_MAX || blocks > INT32_MAX || cap > INT32_MAX)
+    REFUSE("more requests, columns or pages than 32 bits count");
+  const int64_t page_size = integer(a[6], "page_size"), pages = integer(a[7], "num_pages");
+  const int64_t old_lens[] = {B}, lens[] = {R}, table_shape[] = {B, blocks},
+                out_shape[] = {R, blocks}, ring_shape[] = {cap}, two[] = {2}, three[] = {R, 3};
+  constexpr ScalarType I = ScalarType::Int, L = ScalarType::Long;
+  const int32_t* held_p = need<int32_t>(a[0], "held_lens", I, old_lens, dev);
+  const int32_t* table_p = need<int32_t>(a[1], "block_table", I, table_shape, dev);
+  const int32_t* parents_p = need<int32_t>(a[2], "parents", I, lens, dev);
+  const int32_t* keep_p = need<int32_t>(a[3], "keep_lens", I, lens, dev);
+  int32_t* ring_p = need<int32_t>(a[4], "free_pages", I, ring_shape, dev);
+  const int64_t* span_p = need<int64_t>(a[5], "free_range", L, two, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  size_t bytes = 0, have = 0;
+  kda_status_t st = kda_cache_fork_workspace_size((int32_t)pages, (int32_t)R, &bytes);
+  if (st != KDA_OK) return status_object(st);
+  Tensor kv, out, copies, span, ws;
+  int32_t* kv_p = output<int32_t>(a[8], "kv_lens", I, lens, dev, kv);
+  int32_t* out_p = output<int32_t>(a[9], "block_table_out", I, out_shape, dev, out);
+  int32_t* copies_p = output<int32_t>(a[10], "copies", I, three, dev, copies);
+  int64_t* span_out = output<int64_t>(a[11], "free_range_out", L, two, dev, span);
+  void* ws_p = scratch(a[12], bytes, dev, ws, have);
+  st = kda_cache_fork((int32_t)page_size, (int32_t)pages, (int32_t)B, (int32_t)R, (int32_t)blocks,
+                      (int32_t)cap, held_p, table_p, parents_p, keep_p, ring_p, span_p, span_out,
+                      kv_p, out_p, copies_p, ws_p, have, stream_of(dev));
+  if (st != KDA_OK) return status_object(st);
+  return tuple_of({kv, out, copies, span});
+  END_HANDLE_TH_ERRORS
+}
+
+// held_lens, block_table, free_pages, page_size, num_pages, block_table_out, copies,
+// free_range_out, workspace (None: allocated here)
+PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 9);
+  const Tensor& held = tensor(a[0], "held_lens");
+  if (!held.is_cuda()) REFUSE("held_lens must be on a CUDA device, got " << held.device());
+  const c10::Device dev = held.device();
+  const Tensor &table = tensor(a[1], "block_table"), &ring = tensor(a[2], "free_pages");
+  if (table.dim() != 2) REFUSE("block_table must be [B, max_blocks]");
+  const int64_t B = held.numel(), blocks = table.size(1), cap = ring.numel();
+  if (B > INT32_MAX || blocks > INT32_MAX || cap > INT32_MAX)
+    REFUSE("more requests, columns or pages than 32 bits count");
+  const int64_t page_size = integer(a[3], "page_size"), pages = integer(a[4], "num_pages");
+  if (pages < 0) REFUSE("num_pages must not be negative, got " << pages);
+  const int64_t lens[] = {B}, table_shape[] = {B, blocks}, ring_shape[] = {cap}, two[] = {2},
+                moves[] = {pages / 2, 3};
+  constexpr ScalarType I = ScalarType::Int, L = ScalarType::Long;
+  const int32_t* held_p = need<int32_t>(a[0], "held_lens", I, lens, dev);
+  const int32_t* table_p = need<int32_t>(a[1], "block_table", I, table_shape, dev);
+  int32_t* ring_p = need<int32_t>(a[2], "free_pages", I, ring_shape, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  size_t bytes = 0, have = 0;
+  kda_status_t st = kda_cache_compact_workspace_size((int32_t)pages, &bytes);
+  if (st != KDA_OK) return status_object(st);
+  Tensor out, copies, span, ws;
+  int32_t* out_p = output<int32_t>(a[5], "block_table_out", I, table_shape, dev, out);
+  int32_t* copies_p = output<int32_t>(a[6], "copies", I, moves, dev, copies);
+  int64_t* span_p = output<int64_t>(a[7], "free_range_out", L, two, dev, span);
+  void* ws_p = scratch(a[8], bytes, dev, ws, have);
+  st = kda_cache_compact((int32_t)page_size, (int32_t)pages, (int32_t)B, (int32_t)blocks,
+                         (int32_t)cap, held_p, table_p, out_p, copies_p, ring_p, span_p, ws_p,
+                         have, stream_of(dev));
+  if (st != KDA_OK) return status_object(st);
+  return tuple_of({out, copies, span});
+  END_HANDLE_TH_ERRORS
+}
+
+// caches (a tuple of tensors of one shape), copies
+PyObject* copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 2);
+  const Tensor& copies = tensor(a[1], "copies");
+  if (!copies.is_cuda()) REFUSE("copies must be on a CUDA device, got " << copies.device());
+  const c10::Device dev = copies.device();
+  const int64_t shape[] = {copies.numel() / 3, 3};
+  const int32_t* copies_p = need<int32_t>(a[1], "copies", ScalarType::Int, shape, dev);
+  if (shape[0] > INT32_MAX) REFUSE("more copies than 32 bits count");
+  const Py_ssize_t layers = PyTuple_Size(a[0]);
+  if (layers < 0) throw python_error();
+  if (layers == 0) return status_object(KDA_OK);
+  std::vector<void*> pages((size_t)layers);
+  const Tensor& first = tensor(PyTuple_GET_ITEM(a[0], 0), "cache");
+  if (first.dim() != 4)
+    REFUSE("cache must be uint8 [num_pages, kv heads, page_size / 16, bytes], got "
+           << first.sizes());
+  for (int i = 0; i < 4; ++i)
+    if (first.size(i) > (1 << 30)) REFUSE("cache is too large: " << first.sizes());
+  const std::vector<int64_t> sizes = first.sizes().vec();
+  for (Py_ssize_t i = 0; i < layers; ++i)
+    pages[(size_t)i] =
+        need<void>(PyTuple_GET_ITEM(a[0], i), "cache", ScalarType::Byte, sizes, dev);
+  const c10::cuda::CUDAGuard guard(dev);
+  return status_object(kda_cache_copy(
+      (int32_t)layers, pages.data(), (int32_t)sizes[0], (int32_t)sizes[1],
+      (int32_t)(sizes[2] > 4096 ? -1 : sizes[2] * 16), (int32_t)sizes[3], (int32_t)shape[0],
+      copies_p, stream_of(dev)));
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"tables", (PyCFunction)(void (*)())tables, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)())append, METH_FASTCALL, nullptr},
     {"read", (PyCFunction)(void (*)())read, METH_FASTCALL, nullptr},
     {"attention", (PyCFunction)(void (*)())attention, METH_FASTCALL, nullptr},
+    {"append8", (PyCFunction)(void (*)())append8, METH_FASTCALL, nullptr},
+    {"read8", (PyCFunction)(void (*)())read8, METH_FASTCALL, nullptr},
+    {"attention8", (PyCFunction)(void (*)())attention8, METH_FASTCALL, nullptr},
+    {"fork", (PyCFunction)(void (*)())fork, METH_FASTCALL, nullptr},
+    {"compact", (PyCFunction)(void (*)())compact, METH_FASTCALL, nullptr},
+    {"copy", (PyCFunction)(void (*)())copy, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cache_binding", nullptr, -1, methods,

@@ -1,0 +1,46 @@
+// kda_byte_cache_attention.cu -- kda_byte_cache_attention: causal attention over the 8-bit paged cache.
+//
+// The kernel is that of the 4-bit cache (kda_cache_attention.cu), with 8-bit codes and scales
+// that are powers of two of a whole block:
+//   - a code becomes a half by one conversion, without a product;
+//   - K's power of two 2^e goes into the factor of a group's 16 raw scores;
+//   - V's goes into the weights: p 2^(e - E), E the largest exponent that the unit's part has
+//     met (o is rescaled when it rises, in the branch that moves the softmax's reference), so
+//     that a half holds it and the sums o stay in units of 2^E.  The sum l of weights does not
+//     take part in it.
+#include "kda_cache_split.cuh"
+
+namespace kda {
+namespace {
+
+template <typename F>
+auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
+  const bool few = (int64_t)a.max_new * (a.num_heads / c.kv_heads) <= 8;
+  if (a.bf16) {
+    using T = __nv_bfloat16;
+    if (a.head_dim == 128)
+      return few ? f(Split<8, T, 128, 1, 4, 2, 3>{}) : f(Split<8, T, 128, 2, 8, 3, 1>{});
+    return few ? f(Split<8, T, 64, 1, 8, 3, 2>{}) : f(Split<8, T, 64, 2, 8, 4, 1>{});
+  }
+  if (a.head_dim == 128)
+    return few ? f(Split<8, float, 128, 1, 8, 3, 1>{}) : f(Split<8, float, 128, 2, 8, 2, 1>{});
+  return few ? f(Split<8, float, 64, 1, 8, 3, 2>{}) : f(Split<8, float, 64, 2, 8, 4, 1>{});
+}
+
+}  // namespace
+
+size_t byte_cache_attention_workspace_bytes(const View& c, const AttentionArgs& a) {
+  return dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });
+}
+
+cudaError_t launch_byte_cache_attention(const View& c, const AttentionArgs& args, cudaStream_t st) {
+  AttentionArgs a = args;
+  if (take_injected_timeout()) {
+    a.wait_cycles = kInjectedWaitCycles;
+    a.withheld = 1;
+  }
+  const RowRange all{0, INT64_MAX};
+  return dispatch(c, a, [&](auto v) { return decltype(v)::launch(c, a, all, st); });
+}
+
+}  // namespace kda

@@ -1,0 +1,329 @@
+// kda_byte_cache_store.cu -- kda_byte_cache_append and kda_byte_cache_read: keys and values between
+// their own type and the cache's 8-bit blocks.
+//
+// A block is 16 tokens of one head, K or V.  Its exponent e is the least with max |x| <=
+// 448 2^e over the tokens appended to it, its codes are e4m3(x 2^-e): the product with a power
+// of two is exact, so a value is rounded once.  New tokens that raise the exponent of a block
+// begun earlier take its codes along, e4m3(c 2^(e - e')), which is exact but for codes that run
+// into E4M3's smallest numbers.
+//
+// One warp takes the new tokens of one block, a run of neighbours in the batch, and keeps
+// them in registers: 16 bytes of bf16 a lane and token, the largest magnitude by one redux.
+// Nothing is shared between warps.
+#include <algorithm>
+
+#include "kda_byte_cache.cuh"
+#include "kda_launch.h"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace {
+
+using namespace cache;
+
+constexpr int kThreads = 256;
+
+struct Source {
+  const void* p;
+  int64_t token_stride, head_stride;  // elements
+};
+
+// 8 neighbouring values of a row as they lie in memory.  VEC: 16-byte aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fetch8(const T* p, uint32_t (&w)[2 * sizeof(T)]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __float_as_uint(IO<T>::ld(p + 2 * i)) >> 16 |
+             __float_as_uint(IO<T>::ld(p + 2 * i + 1));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(IO<T>::ld(p + i));
+  }
+}
+
+// Value i of them.
+template <typename T>
+__device__ __forceinline__ float value8(const uint32_t (&w)[2 * sizeof(T)], int i) {
+  if constexpr (sizeof(T) == 4)
+    return __uint_as_float(w[i]);
+  else
+    return i & 1 ? tc::bf16_hi(w[i / 2]) : tc::bf16_lo(w[i / 2]);
+}
+
+// Bits of the largest magnitude as fp32 (magnitudes order like their bits).
+template <typename T>
+__device__ __forceinline__ uint32_t top8(const uint32_t (&w)[2 * sizeof(T)]) {
+  uint32_t top = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, w[i] & 0x7fffffffu);
+    return top;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+    return max(top << 16, top & 0xffff0000u);
+  }
+}
+
+// The least e with x <= 448 2^e, in the range of exponents; x given by its bits and finite:
+// 448 = 1.75 * 2^8.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(kLeastExponent, min(e, kMostExponent));
+}
+
+// First byte of a token's 8 channels from c on, which are one run.
+template <int D, bool V>
+__device__ __forceinline__ int place8(int i, int c) {
+  return V ? Layout8<D>::v_code(i, c) : Layout8<D>::k_code(i, c);
+}
+
+// The run of tokens first .. first + n - 1 of the batch, which fill places of one block; lane k
+// < n has the place of the k-th of them.  All lanes of the warp.
+template <typename T, int D, bool VEC, bool V>
+__device__ __forceinline__ void append_run(uint8_t* group, const T* src, int64_t token_stride,
+                                           int n, int place, bool& not_finite) {
+  constexpr int LANES = D / 8;          // of a token
+  constexpr int AT_ONCE = 32 / LANES;   // tokens
+  constexpr int STEPS = kGroup / AT_ONCE;
+  const int lane = threadIdx.x & 31;
+  const int c = lane % LANES * 8, t = lane / LANES;
+  uint32_t w[STEPS][2 * sizeof(T)];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+    if (s * AT_ONCE + t < n) fetch8<T, VEC>(src + (s * AT_ONCE + t) * token_stride + c, w[s]);
+  uint8_t* const exp_at = group + Layout8<D>::kScales + (V ? 1 : 0);
+  // places that the run fills, and whether it begins the block anew
+  const uint32_t filled = __reduce_or_sync(0xffffffffu, lane < n ? 1u << place : 0u);
+  const bool fresh = filled & 1;
+  // (a byte that append did not write is held to the range of those it does)
+  const int before = fresh ? kLeastExponent
+                           : max(kLeastExponent, min((int)*exp_at - kExponentBias, kMostExponent));
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+    if (s * AT_ONCE + t < n) top = max(top, top8<T>(w[s]));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top >= 0x7f800000u) {  // infinities do not count, NaN becomes zero
+    not_finite = true;
+    top = 0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      if (s * AT_ONCE + t >= n) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t m = __float_as_uint(value8<T>(w[s], i)) & 0x7fffffffu;
+        if (m < 0x7f800000u) top = max(top, m);
+        if (m > 0x7f800000u) {
+          if constexpr (sizeof(T) == 4)
+            w[s][i] = 0;
+          else
+            w[s][i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+        }
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  const int e = max(exponent_of(top), before);
+  if (!fresh && e > before) {
+    // pieces of 8 codes, each of one token: 2 D of them
+    const uint32_t f = half_power(e - before);
+#pragma unroll 1
+    for (int p = lane; p < 2 * D; p += 32) {
+      const int i = p / (D / 8);
+      uint2* at = reinterpret_cast<uint2*>(group + place8<D, V>(i, p % (D / 8) * 8));
+      if (filled >> i & 1) continue;
+      const uint2 old = *at;
+      uint32_t h[4];
+      e4m3x4_to_f16(old.x, h[0], h[1]);
+      e4m3x4_to_f16(old.y, h[2], h[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = f16x2_to_e4m3x2(mul_f16x2(h[j], f));
+      *at = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    }
+  }
+  const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int i = __shfl_sync(0xffffffffu, place, (s * AT_ONCE + t) & 31);
+    if (s * AT_ONCE + t < n) {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        b[j] = f32x2_to_e4m3x2(value8<T>(w[s], 2 * j) * down, value8<T>(w[s], 2 * j + 1) * down);
+      *reinterpret_cast<uint2*>(group + place8<D, V>(i, c)) =
+          make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+    }
+  }
+  if (lane == 0) *exp_at = (uint8_t)(e + kExponentBias);
+}
+
+// A warp takes the runs that start among `window` tokens (at most 16), of one head, of K or V.
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    append_kernel(View c, int tokens, int window, Source k, Source v,
+                  const int64_t* __restrict__ slots, int* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int heads = c.kv_heads;
+  const int64_t at = unit / (2 * heads);
+  const int which = (int)(unit - at * 2 * heads);
+  const int head = which % heads;
+  const bool is_v = which >= heads;
+  const int64_t start = at * window;
+  if (start >= tokens) return;
+  // lane l: the slot of token start - 1 + l, as far as a run of the window may reach
+  const int64_t token = start - 1 + lane;
+  int64_t slot = -1;
+  if (token >= 0 && token < tokens && lane < window + kGroup) slot = __ldg(slots + token);
+  const bool there = slot >= 0 && slot < (int64_t)c.num_pages * c.page_size;
+  const bool mine = lane >= 1 && lane <= window;
+  if (!there && slot != -1 && mine && which == 0) report_error(err, kErrDeviceCheck);
+  const int block = there ? (int)(slot / kGroup) : -1;  // fewer than 2^27
+  const int prev = __shfl_up_sync(0xffffffffu, block, 1);
+  const bool goes_on = there && lane > 0 && prev == block;
+  const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
+  uint32_t heads_of = __ballot_sync(0xffffffffu, mine && there && !goes_on);
+  bool not_finite = false;
+  const int groups = c.page_size / kGroup;
+  for (; heads_of; heads_of &= heads_of - 1) {
+    const int l = __ffs(heads_of) - 1;
+    // tokens l, l + 1, ... as long as they go on
+    const uint32_t after = l == 31 ? 0u : ~(on >> (l + 1));
+    const int n = min(after ? __ffs(after) : 32, kGroup);
+    const int place = __shfl_sync(0xffffffffu, (int)(slot & (kGroup - 1)), (l + lane) & 31);
+    const int b = __shfl_sync(0xffffffffu, block, l);
+    const int page = b / groups;
+    uint8_t* group =
+        c.pages + (((int64_t)page * heads + head) * groups + (b - page * groups)) *
+                      Layout8<D>::kGroupBytes;
+    const Source& s = is_v ? v : k;
+    const T* src = static_cast<const T*>(s.p) + (start - 1 + l) * s.token_stride +
+                   head * s.head_stride;
+    if (is_v)
+      append_run<T, D, VEC, true>(group, src, s.token_stride, n, place, not_finite);
+    else
+      append_run<T, D, VEC, false>(group, src, s.token_stride, n, place, not_finite);
+  }
+  if (not_finite && lane == 0) report_error(err, kErrDeviceCheck);
+}
+
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __stcs(reinterpret_cast<float4*>(p) + i,
+             make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __stcs(reinterpret_cast<uint4*>(p) + i,
+             make_uint4(tc::pack_bf16(x[8 * i], x[8 * i + 1]),
+                        tc::pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                        tc::pack_bf16(x[8 * i + 4], x[8 * i + 5]),
+                        tc::pack_bf16(x[8 * i + 6], x[8 * i + 7])));
+  }
+}
+
+// A thread takes 16 channels of a token and every so many heads, of K or V.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+    read_kernel(View c, int tokens, const int64_t* __restrict__ slots, T* __restrict__ k,
+                T* __restrict__ v, int* err) {
+  constexpr int PIECES = D / 16;
+  const int piece = threadIdx.x % PIECES;
+  const int first = threadIdx.x / (8 * PIECES), step = blockDim.x / (8 * PIECES);
+  const int64_t token = (int64_t)blockIdx.x * 8 + threadIdx.x / PIECES % 8;
+  if (token >= tokens) return;
+  const int64_t slot = __ldg(slots + token);
+  const bool there = slot >= 0 && slot < (int64_t)c.num_pages * c.page_size;
+  if (!there && slot != -1) report_error(err, kErrDeviceCheck);
+  const bool is_v = blockIdx.y;
+  const int groups = c.page_size / kGroup;
+  const int64_t head_bytes = (int64_t)groups * Layout8<D>::kGroupBytes;
+  const uint8_t* g = c.pages;
+  int at = 0;
+  if (there) {
+    const int page = (int)(slot / c.page_size), tok = (int)(slot % c.page_size), i = tok % kGroup;
+    g += (int64_t)page * c.kv_heads * head_bytes + tok / kGroup * Layout8<D>::kGroupBytes;
+    at = is_v ? Layout8<D>::v_code(i, piece * 16) : Layout8<D>::k_code(i, piece * 16);
+  }
+  T* out = (is_v ? v : k) + token * c.kv_heads * D + piece * 16;
+#pragma unroll 2
+  for (int h = first; h < c.kv_heads; h += step) {
+    float x[16] = {};
+    if (there) {
+      const uint8_t* p = g + h * head_bytes;
+      uint4 w;
+      if (D == 128 || !is_v) {
+        w = *reinterpret_cast<const uint4*>(p + at);
+      } else {  // V of 64 channels: 8 to a run
+        const uint2 a = *reinterpret_cast<const uint2*>(p + at);
+        const uint2 b = *reinterpret_cast<const uint2*>(p + at + D / 2);
+        w = make_uint4(a.x, a.y, b.x, b.y);
+      }
+      const float f = exponent_factor(p[Layout8<D>::kScales + (is_v ? 1 : 0)]);
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16(words[j], lo, hi);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        x[4 * j] = a.x * f, x[4 * j + 1] = a.y * f;
+        x[4 * j + 2] = b.x * f, x[4 * j + 3] = b.y * f;
+      }
+    }
+    store16(out + (int64_t)h * D, x);
+  }
+}
+
+template <typename T, int D>
+cudaError_t append(const CacheArgs& a, cudaStream_t st) {
+  const Source k{a.k, a.strides[0], a.strides[1]}, v{a.v, a.strides[2], a.strides[3]};
+  const int el = 16 / sizeof(T);
+  bool vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0;
+  for (int64_t s : a.strides) vec = vec && s % el == 0;
+  const int window = (int64_t)a.tokens * a.view.kv_heads >= 1 << 17 ? kGroup : 1;
+  const int64_t units = ((int64_t)a.tokens + window - 1) / window * 2 * a.view.kv_heads;
+  const int64_t ctas = (units * 32 + kThreads - 1) / kThreads;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  auto* kernel = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
+  kernel<<<(unsigned)ctas, kThreads, 0, st>>>(a.view, a.tokens, window, k, v, a.slots, a.err);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t read(const CacheArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.tokens + 7ll) / 8), 2);
+  const int per_head = 8 * (D / 16);
+  const int threads = per_head * std::min(a.view.kv_heads, kThreads / per_head);
+  read_kernel<T, D><<<grid, threads, 0, st>>>(a.view, a.tokens, a.slots,
+                                              static_cast<T*>(a.k_out), static_cast<T*>(a.v_out),
+                                              a.err);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_byte_cache_append(const CacheArgs& a, cudaStream_t st) {
+  if (a.bf16)
+    return a.head_dim == 128 ? append<__nv_bfloat16, 128>(a, st) : append<__nv_bfloat16, 64>(a, st);
+  return a.head_dim == 128 ? append<float, 128>(a, st) : append<float, 64>(a, st);
+}
+
+cudaError_t launch_byte_cache_read(const CacheArgs& a, cudaStream_t st) {
+  if (a.bf16)
+    return a.head_dim == 128 ? read<__nv_bfloat16, 128>(a, st) : read<__nv_bfloat16, 64>(a, st);
+  return a.head_dim == 128 ? read<float, 128>(a, st) : read<float, 64>(a, st);
+}
+
+}  // namespace kda

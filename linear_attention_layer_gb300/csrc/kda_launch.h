@@ -300,6 +300,57 @@ size_t cache_chunk_workspace_bytes(const cache::View& c, const AttentionArgs& a)
 cudaError_t launch_cache_chunk(const cache::View& c, const AttentionArgs& a,
                                const cache::RowRange& range, cudaStream_t st);
 
+// The same for the 8-bit cache (kda_byte_cache_store.cu, kda_byte_cache_attention.cu).
+cudaError_t launch_byte_cache_append(const CacheArgs& a, cudaStream_t st);
+cudaError_t launch_byte_cache_read(const CacheArgs& a, cudaStream_t st);
+size_t byte_cache_attention_workspace_bytes(const cache::View& c, const AttentionArgs& a);
+cudaError_t launch_byte_cache_attention(const cache::View& c, const AttentionArgs& a, cudaStream_t st);
+
+// Pages that several rows hold (kda_cache_pages.cu).
+struct ForkArgs {
+  int page_size, num_pages, old_seqs, num_seqs, max_blocks, ring_size;
+  const int32_t* held_lens;
+  const int32_t* block_table;
+  const int32_t* parents;
+  const int32_t* keep_lens;
+  int32_t* free_pages;
+  const int64_t* free_range;
+  int64_t* free_range_out;  // may equal free_range
+  int32_t* kv_lens;         // may equal held_lens, parents or keep_lens
+  int32_t* block_table_out;
+  int32_t* copies;  // [num_seqs][3]
+  void* workspace;
+  int* err;
+};
+size_t cache_fork_workspace_bytes(const ForkArgs& a);
+cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st);
+
+struct CompactArgs {
+  int page_size, num_pages, num_seqs, max_blocks;
+  const int32_t* held_lens;
+  const int32_t* block_table;
+  int32_t* block_table_out;  // may equal block_table
+  int32_t* copies;           // [num_pages / 2][3]
+  int32_t* free_pages;
+  int64_t* free_range_out;
+  void* workspace;
+  int* err;
+};
+size_t cache_compact_workspace_bytes(const CompactArgs& a);
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st);
+
+constexpr int kCopyLayers = 64;  // caches of one launch
+struct CopyArgs {
+  int num_layers, num_pages;
+  int runs;         // kv heads: runs of groups in a page
+  int groups;       // of 16 tokens in a run
+  int group_bytes;  // a multiple of 16
+  int num_copies;
+  const int32_t* copies;
+  int* err;
+};
+cudaError_t launch_cache_copy(const CopyArgs& a, uint8_t* const* pages, cudaStream_t st);
+
 }  // namespace kda
 
 #include "../../include/kda.h"
