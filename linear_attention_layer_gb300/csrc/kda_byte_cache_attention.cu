@@ -30,7 +30,8 @@ auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
 }  // namespace
 
 size_t byte_cache_attention_workspace_bytes(const View& c, const AttentionArgs& a) {
-  return dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });
+  const size_t split = dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });
+  return std::max(split, cache_chunk_wanted(c, a) ? cache_chunk_workspace_bytes(c, a) : 0);
 }
 
 cudaError_t launch_byte_cache_attention(const View& c, const AttentionArgs& args, cudaStream_t st) {
@@ -39,8 +40,13 @@ cudaError_t launch_byte_cache_attention(const View& c, const AttentionArgs& args
     a.wait_cycles = kInjectedWaitCycles;
     a.withheld = 1;
   }
-  const RowRange all{0, INT64_MAX};
-  return dispatch(c, a, [&](auto v) { return decltype(v)::launch(c, a, all, st); });
+  const bool chunk = cache_chunk_wanted(c, a);
+  // without the second kernel the first takes every request, whatever max_new said
+  const RowRange few{0, chunk ? kSplitRows : INT64_MAX}, many{kSplitRows, INT64_MAX};
+  const cudaError_t e =
+      dispatch(c, a, [&](auto v) { return decltype(v)::launch(c, a, few, st); });
+  if (e != cudaSuccess || !chunk) return e;
+  return launch_cache_chunk(8, c, a, many, st);
 }
 
 }  // namespace kda

@@ -68,14 +68,6 @@ auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
 
 }  // namespace
 
-// Requests with more rows per kv head than this go to the chunk kernel, whose work for a
-// key is that of 128 rows, or 256, whatever their number.  67 windows with up to 40 rows,
-// three passes here: 172 us, with the requests of more than 32 rows over there 203 (they
-// are a fifth of the keys, and the second set of launches costs 15 us); a pass over all of
-// these keys takes 95 us here, the chunk kernel's only one 200, so four passes lose.  Measured
-// with 8 query heads on a kv head and 128 channels; other shapes go by the same number.
-constexpr int64_t kSplitRows = 48;
-
 size_t cache_attention_workspace_bytes(const View& c, const AttentionArgs& a) {
   const size_t split = dispatch(c, a, [&](auto v) { return decltype(v)::workspace(); });
   return std::max(split, cache_chunk_wanted(c, a) ? cache_chunk_workspace_bytes(c, a) : 0);
@@ -97,7 +89,7 @@ cudaError_t launch_cache_attention(const View& c, const AttentionArgs& args, cud
   const cudaError_t e =
       dispatch(c, a, [&](auto v) { return decltype(v)::launch(c, a, few, st); });
   if (e != cudaSuccess || !chunk) return e;
-  return launch_cache_chunk(c, a, many, st);
+  return launch_cache_chunk(4, c, a, many, st);
 }
 
 }  // namespace kda

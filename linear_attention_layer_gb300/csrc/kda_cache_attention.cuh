@@ -1,7 +1,10 @@
-// kda_cache_attention.cuh -- what the two attention kernels over the cache share:
+// kda_cache_attention.cuh -- what the two attention kernels over both forms of the cache share:
 // requests as their planners see them, softmax constants, row output.
 #pragma once
 
+#include <type_traits>
+
+#include "kda_byte_cache.cuh"
 #include "kda_cache.cuh"
 #include "kda_launch.h"
 #include "tc_ptx.cuh"
@@ -15,6 +18,17 @@ namespace cache {
 constexpr float kSlack = 8.f, kLift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+template <int BITS, int D>
+using FormLayout = std::conditional_t<BITS == 4, Layout<D>, Layout8<D>>;
+
+// -m of a row that has seen nothing yet, 8 bits: any score passes it.
+constexpr float kUnset = 1e30f;
+
+// 2^d for d <= 0; 0 where fp32 has no normal number for it.
+__device__ __forceinline__ float power_below(int d) {
+  return d < -126 ? 0.f : __int_as_float((127 + d) << 23);
+}
 
 // Waits for a phase of the barrier; false when it took `limit` cycles or `*failed` (another wait
 // that gave up; may be null) was set.  Each thread has its own answer: before code that needs a

@@ -167,10 +167,10 @@ struct Piece {
   }
 };
 
-template <int D>
+template <int BITS, int D>
 struct Smem {
   static constexpr int kTile = kKeys * D * 2;
-  static constexpr int kRaw = kGroups * Layout<D>::kGroupBytes;
+  static constexpr int kRaw = kGroups * FormLayout<BITS, D>::kGroupBytes;
   alignas(1024) uint8_t k[kTileStages][kTile];
   alignas(1024) uint8_t v[kTileStages][kTile];
   static constexpr bool kQueryHere = D > 64;  // the second block's
@@ -180,6 +180,7 @@ struct Smem {
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
   uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_full[2], issued;
   uint32_t valid[kValidRing];  // groups of a tile that can be read
+  uint32_t powers[kValidRing]; // 8 bits: exponent bytes of a tile's K and, times 256, V
   uint32_t tmem;
   uint32_t copied;  // tiles whose pages were asked for
   int failed;
@@ -198,14 +199,86 @@ struct Ring {
   }
 };
 
-template <int D>
+// Dequantisation of a tile of 8-bit codes, by warp dw of four its group of 16 keys: halves in
+// units of the largest power of two among the tile's groups, as rows of 128 swizzled bytes.  A
+// code times 2^-d is exact down to 2^-24 of the unit.  Lanes take the 16-byte pieces so that
+// eight of them read 128 bytes in a row and write to all banks.
+template <int D, bool V>
+struct Dequant8 {
+  static constexpr int N = D / 32;  // pieces of a lane
+  uint4 w[N];
+
+  __device__ __forceinline__ void load(const uint8_t* g) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if constexpr (V)
+        w[n] = *reinterpret_cast<const uint4*>(g + Layout8<D>::kVCodes + n * 512 + lane * 16);
+      else  // two keys a time, of channels 32 t + 16 h .. in opposite orders
+        w[n] = *reinterpret_cast<const uint4*>(g + half_of(n) * 1024 + key_of(n) * 64 + t * 16);
+    }
+  }
+  // K: the key of piece n, and which 16 of the 32 channels (D = 128)
+  __device__ __forceinline__ static int key_of(int n) {
+    const int lane = threadIdx.x & 31;
+    return 2 * ((lane >> 3) + 4 * (n & 1)) + (lane >> 2 & 1);
+  }
+  __device__ __forceinline__ static int half_of(int n) {
+    return D == 64 ? 0 : (n >> 1) ^ (threadIdx.x >> 1 & 1);
+  }
+  // Eight halves of codes x, y to chunk `chunk` of row `row`.
+  __device__ __forceinline__ static void put(uint8_t* tile, int row, int chunk, uint32_t x,
+                                             uint32_t y, uint32_t f) {
+    uint32_t h[4];
+    e4m3x4_to_f16(x, h[0], h[1]);
+    e4m3x4_to_f16(y, h[2], h[3]);
+    if (f != 0x3c003c00u) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) h[q] = mul_f16x2(h[q], f);
+    }
+    *reinterpret_cast<uint4*>(tile + (chunk >> 3) * (kKeys * 128) + row * 128 +
+                              (((chunk & 7) ^ (row & 7)) << 4)) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  // f: the group's power of two beside the tile's, as two halves; left: keys that there are.
+  __device__ __forceinline__ void store(uint8_t* tile, int dw, uint32_t f, int left) const {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if constexpr (!V) {
+        const int row = dw * kGroup + key_of(n);
+        const int chunk = D == 64 ? 2 * t : 4 * t + 2 * half_of(n);  // 8 channels each
+        put(tile, row, chunk, w[n].x, w[n].y, f);
+        put(tile, row, chunk + 1, w[n].z, w[n].w, f);
+      } else if constexpr (D == 128) {
+        // sub-block n of tokens 8 (n / 2) + 2 t + n % 2, channels 16 (lane / 4) ..
+        const int i = 8 * (n >> 1) + 2 * t + (n & 1), g = lane >> 2;
+        const bool there = i < left;
+        const uint4 x = there ? w[n] : make_uint4(0, 0, 0, 0);
+        const bool swap = g & 1;
+        put(tile, dw * kGroup + i, 2 * g + swap, swap ? x.z : x.x, swap ? x.w : x.y, f);
+        put(tile, dw * kGroup + i, 2 * g + !swap, swap ? x.x : x.z, swap ? x.y : x.w, f);
+      } else {
+        // two sub-blocks a time, tokens 2 t and 2 t + 2 of 8 channels a lane
+        const int sub = 2 * n + (lane >> 4), g = lane >> 1 & 7;
+        const int i = 8 * (sub >> 1) + 4 * (lane & 1) + (sub & 1);
+        const uint32_t a = i < left ? ~0u : 0u, b = i + 2 < left ? ~0u : 0u;
+        put(tile, dw * kGroup + i, g, w[n].x & a, w[n].y & a, f);
+        put(tile, dw * kGroup + i + 2, g, w[n].z & b, w[n].w & b, f);
+      }
+    }
+  }
+};
+
+template <int BITS, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(View c, AttentionArgs a, RowRange range, Plan plan, int q_vec) {
-  using L = Layout<D>;
+  using L = FormLayout<BITS, D>;
+  using S = Smem<BITS, D>;
   constexpr uint32_t TS = 0, TP = 128, TQ = 192, TO = 256;  // columns of S, P, q, O
-  constexpr bool QS = Smem<D>::kQueryHere;
+  constexpr bool QS = S::kQueryHere;
   extern __shared__ uint8_t raw_smem[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw_smem + (-tc::smem_u32(raw_smem) & 1023u));
+  S& sm = *reinterpret_cast<S*>(raw_smem + (-tc::smem_u32(raw_smem) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.num_heads / c.kv_heads;
 
@@ -344,21 +417,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.q_full[blk]);
       }
-      float neg = 0.f, thr = -INFINITY;
+      float neg = BITS == 4 ? 0.f : kUnset, thr = -INFINITY;
+      int v_ref = 0;            // 8 bits: O is in units of 2^(v_ref - 127)
+      bool gave_up = false;     // 8 bits
       uint64_t l2[2] = {0, 0};  // the row's sum, in four parts
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         // a wait that gives up lowers the limit, so that the vote below is taken
-        if (!wait(&sm.s_full[blk], s_full.parity)) thr = -INFINITY;
+        if (!wait(&sm.s_full[blk], s_full.parity)) thr = -INFINITY, gave_up = true;
         s_full.step();
         tc::tc_fence_after();
         float s[kKeys];
         const int key0 = j * kKeys;
-        uint32_t valid;
+        uint32_t valid, powers = 0;
         {
           float h0[32], h1[32];
           tc::tmem_ld32(ts, h0);
           tc::tmem_ld32(ts + 32, h1);
           valid = *(volatile uint32_t*)&sm.valid[tile_no % kValidRing];
+          if constexpr (BITS == 8) powers = *(volatile uint32_t*)&sm.powers[tile_no % kValidRing];
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[i] = h0[i], s[32 + i] = h1[i];
@@ -379,23 +455,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = fmaxf(tc::max3(t4[0], s[kKeys - 4], s[kKeys - 3]),
                                 tc::max3(tc::max3(t4[1], t4[2], t4[3]), s[kKeys - 2], s[kKeys - 1]));
         bool waited = false;
-        if (__any_sync(0xffffffffu, top > thr)) {
+        // 8 bits: the raw scores' factor in this tile (kept positive) and its V's exponent byte
+        const float ft =
+            BITS == 4 ? f
+                      : fminf(fmaxf(f * exponent_factor(powers & 255), 1.2e-38f), 3.e38f);
+        const int v_top = powers >> 8;
+        const bool move = BITS == 4 ? top > thr
+                                    : fmaf(top, ft, neg) > kLift + kSlack || v_top > v_ref || gave_up;
+        if (__any_sync(0xffffffffu, move)) {
           ok = all_ok(!*failed);
           if (!ok) break;
           float keep = 1.f;
           if (top > -INFINITY) {
-            const float before = thr == -INFINITY ? -INFINITY : -neg;
-            const float m = fmaxf(before, top * f - kLift);
+            const bool unset = BITS == 4 ? thr == -INFINITY : neg == kUnset;
+            const float before = unset ? -INFINITY : -neg;
+            const float m = fmaxf(before, top * ft - kLift);
             keep = ex2_approx(before - m);
             neg = -m;
-            thr = score_limit(m, f);
+            if constexpr (BITS == 4) thr = score_limit(m, f);
           }
           const uint64_t keep2 = tc::pack2(keep, keep);
           l2[0] = tc::fma2(l2[0], keep2, 0);
           l2[1] = tc::fma2(l2[1], keep2, 0);
+          if (BITS == 8 && v_top > v_ref) {
+            keep *= v_ref ? power_below(v_ref - v_top) : 0.f;
+            v_ref = v_top;
+          }
           if (j > p.begin) {
             // the product of the tile before has to be in O
-            if (!wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY;
+            if (!wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY, gave_up = true;
             tc::tc_fence_after();
             waited = true;
 #pragma unroll 1
@@ -410,7 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const uint64_t f2 = tc::pack2(f, f), neg2 = tc::pack2(neg, neg);
+        // 8 bits: weights times 2^(v_top - v_ref), which the sums take back.  Values so far below
+        // the largest that a weight could get lost in fp32 count for nothing.
+        const int under = BITS == 4 ? 0 : v_top - v_ref;
+        const bool drop = under < -60;
+        const float shift = drop ? 0.f : (float)under;
+        uint64_t lt[2] = {0, 0};
+        uint64_t(&sum)[2] = BITS == 4 ? l2 : lt;
+        const uint64_t f2 = tc::pack2(ft, ft), neg2 = tc::pack2(neg + shift, neg + shift);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t w[16];
@@ -421,15 +516,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::unpack2(tc::fma2(tc::pack2(s[at], s[at + 1]), f2, neg2), p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
-            l2[i & 1] = tc::add2(l2[i & 1], tc::pack2(p0, p1));
+            sum[i & 1] = tc::add2(sum[i & 1], tc::pack2(p0, p1));
             w[i] = tc::pack_f16(p0, p1);
           }
+          if (BITS == 8 && drop) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = 0;
+          }
           if (half == 0 && j > p.begin) {  // the product before has read its weights
-            if (!waited && !wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY;
+            if (!waited && !wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY, gave_up = true;
             o_full.step();
             tc::tc_fence_after();
           }
           tc::tmem_st16u(tp + half * 16, w);
+        }
+        if constexpr (BITS == 8) {
+          const float up = __int_as_float((127 - (int)shift) << 23);
+          l2[0] = tc::fma2(lt[0], tc::pack2(up, up), l2[0]);
+          l2[1] = tc::fma2(lt[1], tc::pack2(up, up), l2[1]);
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
@@ -445,9 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::unpack2(tc::add2(l2[0], l2[1]), la, lb);
       l = la + lb;
       const bool whole = p.begin == 0 && p.end == p.tiles;
-      const float inv =
-          !whole ? 1.f : l == 0.f ? 0.f : exponent_scale(c.v_exp, p.h, 1) / l;
-      const float m = thr == -INFINITY ? -INFINITY : -neg;
+      const float post = BITS == 4 ? exponent_scale(c.v_exp, p.h, 1) : exponent_factor(v_ref);
+      const float inv = !whole ? (BITS == 4 ? 1.f : post) : l == 0.f ? 0.f : post / l;
+      const bool unset = BITS == 4 ? thr == -INFINITY : neg == kUnset;
+      const float m = unset ? -INFINITY : -neg;
       const int64_t out_at = tok * a.num_heads + head;
       const int64_t part_at =
           (int64_t)(2 * blockIdx.x + (p.begin == 0 ? 1 : 0)) * kRows + blk * kBlock + row;
@@ -469,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float4* dst = reinterpret_cast<float4*>(plan.o + part_at * D + i);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            dst[q] = BITS == 4 ? make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3])
+                               : make_float4(o[4 * q] * inv, o[4 * q + 1] * inv,
+                                             o[4 * q + 2] * inv, o[4 * q + 3] * inv);
         }
       }
       if (tid == 0 && p.begin == 0 && !whole)
@@ -490,13 +597,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<kTileStages> st;
     uint32_t empty_parity = 1;  // a fresh barrier passes for the phase before
     uint32_t tile_no = 0;
-    const int t8 = lane & 7, b4 = lane >> 3;
-    const int kc = L::k_codes(t8, b4), vc = L::v_codes(t8, b4) - L::v_codes(0, 0);
-    const int ks_at = L::k_scale(t8, b4), vs_at = L::v_scale(t8 & 6, b4);
-    // bytes of the scale words that belong to tokens t8 and t8 + 8
-    const uint32_t ks_pick = (ks_at & 3) | (((ks_at & 3) + L::kPer) << 4) | 0x4400;
-    const uint32_t vs_pick = (t8 & 1) | (((t8 & 1) + 2) << 4) | 0x4400;
-    const uint32_t row0 = (dw * kGroup + t8) * 128, chunk0 = ((b4 * 2) ^ t8) << 4;
     bool ok = true;
     for (unsigned long long x = x0; x < x1 && ok;) {
       Piece p;
@@ -504,58 +604,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       x += p.end - p.begin;
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         ok = wait(&sm.raw_full[raw.i], raw.parity);
-        // Warp dw takes group dw of the tile; a lane the tokens t8 and t8 + 8 of it and block
-        // b4 of every four.  The scales of both tokens lie in one word.
-        const uint8_t* g = sm.raw[raw.i] + dw * L::kGroupBytes;
-        const bool here = sm.valid[tile_no % kValidRing] >> dw & 1;
-        const int left = here ? p.q.kv - j * kKeys - dw * kGroup : 0;  // tokens of the group
-        auto put = [&](uint8_t* at, uint2 codes, uint32_t s2) {
-          uint32_t lo[4], hi[4];
-          e2m1x8_to_f16(codes.x, lo);
-          e2m1x8_to_f16(codes.y, hi);
+        if constexpr (BITS == 8) {
+          const uint8_t* const tile = sm.raw[raw.i];
+          const uint32_t valid = sm.valid[tile_no % kValidRing];
+          const int left = valid >> dw & 1 ? p.q.kv - j * kKeys - dw * kGroup : 0;
+          int k_top = 0, v_top = 0;  // the largest exponent bytes of the tile's groups
 #pragma unroll
-          for (int q = 0; q < 4; ++q) lo[q] = mul_f16x2(lo[q], s2), hi[q] = mul_f16x2(hi[q], s2);
-          *reinterpret_cast<uint4*>(at + chunk0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<uint4*>(at + (chunk0 ^ 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        };
-        uint2 codes[2][D / 64];
-        uint32_t scales[D / 64];
+          for (int q = 0; q < kGroups; ++q) {
+            const uint32_t x =
+                *reinterpret_cast<const uint16_t*>(tile + q * L::kGroupBytes + L::kScales);
+            if (valid >> q & 1) k_top = max(k_top, x & 255), v_top = max(v_top, x >> 8);
+          }
+          const uint8_t* const g = tile + dw * L::kGroupBytes;
+          const uint32_t mine = *reinterpret_cast<const uint16_t*>(g + L::kScales);
+          if (dw == 0 && lane == 0)
+            *(volatile uint32_t*)&sm.powers[tile_no % kValidRing] = k_top | v_top << 8;
+          Dequant8<D, false> k;
+          k.load(g);
+          ok &= wait(&sm.k_empty[st.i], empty_parity);
+          k.store(sm.k[st.i], dw, half_power(max(0, k_top - (int)(mine & 255))), kGroup);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.k_full[st.i]);
+          Dequant8<D, true> v;
+          v.load(g);
+          ok &= wait(&sm.v_empty[st.i], empty_parity);
+          v.store(sm.v[st.i], dw, half_power(max(0, v_top - (int)(mine >> 8))), left);
+        } else {
+          const int t8 = lane & 7, b4 = lane >> 3;
+          const int kc = L::k_codes(t8, b4), vc = L::v_codes(t8, b4) - L::v_codes(0, 0);
+          const int ks_at = L::k_scale(t8, b4), vs_at = L::v_scale(t8 & 6, b4);
+          // bytes of the scale words that belong to tokens t8 and t8 + 8
+          const uint32_t ks_pick = (ks_at & 3) | (((ks_at & 3) + L::kPer) << 4) | 0x4400;
+          const uint32_t vs_pick = (t8 & 1) | (((t8 & 1) + 2) << 4) | 0x4400;
+          const uint32_t row0 = (dw * kGroup + t8) * 128, chunk0 = ((b4 * 2) ^ t8) << 4;
+          // Warp dw takes group dw of the tile; a lane the tokens t8 and t8 + 8 of it and block
+          // b4 of every four.  The scales of both tokens lie in one word.
+          const uint8_t* g = sm.raw[raw.i] + dw * L::kGroupBytes;
+          const bool here = sm.valid[tile_no % kValidRing] >> dw & 1;
+          const int left = here ? p.q.kv - j * kKeys - dw * kGroup : 0;  // tokens of the group
+          auto put = [&](uint8_t* at, uint2 codes, uint32_t s2) {
+            uint32_t lo[4], hi[4];
+            e2m1x8_to_f16(codes.x, lo);
+            e2m1x8_to_f16(codes.y, hi);
 #pragma unroll
-        for (int bb = 0; bb < D / 64; ++bb) {
+            for (int q = 0; q < 4; ++q) lo[q] = mul_f16x2(lo[q], s2), hi[q] = mul_f16x2(hi[q], s2);
+            *reinterpret_cast<uint4*>(at + chunk0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(at + (chunk0 ^ 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          };
+          uint2 codes[2][D / 64];
+          uint32_t scales[D / 64];
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::k_codes(half * 8, bb * 4) + kc);
-          scales[bb] = *reinterpret_cast<const uint32_t*>(g + (ks_at & ~3) + bb * 8);
-        }
-        ok &= wait(&sm.k_empty[st.i], empty_parity);
+          for (int bb = 0; bb < D / 64; ++bb) {
 #pragma unroll
-        for (int bb = 0; bb < D / 64; ++bb) {
-          const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, ks_pick));
+            for (int half = 0; half < 2; ++half)
+              codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::k_codes(half * 8, bb * 4) + kc);
+            scales[bb] = *reinterpret_cast<const uint32_t*>(g + (ks_at & ~3) + bb * 8);
+          }
+          ok &= wait(&sm.k_empty[st.i], empty_parity);
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            put(sm.k[st.i] + row0 + half * 1024 + bb * (kKeys * 128), codes[half][bb],
-                __byte_perm(h, 0, half ? 0x3232 : 0x1010));
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.k_full[st.i]);
+          for (int bb = 0; bb < D / 64; ++bb) {
+            const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, ks_pick));
 #pragma unroll
-        for (int bb = 0; bb < D / 64; ++bb) {
+            for (int half = 0; half < 2; ++half)
+              put(sm.k[st.i] + row0 + half * 1024 + bb * (kKeys * 128), codes[half][bb],
+                  __byte_perm(h, 0, half ? 0x3232 : 0x1010));
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.k_full[st.i]);
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::v_codes(half * 8, bb * 4) + vc);
-          scales[bb] = *reinterpret_cast<const uint32_t*>(g + vs_at + bb * 64);
-        }
-        ok &= wait(&sm.v_empty[st.i], empty_parity);
-        // what lies past the request's length may be anything: its scale becomes 0
-        const uint32_t keep = (t8 < left ? 0x00ffu : 0u) | (t8 + 8 < left ? 0xff00u : 0u);
+          for (int bb = 0; bb < D / 64; ++bb) {
 #pragma unroll
-        for (int bb = 0; bb < D / 64; ++bb) {
-          const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, vs_pick) & keep);
+            for (int half = 0; half < 2; ++half)
+              codes[half][bb] = *reinterpret_cast<const uint2*>(g + L::v_codes(half * 8, bb * 4) + vc);
+            scales[bb] = *reinterpret_cast<const uint32_t*>(g + vs_at + bb * 64);
+          }
+          ok &= wait(&sm.v_empty[st.i], empty_parity);
+          // what lies past the request's length may be anything: its scale becomes 0
+          const uint32_t keep = (t8 < left ? 0x00ffu : 0u) | (t8 + 8 < left ? 0xff00u : 0u);
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            put(sm.v[st.i] + row0 + half * 1024 + bb * (kKeys * 128), codes[half][bb],
-                __byte_perm(h, 0, half ? 0x3232 : 0x1010));
+          for (int bb = 0; bb < D / 64; ++bb) {
+            const uint32_t h = e4m3x2_to_f16x2(__byte_perm(scales[bb], 0, vs_pick) & keep);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              put(sm.v[st.i] + row0 + half * 1024 + bb * (kKeys * 128), codes[half][bb],
+                  __byte_perm(h, 0, half ? 0x3232 : 0x1010));
+          }
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -591,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scores of the next tile, as soon as the softmax has the tile before in registers
         auto scores = [&]() {
           ok = wait(&sm.k_full[ks.i], ks.parity);
-          const uint64_t b0 = kd + (uint64_t)(ks.i * Smem<D>::kTile >> 4);
+          const uint64_t b0 = kd + (uint64_t)(ks.i * S::kTile >> 4);
           for (int blk = 0; blk < blocks && ok; ++blk) {
             ok = wait(&sm.s_free[blk], free_parity[blk]);
             if (!ok) break;
@@ -622,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < n && ok; ++j) {
           if (j + 1 < n) scores();
           if (ok) ok = wait(&sm.v_full[vs.i], vs.parity);
-          const uint64_t b0 = vd + (uint64_t)(vs.i * Smem<D>::kTile >> 4);
+          const uint64_t b0 = vd + (uint64_t)(vs.i * S::kTile >> 4);
           for (int blk = 0; blk < blocks && ok; ++blk) {
             ok = wait(&sm.p_full[blk], p_full[blk].parity);
             if (!ok) break;
@@ -733,12 +868,13 @@ size_t layout(const View& c, const AttentionArgs& a, uint8_t* ws, Plan* plan) {
   return at;
 }
 
-template <int D>
+template <int BITS, int D>
 cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cudaStream_t st) {
   static PerDeviceInit init;
-  constexpr int kSmem = (int)sizeof(Smem<D>) + 1024;
+  constexpr int kSmem = (int)sizeof(Smem<BITS, D>) + 1024;
+  static_assert(kSmem <= 227 * 1024, "more shared memory than a CTA has");
   cudaError_t e = init.run([&] {
-    return cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(chunk_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kSmem);
   });
   if (e != cudaSuccess) return e;
@@ -749,7 +885,7 @@ cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cu
                     a.q_head_stride % 8 == 0;
   plan_kernel<<<1, 1024, 0, st>>>(c, a, range, plan, (int)max_entries(c, a));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  chunk_kernel<D><<<ctas, kThreads, kSmem, st>>>(c, a, range, plan, q_vec);
+  chunk_kernel<BITS, D><<<ctas, kThreads, kSmem, st>>>(c, a, range, plan, q_vec);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, D, 4, 1>(c, a, plan.open, plan.o, plan.ml, 0, kRows, ctas, st);
 }
@@ -761,9 +897,10 @@ size_t cache_chunk_workspace_bytes(const View& c, const AttentionArgs& a) {
                            : layout<64>(c, a, nullptr, nullptr);
 }
 
-cudaError_t launch_cache_chunk(const View& c, const AttentionArgs& a, const RowRange& range,
-                               cudaStream_t st) {
-  return a.head_dim == 128 ? run<128>(c, a, range, st) : run<64>(c, a, range, st);
+cudaError_t launch_cache_chunk(int bits, const View& c, const AttentionArgs& a,
+                               const RowRange& range, cudaStream_t st) {
+  if (bits == 8) return a.head_dim == 128 ? run<8, 128>(c, a, range, st) : run<8, 64>(c, a, range, st);
+  return a.head_dim == 128 ? run<4, 128>(c, a, range, st) : run<4, 64>(c, a, range, st);
 }
 
 }  // namespace kda

@@ -6,9 +6,7 @@
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
-#include "kda_byte_cache.cuh"
 #include "kda_cache_attention.cuh"
 
 namespace kda {
@@ -20,16 +18,13 @@ constexpr int kTileGroups = 2;                   // groups of 16 keys in a tile
 constexpr int kTileKeys = kTileGroups * kGroup;  // 32
 constexpr int kMaxSeqs = 1024;                   // requests of one launch (their plan is in smem)
 
-template <int BITS, int D>
-using FormLayout = std::conditional_t<BITS == 4, Layout<D>, Layout8<D>>;
-
-// -m of a row that has seen nothing yet, 8 bits: any score passes it.
-constexpr float kUnset = 1e30f;
-
-// 2^d for d <= 0; 0 where fp32 has no normal number for it.
-__device__ __forceinline__ float power_below(int d) {
-  return d < -126 ? 0.f : __int_as_float((127 + d) << 23);
-}
+// Requests with more rows per kv head than this go to the chunk kernel, whose work for a
+// key is that of 128 rows, or 256, whatever their number.  67 windows with up to 40 rows,
+// three passes here: 172 us, with the requests of more than 32 rows over there 203 (they
+// are a fifth of the keys, and the second set of launches costs 15 us); a pass over all of
+// these keys takes 95 us here, the chunk kernel's only one 200, so four passes lose.  Measured
+// with 8 query heads on a kv head and 128 channels; other shapes go by the same number.
+constexpr int64_t kSplitRows = 48;
 
 // What a launch leaves in the workspace.
 struct Parts {

@@ -297,7 +297,7 @@ struct RowRange;
 }
 bool cache_chunk_wanted(const cache::View& c, const AttentionArgs& a);
 size_t cache_chunk_workspace_bytes(const cache::View& c, const AttentionArgs& a);
-cudaError_t launch_cache_chunk(const cache::View& c, const AttentionArgs& a,
+cudaError_t launch_cache_chunk(int bits, const cache::View& c, const AttentionArgs& a,
                                const cache::RowRange& range, cudaStream_t st);
 
 // The same for the 8-bit cache (kda_byte_cache_store.cu, kda_byte_cache_attention.cu).
