@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 
 struct Source {
   const void* p;
-  int64_t token_stride, head_stride;  // elements
+  int token_stride, head_stride;  // elements
 };
 
 // 8 neighbouring values of a row as they lie in memory.  VEC: 16-byte aligned.
@@ -85,20 +85,53 @@ __device__ __forceinline__ int place8(int i, int c) {
   return V ? Layout8<D>::v_code(i, c) : Layout8<D>::k_code(i, c);
 }
 
-// The run of tokens first .. first + n - 1 of the batch, which fill places of one block; lane k
-// < n has the place of the k-th of them.  All lanes of the warp.
-template <typename T, int D, bool VEC, bool V>
-__device__ __forceinline__ void append_run(uint8_t* group, const T* src, int64_t token_stride,
-                                           int n, int place, bool& not_finite) {
-  constexpr int LANES = D / 8;          // of a token
-  constexpr int AT_ONCE = 32 / LANES;   // tokens
-  constexpr int STEPS = kGroup / AT_ONCE;
+// Magnitude bits of value i, 0 where it is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t finite8(const uint32_t (&w)[2 * sizeof(T)], int i) {
+  const uint32_t m = __float_as_uint(value8<T>(w, i)) & 0x7fffffffu;
+  return m < 0x7f800000u ? m : 0u;
+}
+
+// Zero in place of the bytes of a word that are codes of NaN (0x7f and 0xff).
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  return w & ~__vcmpeq4(w | 0x80808080u, 0xffffffffu);
+}
+
+// How a warp's lanes share the tokens of a run: 8 channels each, AT_ONCE tokens a step.
+template <int D>
+struct Lanes {
+  static constexpr int PER_TOKEN = D / 8, AT_ONCE = 32 / PER_TOKEN, STEPS = kGroup / AT_ONCE;
+  int c, t;
+  __device__ __forceinline__ Lanes() {
+    const int lane = threadIdx.x & 31;
+    c = lane % PER_TOKEN * 8;
+    t = lane / PER_TOKEN;
+  }
+};
+
+// A run of n tokens of the batch, which fill places of one block; lane k < n has the place of
+// the k-th of them.  p: the lane's channels of its first token, whose values are in `first` if
+// HAVE_FIRST.  All lanes of the warp.
+template <typename T, int D, bool VEC, bool V, bool HAVE_FIRST>
+__device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token_stride, int n,
+                                           int place, const uint32_t (&first)[2 * sizeof(T)],
+                                           bool& not_finite) {
+  using W = Lanes<D>;
+  const W at;
   const int lane = threadIdx.x & 31;
-  const int c = lane % LANES * 8, t = lane / LANES;
-  uint32_t w[STEPS][2 * sizeof(T)];
+  uint32_t w[W::STEPS][2 * sizeof(T)];
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s)
-    if (s * AT_ONCE + t < n) fetch8<T, VEC>(src + (s * AT_ONCE + t) * token_stride + c, w[s]);
+  for (int s = 0; s < W::STEPS; ++s) {
+    if (s == 0 && HAVE_FIRST) {
+#pragma unroll
+      for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[0][i] = first[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[s][i] = 0;
+      if (s * W::AT_ONCE + at.t < n) fetch8<T, VEC>(p, w[s]);
+    }
+    p += (int64_t)W::AT_ONCE * token_stride;
+  }
   uint8_t* const exp_at = group + Layout8<D>::kScales + (V ? 1 : 0);
   // places that the run fills, and whether it begins the block anew
   const uint32_t filled = __reduce_or_sync(0xffffffffu, lane < n ? 1u << place : 0u);
@@ -108,111 +141,129 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* src, int64_t
                            : max(kLeastExponent, min((int)*exp_at - kExponentBias, kMostExponent));
   uint32_t top = 0;
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s)
-    if (s * AT_ONCE + t < n) top = max(top, top8<T>(w[s]));
+  for (int s = 0; s < W::STEPS; ++s)
+    if (!HAVE_FIRST || s > 0 || at.t < n) top = max(top, top8<T>(w[s]));
   top = __reduce_max_sync(0xffffffffu, top);
-  if (top >= 0x7f800000u) {  // infinities do not count, NaN becomes zero
+  const bool odd = top >= 0x7f800000u;  // infinities do not count, NaN becomes zero
+  if (odd) {
     not_finite = true;
     top = 0;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      if (s * AT_ONCE + t >= n) continue;
+    for (int s = 0; s < W::STEPS; ++s) {
+      if (HAVE_FIRST && s == 0 && at.t >= n) continue;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t m = __float_as_uint(value8<T>(w[s], i)) & 0x7fffffffu;
-        if (m < 0x7f800000u) top = max(top, m);
-        if (m > 0x7f800000u) {
-          if constexpr (sizeof(T) == 4)
-            w[s][i] = 0;
-          else
-            w[s][i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
-        }
-      }
+      for (int i = 0; i < 8; ++i) top = max(top, finite8<T>(w[s], i));
     }
     top = __reduce_max_sync(0xffffffffu, top);
   }
   const int e = max(exponent_of(top), before);
   if (!fresh && e > before) {
-    // pieces of 8 codes, each of one token: 2 D of them
+    // pieces of 8 codes, each of one token: 2 D of them, four of a lane asked for at once
     const uint32_t f = half_power(e - before);
 #pragma unroll 1
-    for (int p = lane; p < 2 * D; p += 32) {
-      const int i = p / (D / 8);
-      uint2* at = reinterpret_cast<uint2*>(group + place8<D, V>(i, p % (D / 8) * 8));
-      if (filled >> i & 1) continue;
-      const uint2 old = *at;
-      uint32_t h[4];
-      e4m3x4_to_f16(old.x, h[0], h[1]);
-      e4m3x4_to_f16(old.y, h[2], h[3]);
+    for (int q0 = 0; q0 < D / 16; q0 += 4) {
+      uint2 old[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = f16x2_to_e4m3x2(mul_f16x2(h[j], f));
-      *at = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+      for (int q = 0; q < 4; ++q)
+        old[q] = *reinterpret_cast<const uint2*>(
+            group + place8<D, V>((q0 + q) * W::AT_ONCE + at.t, at.c));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = (q0 + q) * W::AT_ONCE + at.t;
+        if (filled >> i & 1) continue;
+        uint32_t h[4];
+        e4m3x4_to_f16(old[q].x, h[0], h[1]);
+        e4m3x4_to_f16(old[q].y, h[2], h[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = f16x2_to_e4m3x2(mul_f16x2(h[j], f));
+        *reinterpret_cast<uint2*>(group + place8<D, V>(i, at.c)) =
+            make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+      }
     }
   }
   const float down = __int_as_float((127 - e) << 23);
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int i = __shfl_sync(0xffffffffu, place, (s * AT_ONCE + t) & 31);
-    if (s * AT_ONCE + t < n) {
+  for (int s = 0; s < W::STEPS; ++s) {
+    const int i = __shfl_sync(0xffffffffu, place, (s * W::AT_ONCE + at.t) & 31);
+    if (s * W::AT_ONCE + at.t < n) {
       uint32_t b[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         b[j] = f32x2_to_e4m3x2(value8<T>(w[s], 2 * j) * down, value8<T>(w[s], 2 * j + 1) * down);
-      *reinterpret_cast<uint2*>(group + place8<D, V>(i, c)) =
-          make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+      uint2 codes = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+      if (odd) codes = make_uint2(without_nan(codes.x), without_nan(codes.y));
+      *reinterpret_cast<uint2*>(group + place8<D, V>(i, at.c)) = codes;
     }
   }
   if (lane == 0) *exp_at = (uint8_t)(e + kExponentBias);
 }
 
-// A warp takes the runs that start among `window` tokens (at most 16), of one head, of K or V.
-template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(View c, int tokens, int window, Source k, Source v,
-                  const int64_t* __restrict__ slots, int* err) {
+// A warp takes the runs that start among WINDOW tokens (16 or 1), of one head, of K or V.
+template <typename T, int D, bool VEC, int WINDOW, bool V>
+__device__ __forceinline__ void append_window(const View& c, int tokens, const Source& src,
+                                              const int64_t* __restrict__ slots, int* err) {
   const int lane = threadIdx.x & 31;
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int heads = c.kv_heads;
-  const int64_t at = unit / (2 * heads);
-  const int which = (int)(unit - at * 2 * heads);
-  const int head = which % heads;
-  const bool is_v = which >= heads;
-  const int64_t start = at * window;
+  const int64_t window = unit / c.kv_heads;
+  const int head = (int)(unit - window * c.kv_heads);
+  const int64_t start = window * WINDOW;
   if (start >= tokens) return;
+  const Lanes<D> mine;
+  const T* p = static_cast<const T*>(src.p) + (start + mine.t) * src.token_stride +
+               (int64_t)head * src.head_stride + mine.c;
   // lane l: the slot of token start - 1 + l, as far as a run of the window may reach
   const int64_t token = start - 1 + lane;
   int64_t slot = -1;
-  if (token >= 0 && token < tokens && lane < window + kGroup) slot = __ldg(slots + token);
+  if (token >= 0 && token < tokens && lane < WINDOW + kGroup) slot = __ldg(slots + token);
+  // Its tokens' values are on their way to L2 while the slots are: which of them a run takes,
+  // these or some of the next window's, hangs on the slots.
+  if constexpr (WINDOW > 1) {
+    constexpr int kLines = D * (int)sizeof(T) / 128;
+#pragma unroll
+    for (int i = lane; i < WINDOW * kLines; i += 32)
+      if (start + i / kLines < tokens)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            static_cast<const T*>(src.p) + (start + i / kLines) * src.token_stride +
+            (int64_t)head * src.head_stride + i % kLines * (128 / (int)sizeof(T))));
+  }
+  // a single token's values are under way before its slot is known
+  uint32_t first[2 * sizeof(T)] = {};
+  if (WINDOW == 1 && start + mine.t < tokens) fetch8<T, VEC>(p, first);
   const bool there = slot >= 0 && slot < (int64_t)c.num_pages * c.page_size;
-  const bool mine = lane >= 1 && lane <= window;
-  if (!there && slot != -1 && mine && which == 0) report_error(err, kErrDeviceCheck);
+  const bool counts = lane >= 1 && lane <= WINDOW;
+  if (!there && slot != -1 && counts && head == 0 && !V) report_error(err, kErrDeviceCheck);
   const int block = there ? (int)(slot / kGroup) : -1;  // fewer than 2^27
   const int prev = __shfl_up_sync(0xffffffffu, block, 1);
   const bool goes_on = there && lane > 0 && prev == block;
   const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
-  uint32_t heads_of = __ballot_sync(0xffffffffu, mine && there && !goes_on);
+  uint32_t starts = __ballot_sync(0xffffffffu, counts && there && !goes_on);
   bool not_finite = false;
   const int groups = c.page_size / kGroup;
-  for (; heads_of; heads_of &= heads_of - 1) {
-    const int l = __ffs(heads_of) - 1;
+  for (; starts; starts &= starts - 1) {
+    const int l = __ffs(starts) - 1;
     // tokens l, l + 1, ... as long as they go on
-    const uint32_t after = l == 31 ? 0u : ~(on >> (l + 1));
+    const uint32_t after = ~(on >> (l + 1));
     const int n = min(after ? __ffs(after) : 32, kGroup);
     const int place = __shfl_sync(0xffffffffu, (int)(slot & (kGroup - 1)), (l + lane) & 31);
     const int b = __shfl_sync(0xffffffffu, block, l);
     const int page = b / groups;
     uint8_t* group =
-        c.pages + (((int64_t)page * heads + head) * groups + (b - page * groups)) *
+        c.pages + (((int64_t)page * c.kv_heads + head) * groups + (b - page * groups)) *
                       Layout8<D>::kGroupBytes;
-    const Source& s = is_v ? v : k;
-    const T* src = static_cast<const T*>(s.p) + (start - 1 + l) * s.token_stride +
-                   head * s.head_stride;
-    if (is_v)
-      append_run<T, D, VEC, true>(group, src, s.token_stride, n, place, not_finite);
-    else
-      append_run<T, D, VEC, false>(group, src, s.token_stride, n, place, not_finite);
+    append_run<T, D, VEC, V, WINDOW == 1>(group, p + (int64_t)(l - 1) * src.token_stride,
+                                          src.token_stride, n, place, first, not_finite);
   }
   if (not_finite && lane == 0) report_error(err, kErrDeviceCheck);
+}
+
+template <typename T, int D, bool VEC, int WINDOW>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && WINDOW > 1 ? 3 : 2)
+    append_kernel(View c, int tokens, Source k, Source v, const int64_t* __restrict__ slots,
+                  int* err) {
+  if (blockIdx.y)
+    append_window<T, D, VEC, WINDOW, true>(c, tokens, v, slots, err);
+  else
+    append_window<T, D, VEC, WINDOW, false>(c, tokens, k, slots, err);
 }
 
 template <typename T>
@@ -286,18 +337,24 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// From so many rows (tokens x heads) on a warp takes the runs of 16 tokens, not of one.
+constexpr int64_t kManyRows = 1 << 17;
+
 template <typename T, int D>
 cudaError_t append(const CacheArgs& a, cudaStream_t st) {
-  const Source k{a.k, a.strides[0], a.strides[1]}, v{a.v, a.strides[2], a.strides[3]};
+  const Source k{a.k, (int)a.strides[0], (int)a.strides[1]},
+      v{a.v, (int)a.strides[2], (int)a.strides[3]};
   const int el = 16 / sizeof(T);
   bool vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0;
   for (int64_t s : a.strides) vec = vec && s % el == 0;
-  const int window = (int64_t)a.tokens * a.view.kv_heads >= 1 << 17 ? kGroup : 1;
-  const int64_t units = ((int64_t)a.tokens + window - 1) / window * 2 * a.view.kv_heads;
+  const int window = (int64_t)a.tokens * a.view.kv_heads >= kManyRows ? kGroup : 1;
+  const int64_t units = ((int64_t)a.tokens + window - 1) / window * a.view.kv_heads;
   const int64_t ctas = (units * 32 + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  auto* kernel = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
-  kernel<<<(unsigned)ctas, kThreads, 0, st>>>(a.view, a.tokens, window, k, v, a.slots, a.err);
+  auto* kernel = window == 1 ? (vec ? append_kernel<T, D, true, 1> : append_kernel<T, D, false, 1>)
+                 : vec       ? append_kernel<T, D, true, kGroup>
+                             : append_kernel<T, D, false, kGroup>;
+  kernel<<<dim3((unsigned)ctas, 2), kThreads, 0, st>>>(a.view, a.tokens, k, v, a.slots, a.err);
   return cudaGetLastError();
 }
 

@@ -213,7 +213,7 @@ struct Dequant8 {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       if constexpr (V)
-        w[n] = *reinterpret_cast<const uint4*>(g + Layout8<D>::kVCodes + n * 512 + lane * 16);
+        w[n] = *reinterpret_cast<const uint4*>(g + Layout8<D>::kVCodes + sub_of(n) * 512 + lane * 16);
       else  // two keys a time, of channels 32 t + 16 h .. in opposite orders
         w[n] = *reinterpret_cast<const uint4*>(g + half_of(n) * 1024 + key_of(n) * 64 + t * 16);
     }
@@ -225,6 +225,10 @@ struct Dequant8 {
   }
   __device__ __forceinline__ static int half_of(int n) {
     return D == 64 ? 0 : (n >> 1) ^ (threadIdx.x >> 1 & 1);
+  }
+  // V: the sub-block of piece n (D = 128), in opposite orders for neighbouring channels
+  __device__ __forceinline__ static int sub_of(int n) {
+    return D == 64 ? n : n ^ (threadIdx.x >> 2 & 1);
   }
   // Eight halves of codes x, y to chunk `chunk` of row `row`.
   __device__ __forceinline__ static void put(uint8_t* tile, int row, int chunk, uint32_t x,
@@ -251,13 +255,12 @@ struct Dequant8 {
         put(tile, row, chunk, w[n].x, w[n].y, f);
         put(tile, row, chunk + 1, w[n].z, w[n].w, f);
       } else if constexpr (D == 128) {
-        // sub-block n of tokens 8 (n / 2) + 2 t + n % 2, channels 16 (lane / 4) ..
-        const int i = 8 * (n >> 1) + 2 * t + (n & 1), g = lane >> 2;
-        const bool there = i < left;
-        const uint4 x = there ? w[n] : make_uint4(0, 0, 0, 0);
-        const bool swap = g & 1;
-        put(tile, dw * kGroup + i, 2 * g + swap, swap ? x.z : x.x, swap ? x.w : x.y, f);
-        put(tile, dw * kGroup + i, 2 * g + !swap, swap ? x.x : x.z, swap ? x.y : x.w, f);
+        // tokens 8 (sub / 2) + 2 t + sub % 2, channels 16 (lane / 4) ..
+        const int sub = sub_of(n), i = 8 * (sub >> 1) + 2 * t + (sub & 1), g = lane >> 2;
+        uint4 x = w[n];
+        if (left < kGroup && i >= left) x = make_uint4(0, 0, 0, 0);
+        put(tile, dw * kGroup + i, 2 * g, x.x, x.y, f);
+        put(tile, dw * kGroup + i, 2 * g + 1, x.z, x.w, f);
       } else {
         // two sub-blocks a time, tokens 2 t and 2 t + 2 of 8 channels a lane
         const int sub = 2 * n + (lane >> 4), g = lane >> 1 & 7;
@@ -498,14 +501,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // 8 bits: weights times 2^(v_top - v_ref), which the sums take back.  Values so far below
-        // the largest that a weight could get lost in fp32 count for nothing.
-        const int under = BITS == 4 ? 0 : v_top - v_ref;
-        const bool drop = under < -60;
-        const float shift = drop ? 0.f : (float)under;
+        // 8 bits: weights times 2^(v_top - v_ref), which the sums take back.  2^-60 at least, or a
+        // weight could get lost in fp32: far less than a half holds of the largest either way.
+        const int shift = BITS == 4 ? 0 : max(v_top - v_ref, -60);
         uint64_t lt[2] = {0, 0};
         uint64_t(&sum)[2] = BITS == 4 ? l2 : lt;
-        const uint64_t f2 = tc::pack2(ft, ft), neg2 = tc::pack2(neg + shift, neg + shift);
+        const uint64_t f2 = tc::pack2(ft, ft), neg2 = tc::pack2(neg + (float)shift, neg + (float)shift);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t w[16];
@@ -519,10 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[i & 1] = tc::add2(sum[i & 1], tc::pack2(p0, p1));
             w[i] = tc::pack_f16(p0, p1);
           }
-          if (BITS == 8 && drop) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = 0;
-          }
           if (half == 0 && j > p.begin) {  // the product before has read its weights
             if (!waited && !wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY, gave_up = true;
             o_full.step();
@@ -531,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_st16u(tp + half * 16, w);
         }
         if constexpr (BITS == 8) {
-          const float up = __int_as_float((127 - (int)shift) << 23);
+          const float up = __int_as_float((127 - shift) << 23);
           l2[0] = tc::fma2(lt[0], tc::pack2(up, up), l2[0]);
           l2[1] = tc::fma2(lt[1], tc::pack2(up, up), l2[1]);
         }
