@@ -6,8 +6,11 @@
 // kda_cache_tables cannot disagree about it.  Each call marks the pages of a table's rows in a
 // bitmap (a bit a page, set by an atomic OR: the order does not matter), and everything else
 // follows from sums over the bitmap's words in the pages' order, which one CTA takes: 32 pages
-// a word, so 131072 pages are four words a thread.  What bounds the calls is the chain of
-// launches and dependent loads; what bounds the copies is HBM.
+// a word, so 131072 pages are four words a thread.
+//
+// What bounds the calls is the chain of dependent loads, and launches: the steps of a call (rows
+// settled, pages marked, sums, new rows) run in one cluster of CTAs with barriers between them,
+// or, for large tables, as a kernel each over the whole GPU.
 #include <algorithm>
 
 #include "kda_common.cuh"
@@ -17,6 +20,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 1024;  // of the CTA that sums
+constexpr int kBatch = 4;       // entries of a table that a thread has under way
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int page) {
   return (int)((tokens + page - 1) / page);
@@ -28,14 +32,80 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// All CTAs of the cluster, and their memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+
+// The CTAs that share a step: this one's number and how many they are.
+struct Crew {
+  uint32_t cta, ctas;
+  __device__ __forceinline__ uint32_t thread() const { return cta * blockDim.x + threadIdx.x; }
+  __device__ __forceinline__ uint32_t threads() const { return ctas * blockDim.x; }
+};
+__device__ __forceinline__ Crew grid_crew() { return Crew{blockIdx.x, gridDim.x}; }
+
 __device__ __forceinline__ void set_bit(uint32_t* map, int page) {
-  const uint32_t bit = 1u << (page & 31);
-  uint32_t* w = map + (page >> 5);
-  // shared pages are marked by many rows; a stale word only costs the atomic
-  if (!(*(volatile uint32_t*)w & bit)) atomicOr(w, bit);
+  atomicOr(map + (page >> 5), 1u << (page & 31));
 }
 __device__ __forceinline__ bool bit_of(const uint32_t* map, int page) {
   return map[page >> 5] >> (page & 31) & 1;
+}
+
+// Marks the pages of a batch; shared ones are marked by many rows, so their words are looked at
+// first (a stale one only costs the atomic).  A page of -1 is none.
+__device__ __forceinline__ void set_bits(uint32_t* map, const int (&page)[kBatch]) {
+  uint32_t w[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    w[j] = page[j] >= 0 ? *(volatile uint32_t*)(map + (page[j] >> 5)) : ~0u;
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (!(w[j] >> (page[j] & 31) & 1)) set_bit(map, page[j]);
+}
+
+// Whether a row of a table makes sense.
+__device__ __forceinline__ bool sound(int held, int page_size, int max_blocks) {
+  return held >= 0 && pages_of(held, page_size) <= max_blocks;
+}
+
+// Marks the pages that rows hold.
+__device__ __forceinline__ void mark_rows(uint32_t* map, const int32_t* table, const int32_t* lens,
+                                          int rows, int columns, int page_size, int num_pages,
+                                          int* err, Crew crew) {
+  const uint64_t total = (uint64_t)(uint32_t)rows * (uint32_t)columns, step = crew.threads();
+  for (uint64_t i = crew.thread(); i < total; i += kBatch * step) {
+    int held[kBatch], page[kBatch];
+    uint32_t col[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint64_t e = i + j * step;
+      held[j] = 0;
+      col[j] = 0;
+      if (e < total) {
+        const uint32_t row = (uint32_t)e / (uint32_t)columns;
+        col[j] = (uint32_t)e - row * (uint32_t)columns;
+        held[j] = lens[row];
+      }
+    }
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      page[j] = -1;
+      if (sound(held[j], page_size, columns) && col[j] < (uint32_t)pages_of(held[j], page_size))
+        page[j] = table[i + j * step];
+      else
+        col[j] = ~0u;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (col[j] != ~0u && (page[j] < 0 || page[j] >= num_pages)) page[j] = -1, bad = true;
+    if (bad) report_error(err, kErrDeviceCheck);
+    set_bits(map, page);
+  }
 }
 
 // Sums of the CTA's threads before this one; `total` gets the sum of all.
@@ -76,17 +146,20 @@ struct ForkScratch {
 
 // Zeroes the bitmaps and settles each new row: a row whose parent or length does not make sense
 // keeps nothing.
-__global__ void __launch_bounds__(256) fork_rows_kernel(ForkArgs a, ForkScratch s, int words) {
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x, n = gridDim.x * 256;
+__device__ __forceinline__ void fork_rows(const ForkArgs& a, const ForkScratch& s, int words,
+                                          Crew crew) {
+  const uint32_t i = crew.thread(), n = crew.threads();
   for (uint32_t w = i; w < (uint32_t)words; w += n)
     s.old_map[w] = s.whole_map[w] = s.tail_map[w] = 0;
   const int P = a.page_size;
+  for (uint32_t r = i; r < (uint32_t)a.old_seqs; r += n)  // its pages stay where they are
+    if (!sound(a.held_lens[r], P, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
   for (uint32_t b = i; b < (uint32_t)a.num_seqs; b += n) {
     const int parent = a.parents[b];
     Row r{0, -1};
     if (parent >= 0 && parent < a.old_seqs) {
       const int held = a.held_lens[parent], keep = a.keep_lens[b];
-      if (held >= 0 && pages_of(held, P) <= a.max_blocks && keep >= 0 && keep <= held) {
+      if (sound(held, P, a.max_blocks) && keep >= 0 && keep <= held) {
         r.keep = keep;
         if (keep % P) {
           const int page = a.block_table[(int64_t)parent * a.max_blocks + keep / P];
@@ -105,55 +178,52 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(ForkArgs a, ForkScratch 
   }
 }
 
-constexpr int kColumns = 1024;  // of a row that one CTA takes
-// The first of them (grid_of); columns count up in 32 bits without a sign.
-__device__ __forceinline__ int64_t first_column() {
-  return ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * kColumns;
+__device__ __forceinline__ void fork_mark_old(const ForkArgs& a, const ForkScratch& s, Crew crew) {
+  mark_rows(s.old_map, a.block_table, a.held_lens, a.old_seqs, a.max_blocks, a.page_size,
+            a.num_pages, a.err, crew);
 }
 
-// Marks the old rows' pages; writes the new rows and marks theirs.
-__global__ void __launch_bounds__(256) fork_mark_kernel(ForkArgs a, ForkScratch s) {
-  wait_for_previous();
+// Writes the new rows and marks their pages.
+__device__ __forceinline__ void fork_mark_new(const ForkArgs& a, const ForkScratch& s, Crew crew) {
   const int P = a.page_size;
-  const int64_t col0 = first_column();
-  if (col0 >= a.max_blocks) return;
-  const int cols = (int)min((int64_t)a.max_blocks, col0 + kColumns);
-  for (uint32_t r = blockIdx.x; r < (uint32_t)a.old_seqs + (uint32_t)a.num_seqs; r += gridDim.x) {
-    if (r < (uint32_t)a.old_seqs) {
-      const int held = a.held_lens[r];
-      if (held < 0 || pages_of(held, P) > a.max_blocks) {  // its pages stay where they are
-        if (threadIdx.x == 0 && col0 == 0) report_error(a.err, kErrDeviceCheck);
-        continue;
+  for (uint32_t b = crew.thread(); b < (uint32_t)a.num_seqs; b += crew.threads()) {
+    const int tail = s.rows[b].tail;
+    if (tail >= 0) atomicMin(s.first + tail, (int)b);
+  }
+  const uint64_t total = (uint64_t)a.num_seqs * a.max_blocks, step = crew.threads();
+  for (uint64_t i = crew.thread(); i < total; i += kBatch * step) {
+    int keep[kBatch], parent[kBatch], page[kBatch];
+    uint32_t col[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint64_t e = i + j * step;
+      keep[j] = parent[j] = 0;
+      col[j] = 0;
+      if (e < total) {
+        const uint32_t row = (uint32_t)e / (uint32_t)a.max_blocks;
+        col[j] = (uint32_t)e - row * (uint32_t)a.max_blocks;
+        keep[j] = s.rows[row].keep;
+        parent[j] = a.parents[row];
       }
-      const int n = min(cols, pages_of(held, P));
-      for (uint32_t c = (uint32_t)col0 + threadIdx.x; c < (uint32_t)n; c += 256) {
-        const int page = a.block_table[(int64_t)r * a.max_blocks + c];
-        if (page >= 0 && page < a.num_pages)
-          set_bit(s.old_map, page);
-        else
-          report_error(a.err, kErrDeviceCheck);
-      }
-    } else {
-      const int b = (int)(r - a.old_seqs);
-      const Row row = s.rows[b];
-      const int whole = row.keep / P, n = pages_of(row.keep, P);
-      const int32_t* from = a.block_table + (int64_t)max(0, a.parents[b]) * a.max_blocks;
-      int32_t* to = a.block_table_out + (int64_t)b * a.max_blocks;
-      for (uint32_t c = (uint32_t)col0 + threadIdx.x; c < (uint32_t)cols; c += 256) {
-        const int page = c < (uint32_t)n ? from[c] : -1;
-        to[c] = page;
-        if (c < (uint32_t)whole && page >= 0 && page < a.num_pages) set_bit(s.whole_map, page);
-      }
-      if (threadIdx.x == 0 && col0 == 0 && row.tail >= 0) atomicMin(s.first + row.tail, b);
     }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      page[j] = col[j] < (uint32_t)pages_of(keep[j], P)
+                    ? a.block_table[(int64_t)parent[j] * a.max_blocks + col[j]]
+                    : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint64_t e = i + j * step;
+      if (e < total) a.block_table_out[e] = page[j];
+      if (col[j] >= (uint32_t)(keep[j] / P) || page[j] >= a.num_pages) page[j] = -1;
+    }
+    set_bits(s.whole_map, page);
   }
 }
 
-// Settles the unfinished last pages and gives back what nobody holds.
-__global__ void __launch_bounds__(kThreads) fork_settle_kernel(ForkArgs a, ForkScratch s,
-                                                               int words) {
-  __shared__ int warp_sums[32];
-  wait_for_previous();
+// Settles the unfinished last pages and gives back what nobody holds: one CTA.
+__device__ __forceinline__ void fork_settle(const ForkArgs& a, const ForkScratch& s, int words,
+                                            int* warp_sums) {
   const int P = a.page_size;
   int64_t head = a.free_range[0], tail = a.free_range[1];
   if (!(head >= 0 && tail >= head && tail - head <= a.ring_size)) {
@@ -161,6 +231,10 @@ __global__ void __launch_bounds__(kThreads) fork_settle_kernel(ForkArgs a, ForkS
     if (threadIdx.x == 0) report_error(a.err, kErrDeviceCheck);
   }
   const int64_t avail = tail - head;
+  // the ring runs on from its head without a division: a row's place in it is less than two turns
+  // off as long as no more pages are asked for than there are
+  const int64_t head0 = head % a.ring_size, tail0 = tail % a.ring_size;
+  auto in_ring = [&](int64_t at) { return at < a.ring_size ? at : at % a.ring_size; };
   int64_t asked = 0;
   for (uint32_t base = 0; base < (uint32_t)a.num_seqs; base += kThreads) {
     const uint32_t b = base + threadIdx.x;
@@ -181,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) fork_settle_kernel(ForkArgs a, ForkS
         int32_t* entry = a.block_table_out + (int64_t)b * a.max_blocks + r.keep / P;
         if (at < avail) {
           copy[0] = r.tail;
-          copy[1] = a.free_pages[(head + at) % a.ring_size];
+          copy[1] = a.free_pages[in_ring(head0 + at)];
           copy[2] = r.keep % P;
           *entry = copy[1];
         } else {  // no page is left: the row ends with its last whole one
@@ -203,16 +277,46 @@ __global__ void __launch_bounds__(kThreads) fork_settle_kernel(ForkArgs a, ForkS
   int count = 0, freed;
   for (int w = w0; w < w1; ++w)
     count += __popc(s.old_map[w] & ~(s.whole_map[w] | *(volatile uint32_t*)(s.tail_map + w)));
-  int64_t at = block_scan(count, warp_sums, freed) + tail;
+  int64_t at = block_scan(count, warp_sums, freed) + tail0;
   for (int w = w0; w < w1; ++w) {
     uint32_t gone = s.old_map[w] & ~(s.whole_map[w] | *(volatile uint32_t*)(s.tail_map + w));
-    for (; gone; gone &= gone - 1) a.free_pages[at++ % a.ring_size] = w * 32 + __ffs(gone) - 1;
+    for (; gone; gone &= gone - 1) a.free_pages[in_ring(at++)] = w * 32 + __ffs(gone) - 1;
   }
   if (threadIdx.x == 0) {
     a.free_range_out[0] = head + taken;
     a.free_range_out[1] = tail + freed;
     if (avail - taken + freed > a.ring_size) report_error(a.err, kErrDeviceCheck);
   }
+}
+
+constexpr int kCluster = 8;  // CTAs of kThreads that take a call in one launch
+
+__global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, ForkScratch s, int words) {
+  __shared__ int warp_sums[32];
+  fork_rows(a, s, words, grid_crew());
+  cluster_sync();
+  const Crew half{blockIdx.x % (kCluster / 2), kCluster / 2};  // side by side, not in turn
+  if (blockIdx.x < kCluster / 2)
+    fork_mark_old(a, s, half);
+  else
+    fork_mark_new(a, s, half);
+  cluster_sync();
+  if (blockIdx.x == 0) fork_settle(a, s, words, warp_sums);
+}
+// The same as a kernel each.
+__global__ void __launch_bounds__(256) fork_rows_kernel(ForkArgs a, ForkScratch s, int words) {
+  fork_rows(a, s, words, grid_crew());
+}
+__global__ void __launch_bounds__(256) fork_mark_kernel(ForkArgs a, ForkScratch s) {
+  wait_for_previous();
+  fork_mark_old(a, s, grid_crew());
+  fork_mark_new(a, s, grid_crew());
+}
+__global__ void __launch_bounds__(kThreads) fork_settle_kernel(ForkArgs a, ForkScratch s,
+                                                               int words) {
+  __shared__ int warp_sums[32];
+  wait_for_previous();
+  fork_settle(a, s, words, warp_sums);
 }
 
 // --------------------------------------------------------------- compact ----
@@ -223,36 +327,24 @@ struct CompactScratch {
   int32_t* count;    // pages in use
 };
 
-__global__ void __launch_bounds__(256) compact_clear_kernel(CompactScratch s, int words) {
-  for (uint32_t w = blockIdx.x * 256 + threadIdx.x; w < (uint32_t)words; w += gridDim.x * 256)
-    s.live[w] = 0;
+__device__ __forceinline__ void compact_clear(const CompactArgs& a, const CompactScratch& s,
+                                              int words, Crew crew) {
+  for (uint32_t w = crew.thread(); w < (uint32_t)words; w += crew.threads()) s.live[w] = 0;
+  for (uint32_t r = crew.thread(); r < (uint32_t)a.num_seqs; r += crew.threads())
+    if (!sound(a.held_lens[r], a.page_size, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
 }
 
-__global__ void __launch_bounds__(256) compact_mark_kernel(CompactArgs a, CompactScratch s) {
-  wait_for_previous();
-  const int64_t col0 = first_column();
-  for (uint32_t r = blockIdx.x; r < (uint32_t)a.num_seqs; r += gridDim.x) {
-    const int held = a.held_lens[r];
-    const bool sound = held >= 0 && pages_of(held, a.page_size) <= a.max_blocks;
-    if (!sound && threadIdx.x == 0 && col0 == 0) report_error(a.err, kErrDeviceCheck);
-    const int n = sound ? (int)min(col0 + kColumns, (int64_t)pages_of(held, a.page_size)) : 0;
-    for (uint32_t c = (uint32_t)col0 + threadIdx.x; c < (uint32_t)n; c += 256) {
-      const int page = a.block_table[(int64_t)r * a.max_blocks + c];
-      if (page >= 0 && page < a.num_pages)
-        set_bit(s.live, page);
-      else
-        report_error(a.err, kErrDeviceCheck);
-    }
-  }
+__device__ __forceinline__ void compact_mark(const CompactArgs& a, const CompactScratch& s,
+                                             Crew crew) {
+  mark_rows(s.live, a.block_table, a.held_lens, a.num_seqs, a.max_blocks, a.page_size, a.num_pages,
+            a.err, crew);
 }
 
 // Pages in use before each word, and the list of moves: the i-th page in use at or past their
 // number L goes to the i-th free one below it.
-__global__ void __launch_bounds__(kThreads) compact_plan_kernel(CompactArgs a, CompactScratch s,
-                                                                int words) {
-  __shared__ int warp_sums[32];
-  __shared__ int before_l;
-  wait_for_previous();
+// One CTA.
+__device__ __forceinline__ void compact_plan(const CompactArgs& a, const CompactScratch& s,
+                                             int words, int* warp_sums, int& before_l) {
   const int per = (words + kThreads - 1) / kThreads;
   const int w0 = min(words, per * (int)threadIdx.x), w1 = min(words, w0 + per);
   int count = 0, L;
@@ -296,35 +388,81 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(CompactArgs a, C
 }
 
 // The rows with the pages' new numbers, and the ring.
-__global__ void __launch_bounds__(256) compact_rows_kernel(CompactArgs a, CompactScratch s) {
-  wait_for_previous();
+__device__ __forceinline__ void compact_rows(const CompactArgs& a, const CompactScratch& s,
+                                             Crew crew) {
   const int L = s.count[0];
   // pages in use below L: those that stay
   const int stay = L < a.num_pages
                        ? s.before[L >> 5] + __popc(s.live[L >> 5] & ((1u << (L & 31)) - 1))
                        : L;
-  const int64_t col0 = first_column();
-  const int cols = (int)min((int64_t)a.max_blocks, col0 + kColumns);
-  for (uint32_t r = blockIdx.x; r < (uint32_t)a.num_seqs; r += gridDim.x) {
-    const int held = a.held_lens[r];
-    const bool sound = held >= 0 && pages_of(held, a.page_size) <= a.max_blocks;
-    const int n = sound ? pages_of(held, a.page_size) : 0;
-    for (uint32_t c = (uint32_t)col0 + threadIdx.x; c < (uint32_t)cols; c += 256) {
-      const int64_t at = (int64_t)r * a.max_blocks + c;
-      int page = c < (uint32_t)n ? a.block_table[at] : -1;
-      if (page >= L && page < a.num_pages) {
-        const int rank = s.before[page >> 5] +
-                         __popc(s.live[page >> 5] & ((1u << (page & 31)) - 1)) - stay;
-        page = a.copies[3 * (int64_t)rank + 1];
+  const uint64_t total = (uint64_t)a.num_seqs * a.max_blocks, step = crew.threads();
+  for (uint64_t i = crew.thread(); i < total; i += kBatch * step) {
+    int held[kBatch], page[kBatch];
+    uint32_t col[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint64_t e = i + j * step;
+      held[j] = 0;
+      col[j] = 0;
+      if (e < total) {
+        const uint32_t row = (uint32_t)e / (uint32_t)a.max_blocks;
+        col[j] = (uint32_t)e - row * (uint32_t)a.max_blocks;
+        held[j] = a.held_lens[row];
       }
-      a.block_table_out[at] = page;
     }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      page[j] = sound(held[j], a.page_size, a.max_blocks) &&
+                        col[j] < (uint32_t)pages_of(held[j], a.page_size)
+                    ? a.block_table[i + j * step]
+                    : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (page[j] >= L && page[j] < a.num_pages) {
+        const int w = page[j] >> 5;
+        const int rank =
+            s.before[w] + __popc(s.live[w] & ((1u << (page[j] & 31)) - 1)) - stay;
+        page[j] = a.copies[3 * (int64_t)rank + 1];
+      }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (i + j * step < total) a.block_table_out[i + j * step] = page[j];
   }
-  if (blockIdx.z) return;
-  const int64_t n = (int64_t)gridDim.x * gridDim.y * 256;
-  for (int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-       i < a.num_pages - L; i += n)
+  for (int64_t i = crew.thread(); i < a.num_pages - L; i += crew.threads())
     a.free_pages[i] = L + (int)i;
+}
+
+__global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, CompactScratch s,
+                                                           int words) {
+  __shared__ int warp_sums[32];
+  __shared__ int before_l;
+  compact_clear(a, s, words, grid_crew());
+  cluster_sync();
+  compact_mark(a, s, grid_crew());
+  cluster_sync();
+  if (blockIdx.x == 0) compact_plan(a, s, words, warp_sums, before_l);
+  cluster_sync();
+  compact_rows(a, s, grid_crew());
+}
+// The same as a kernel each.
+__global__ void __launch_bounds__(256) compact_clear_kernel(CompactArgs a, CompactScratch s,
+                                                            int words) {
+  compact_clear(a, s, words, grid_crew());
+}
+__global__ void __launch_bounds__(256) compact_mark_kernel(CompactArgs a, CompactScratch s) {
+  wait_for_previous();
+  compact_mark(a, s, grid_crew());
+}
+__global__ void __launch_bounds__(kThreads) compact_plan_kernel(CompactArgs a, CompactScratch s,
+                                                                int words) {
+  __shared__ int warp_sums[32];
+  __shared__ int before_l;
+  wait_for_previous();
+  compact_plan(a, s, words, warp_sums, before_l);
+}
+__global__ void __launch_bounds__(256) compact_rows_kernel(CompactArgs a, CompactScratch s) {
+  wait_for_previous();
+  compact_rows(a, s, grid_crew());
 }
 
 // ------------------------------------------------------------------ copy ----
@@ -333,50 +471,66 @@ struct Layers {
   uint8_t* pages[kCopyLayers];
 };
 
-constexpr int kVecs = 8;                       // 16-byte words of a thread under way
-constexpr int kPart = 256 * kVecs;             // words of a CTA's part of a page
+constexpr int kVecs = 8;            // 16-byte words of a thread under way
+constexpr int kPart = 256 * kVecs;  // words of a part of a page at most
+constexpr int kList = 256;          // items that a CTA looks at in one go
 
-// The items (copy, layer, part of a page) are dealt out to the CTAs in turn.
-__global__ void __launch_bounds__(256) copy_kernel(CopyArgs a, Layers layers, int parts) {
+// The items (copy, layer, part of a page) are dealt out to the CTAs in turn.  A list of copies
+// may be empty for the most part: a CTA looks at its items together, a thread each, and keeps
+// those that ask for something.
+__global__ void __launch_bounds__(256, 4) copy_kernel(CopyArgs a, Layers layers, int parts,
+                                                      int part_vecs) {
+  __shared__ int4 list[kList];  // from, to, tokens, layer and part
+  __shared__ int count;
   wait_for_previous();
-  const int group_vecs = a.group_bytes / 16;
-  const int64_t head_vecs = (int64_t)a.groups * group_vecs, page_vecs = head_vecs * a.runs;
-  const int64_t items = (int64_t)a.num_copies * a.num_layers * parts;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int part = (int)(item % parts);
-    const int64_t rest = item / parts;
-    const int layer = (int)(rest % a.num_layers);
-    const int32_t* copy = a.copies + 3 * (rest / a.num_layers);
-    const int from = __ldg(copy), to = __ldg(copy + 1), tokens = __ldg(copy + 2);
-    if (from == -1 || tokens == 0 || from == to) continue;
-    if (from < 0 || from >= a.num_pages || to < 0 || to >= a.num_pages || tokens < 0 ||
-        tokens > a.groups * 16) {
-      if (threadIdx.x == 0) report_error(a.err, kErrDeviceCheck);
-      continue;
-    }
-    // the groups in use of each head, one run where that is all of them
-    const int groups = (tokens + 15) / 16;
-    const bool all = groups == a.groups;
-    const uint32_t run = all ? (uint32_t)page_vecs : (uint32_t)(groups * group_vecs);
-    const uint32_t vecs = all ? run : run * (uint32_t)a.runs;
-    uint8_t* base = layers.pages[layer];
-    const uint4* src = reinterpret_cast<const uint4*>(base) + from * page_vecs;
-    uint4* dst = reinterpret_cast<uint4*>(base) + to * page_vecs;
-    const uint32_t first = (uint32_t)part * kPart + threadIdx.x;
-    uint4 x[kVecs];
-    int64_t at[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const uint32_t v = first + i * 256;
-      if (v < vecs) {
-        const uint32_t head = v / run;
-        at[i] = head * head_vecs + (v - head * run);
-        x[i] = __ldcs(src + at[i]);
+  const uint32_t group_vecs = a.group_bytes / 16;
+  const uint32_t head_vecs = a.groups * group_vecs, page_vecs = head_vecs * a.runs;
+  const uint64_t per_copy = (uint64_t)a.num_layers * parts;
+  const uint64_t items = (uint64_t)a.num_copies * per_copy;
+  for (uint64_t base = blockIdx.x; base < items; base += (uint64_t)kList * gridDim.x) {
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    const uint64_t item = base + (uint64_t)threadIdx.x * gridDim.x;
+    if (item < items) {
+      const uint64_t i = item / per_copy;
+      const int32_t* copy = a.copies + 3 * i;
+      const int from = __ldg(copy), to = __ldg(copy + 1), tokens = __ldg(copy + 2);
+      if (from != -1 && tokens != 0 && from != to) {
+        if (from >= 0 && from < a.num_pages && to >= 0 && to < a.num_pages && tokens > 0 &&
+            tokens <= a.groups * 16)
+          list[atomicAdd(&count, 1)] = make_int4(from, to, tokens, (int)(item - i * per_copy));
+        else
+          report_error(a.err, kErrDeviceCheck);
       }
     }
+    __syncthreads();
+    const int n = count;
+    for (int e = 0; e < n; ++e) {
+      const int4 it = list[e];
+      const int layer = it.w / parts, part = it.w - layer * parts;
+      // the groups in use of each head, one run where that is all of them
+      const uint32_t groups = (it.z + 15) / 16;
+      const bool all = groups == (uint32_t)a.groups;
+      const uint32_t run = all ? page_vecs : groups * group_vecs;
+      const uint32_t vecs = all ? run : run * a.runs;
+      uint4* const pages = reinterpret_cast<uint4*>(layers.pages[layer]);
+      const uint4* const src = pages + (int64_t)it.x * page_vecs;
+      uint4* const dst = pages + (int64_t)it.y * page_vecs;
+      const uint32_t first = (uint32_t)part * part_vecs + threadIdx.x;
+      const uint32_t end = min(vecs, (uint32_t)(part + 1) * part_vecs);
+      uint4 x[kVecs];
+      uint32_t at[kVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (first + i * 256 < vecs) __stcs(dst + at[i], x[i]);
+      for (int i = 0; i < kVecs; ++i) {
+        const uint32_t v = first + i * 256, head = v / run;
+        at[i] = head * head_vecs + (v - head * run);
+        if (v < end) x[i] = __ldcs(src + at[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        if (first + i * 256 < end) __stcs(dst + at[i], x[i]);
+    }
+    __syncthreads();  // the list is read
   }
 }
 
@@ -404,10 +558,30 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Rows in x; parts of a row in y, in z what y has no room for.
-dim3 grid_of(int64_t rows, unsigned parts, int most) {
-  const unsigned y = std::min(parts, 32768u);
-  return dim3((unsigned)std::min<int64_t>(rows, most), y, (parts + y - 1) / y);
+// One cluster, whose CTAs wait for one another at the barriers between the steps.
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Up to so many entries of tables, and pages, the cluster takes.
+constexpr int64_t kClusterEntries = 1 << 18;
+constexpr int kClusterPages = 1 << 20;
+
+// CTAs of a kernel over a table's entries.
+unsigned entry_ctas(int64_t entries, int most) {
+  const int64_t per = 256 * kBatch;
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((entries + per - 1) / per, most));
 }
 
 int words_of(int pages) { return (int)(((int64_t)pages + 31) / 32); }
@@ -450,40 +624,45 @@ size_t cache_compact_workspace_bytes(const CompactArgs& a) {
 cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
   ForkScratch s;
   fork_layout(a, static_cast<uint8_t*>(a.workspace), &s);
-  const int words = words_of(a.num_pages), most = 8 * sm_count();
-  const int64_t work = std::max<int64_t>(std::max(words, a.num_seqs), 1);
-  fork_rows_kernel<<<(unsigned)std::min<int64_t>((work + 255) / 256, most), 256, 0, st>>>(a, s,
-                                                                                          words);
+  const int words = words_of(a.num_pages);
+  const int64_t rows = (int64_t)a.old_seqs + a.num_seqs;
+  if (rows * std::max(a.max_blocks, 1) <= kClusterEntries && a.num_pages <= kClusterPages)
+    return launch_cluster(fork_kernel, st, a, s, words);
+  const int most = 8 * sm_count();
+  fork_rows_kernel<<<(unsigned)std::min<int64_t>(std::max<int64_t>(words, rows) / 256 + 1, most),
+                     256, 0, st>>>(
+      a, s, words);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.old_seqs + a.num_seqs;
-  const unsigned parts = (unsigned)(((int64_t)a.max_blocks + kColumns - 1) / kColumns);
-  if (rows > 0 && parts > 0) {
-    e = launch_after(fork_mark_kernel, grid_of(rows, parts, most), 256, st, a, s);
-    if (e != cudaSuccess) return e;
-  }
+  e = launch_after(fork_mark_kernel, dim3(entry_ctas(rows * a.max_blocks, most)), 256, st, a, s);
+  if (e != cudaSuccess) return e;
   return launch_after(fork_settle_kernel, dim3(1), kThreads, st, a, s, words);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
   CompactScratch s;
   compact_layout(a, static_cast<uint8_t*>(a.workspace), &s);
-  const int words = words_of(a.num_pages), most = 8 * sm_count();
-  compact_clear_kernel<<<std::min((words + 255) / 256 + 1, most), 256, 0, st>>>(s, words);
+  const int words = words_of(a.num_pages);
+  if ((int64_t)a.num_seqs * std::max(a.max_blocks, 1) <= kClusterEntries &&
+      a.num_pages <= kClusterPages)
+    return launch_cluster(compact_kernel, st, a, s, words);
+  const int most = 8 * sm_count();
+  compact_clear_kernel<<<std::min(std::max(words, a.num_seqs) / 256 + 1, most), 256, 0, st>>>(
+      a, s, words);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const unsigned parts = (unsigned)(((int64_t)a.max_blocks + kColumns - 1) / kColumns);
-  const dim3 grid = grid_of(std::max(a.num_seqs, 1), std::max(parts, 1u), most);
-  e = launch_after(compact_mark_kernel, grid, 256, st, a, s);
+  const dim3 ctas(entry_ctas((int64_t)a.num_seqs * a.max_blocks, most));
+  e = launch_after(compact_mark_kernel, ctas, 256, st, a, s);
   if (e != cudaSuccess) return e;
   e = launch_after(compact_plan_kernel, dim3(1), kThreads, st, a, s, words);
   if (e != cudaSuccess) return e;
-  return launch_after(compact_rows_kernel, grid, 256, st, a, s);
+  return launch_after(compact_rows_kernel, ctas, 256, st, a, s);
 }
 
 cudaError_t launch_cache_copy(const CopyArgs& a, uint8_t* const* pages, cudaStream_t st) {
-  const int64_t vecs = (int64_t)a.groups * a.group_bytes / 16 * a.runs;
-  const int parts = (int)((vecs + kPart - 1) / kPart);
+  // a page has fewer than 2^27 words; its parts are alike, but for the last
+  const int vecs = (int)((int64_t)a.groups * a.group_bytes / 16 * a.runs);
+  const int parts = (vecs + kPart - 1) / kPart, part_vecs = (vecs + parts - 1) / parts;
   for (int first = 0; first < a.num_layers; first += kCopyLayers) {
     CopyArgs b = a;
     b.num_layers = std::min(a.num_layers - first, kCopyLayers);
@@ -491,8 +670,8 @@ cudaError_t launch_cache_copy(const CopyArgs& a, uint8_t* const* pages, cudaStre
     for (int i = 0; i < b.num_layers; ++i) layers.pages[i] = pages[first + i];
     const int64_t items = (int64_t)b.num_copies * b.num_layers * parts;
     const cudaError_t e =
-        launch_after(copy_kernel, dim3((unsigned)std::min<int64_t>(items, 8ll * sm_count())), 256,
-                     st, b, layers, parts);
+        launch_after(copy_kernel, dim3((unsigned)std::min<int64_t>(items, 4ll * sm_count())), 256,
+                     st, b, layers, parts, part_vecs);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
