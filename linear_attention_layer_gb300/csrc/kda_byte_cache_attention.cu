@@ -24,7 +24,7 @@ auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
   }
   if (a.head_dim == 128)
     return few ? f(Split<8, float, 128, 1, 8, 3, 1>{}) : f(Split<8, float, 128, 2, 8, 2, 1>{});
-  return few ? f(Split<8, float, 64, 1, 8, 3, 2>{}) : f(Split<8, float, 64, 2, 8, 4, 1>{});
+  return few ? f(Split<8, float, 64, 1, 4, 4, 3>{}) : f(Split<8, float, 64, 2, 8, 4, 1>{});
 }
 
 }  // namespace

@@ -180,7 +180,7 @@ struct Smem {
   uint64_t k_full[kTileStages], k_empty[kTileStages], v_full[kTileStages], v_empty[kTileStages];
   uint64_t q_full[2], s_full[2], s_free[2], p_full[2], o_full[2], issued;
   uint32_t valid[kValidRing];  // groups of a tile that can be read
-  uint32_t powers[kValidRing]; // 8 bits: exponent bytes of a tile's K and, times 256, V
+  uint32_t powers[kValidRing]; // 8 bits: exponent bytes that a tile's K and, times 256, V are under
   uint32_t tmem;
   uint32_t copied;  // tiles whose pages were asked for
   int failed;
@@ -200,8 +200,11 @@ struct Ring {
 };
 
 // Dequantisation of a tile of 8-bit codes, by warp dw of four its group of 16 keys: halves in
-// units of the largest power of two among the tile's groups, as rows of 128 swizzled bytes.  A
-// code times 2^-d is exact down to 2^-24 of the unit.  Lanes take the 16-byte pieces so that
+// units of the largest power of two that the piece has met, as rows of 128 swizzled bytes: scores
+// and O then change their units only where a larger one turns up, in the branch that moves the
+// softmax's reference, and a tile costs the softmax what a 4-bit one does (powers of its own for
+// each tile, taken into the weights there: 797 us for the chunk above).  A code times 2^-d is
+// exact down to 2^-24 of the unit.  Lanes take the 16-byte pieces so that
 // eight of them read 128 bytes in a row and write to all banks.
 template <int D, bool V>
 struct Dequant8 {
@@ -244,7 +247,7 @@ struct Dequant8 {
                               (((chunk & 7) ^ (row & 7)) << 4)) =
         make_uint4(h[0], h[1], h[2], h[3]);
   }
-  // f: the group's power of two beside the tile's, as two halves; left: keys that there are.
+  // f: the group's power of two beside the unit, as two halves; left: keys that there are.
   __device__ __forceinline__ void store(uint8_t* tile, int dw, uint32_t f, int left) const {
     const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll
@@ -420,24 +423,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.q_full[blk]);
       }
-      float neg = BITS == 4 ? 0.f : kUnset, thr = -INFINITY;
-      int v_ref = 0;            // 8 bits: O is in units of 2^(v_ref - 127)
-      bool gave_up = false;     // 8 bits
+      float neg = 0.f, thr = -INFINITY;
+      // 8 bits: exponent bytes under which the tiles' K and V are (f and O are in their units), and
+      // f without K's
+      uint32_t powers = 0;
+      const float f0 = f;
       uint64_t l2[2] = {0, 0};  // the row's sum, in four parts
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         // a wait that gives up lowers the limit, so that the vote below is taken
-        if (!wait(&sm.s_full[blk], s_full.parity)) thr = -INFINITY, gave_up = true;
+        if (!wait(&sm.s_full[blk], s_full.parity)) thr = -INFINITY;
         s_full.step();
         tc::tc_fence_after();
         float s[kKeys];
         const int key0 = j * kKeys;
-        uint32_t valid, powers = 0;
+        uint32_t valid, under = 0;
         {
           float h0[32], h1[32];
           tc::tmem_ld32(ts, h0);
           tc::tmem_ld32(ts + 32, h1);
           valid = *(volatile uint32_t*)&sm.valid[tile_no % kValidRing];
-          if constexpr (BITS == 8) powers = *(volatile uint32_t*)&sm.powers[tile_no % kValidRing];
+          if constexpr (BITS == 8) under = *(volatile uint32_t*)&sm.powers[tile_no % kValidRing];
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[i] = h0[i], s[32 + i] = h1[i];
@@ -458,35 +463,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = fmaxf(tc::max3(t4[0], s[kKeys - 4], s[kKeys - 3]),
                                 tc::max3(tc::max3(t4[1], t4[2], t4[3]), s[kKeys - 2], s[kKeys - 1]));
         bool waited = false;
-        // 8 bits: the raw scores' factor in this tile (kept positive) and its V's exponent byte
-        const float ft =
-            BITS == 4 ? f
-                      : fminf(fmaxf(f * exponent_factor(powers & 255), 1.2e-38f), 3.e38f);
-        const int v_top = powers >> 8;
-        const bool move = BITS == 4 ? top > thr
-                                    : fmaf(top, ft, neg) > kLift + kSlack || v_top > v_ref || gave_up;
-        if (__any_sync(0xffffffffu, move)) {
+        if (__any_sync(0xffffffffu, top > thr || (BITS == 8 && under != powers))) {
           ok = all_ok(!*failed);
           if (!ok) break;
-          float keep = 1.f;
+          float keep = 1.f, down = 1.f;
+          if (BITS == 8 && under != powers) {  // larger ones from this tile on
+            f = fminf(fmaxf(f0 * exponent_factor(under & 255), 1.2e-38f), 3.e38f);
+            down = powers ? power_below((int)(powers >> 8) - (int)(under >> 8)) : 0.f;
+            powers = under;
+            if (thr != -INFINITY) thr = score_limit(-neg, f);
+          }
           if (top > -INFINITY) {
-            const bool unset = BITS == 4 ? thr == -INFINITY : neg == kUnset;
-            const float before = unset ? -INFINITY : -neg;
-            const float m = fmaxf(before, top * ft - kLift);
+            const float before = thr == -INFINITY ? -INFINITY : -neg;
+            const float m = fmaxf(before, top * f - kLift);
             keep = ex2_approx(before - m);
             neg = -m;
-            if constexpr (BITS == 4) thr = score_limit(m, f);
+            thr = score_limit(m, f);
           }
           const uint64_t keep2 = tc::pack2(keep, keep);
           l2[0] = tc::fma2(l2[0], keep2, 0);
           l2[1] = tc::fma2(l2[1], keep2, 0);
-          if (BITS == 8 && v_top > v_ref) {
-            keep *= v_ref ? power_below(v_ref - v_top) : 0.f;
-            v_ref = v_top;
-          }
+          keep *= down;
           if (j > p.begin) {
             // the product of the tile before has to be in O
-            if (!wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY, gave_up = true;
+            if (!wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY;
             tc::tc_fence_after();
             waited = true;
 #pragma unroll 1
@@ -501,12 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // 8 bits: weights times 2^(v_top - v_ref), which the sums take back.  2^-60 at least, or a
-        // weight could get lost in fp32: far less than a half holds of the largest either way.
-        const int shift = BITS == 4 ? 0 : max(v_top - v_ref, -60);
-        uint64_t lt[2] = {0, 0};
-        uint64_t(&sum)[2] = BITS == 4 ? l2 : lt;
-        const uint64_t f2 = tc::pack2(ft, ft), neg2 = tc::pack2(neg + (float)shift, neg + (float)shift);
+        const uint64_t f2 = tc::pack2(f, f), neg2 = tc::pack2(neg, neg);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t w[16];
@@ -517,20 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::unpack2(tc::fma2(tc::pack2(s[at], s[at + 1]), f2, neg2), p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
-            sum[i & 1] = tc::add2(sum[i & 1], tc::pack2(p0, p1));
+            l2[i & 1] = tc::add2(l2[i & 1], tc::pack2(p0, p1));
             w[i] = tc::pack_f16(p0, p1);
           }
           if (half == 0 && j > p.begin) {  // the product before has read its weights
-            if (!waited && !wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY, gave_up = true;
+            if (!waited && !wait(&sm.o_full[blk], o_full.parity)) thr = -INFINITY;
             o_full.step();
             tc::tc_fence_after();
           }
           tc::tmem_st16u(tp + half * 16, w);
-        }
-        if constexpr (BITS == 8) {
-          const float up = __int_as_float((127 - shift) << 23);
-          l2[0] = tc::fma2(lt[0], tc::pack2(up, up), l2[0]);
-          l2[1] = tc::fma2(lt[1], tc::pack2(up, up), l2[1]);
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
@@ -546,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::unpack2(tc::add2(l2[0], l2[1]), la, lb);
       l = la + lb;
       const bool whole = p.begin == 0 && p.end == p.tiles;
-      const float post = BITS == 4 ? exponent_scale(c.v_exp, p.h, 1) : exponent_factor(v_ref);
+      const float post =
+          BITS == 4 ? exponent_scale(c.v_exp, p.h, 1) : exponent_factor((int)(powers >> 8));
       const float inv = !whole ? (BITS == 4 ? 1.f : post) : l == 0.f ? 0.f : post / l;
-      const bool unset = BITS == 4 ? thr == -INFINITY : neg == kUnset;
-      const float m = unset ? -INFINITY : -neg;
+      const float m = thr == -INFINITY ? -INFINITY : -neg;
       const int64_t out_at = tok * a.num_heads + head;
       const int64_t part_at =
           (int64_t)(2 * blockIdx.x + (p.begin == 0 ? 1 : 0)) * kRows + blk * kBlock + row;
@@ -599,13 +589,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       Piece p;
       p.set(c, a, range, plan, entries, x, x1);
       x += p.end - p.begin;
+      int k_top = 0, v_top = 0;  // 8 bits: the largest exponent bytes of the piece so far
       for (int j = p.begin; j < p.end; ++j, ++tile_no) {
         ok = wait(&sm.raw_full[raw.i], raw.parity);
         if constexpr (BITS == 8) {
           const uint8_t* const tile = sm.raw[raw.i];
           const uint32_t valid = sm.valid[tile_no % kValidRing];
           const int left = valid >> dw & 1 ? p.q.kv - j * kKeys - dw * kGroup : 0;
-          int k_top = 0, v_top = 0;  // the largest exponent bytes of the tile's groups
 #pragma unroll
           for (int q = 0; q < kGroups; ++q) {
             const uint32_t x =
