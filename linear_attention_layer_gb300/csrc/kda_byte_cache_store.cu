@@ -9,7 +9,12 @@
 //
 // One warp takes the new tokens of one block, a run of neighbours in the batch, and keeps
 // them in registers: 16 bytes of bf16 a lane and token, the largest magnitude by one redux.
-// Nothing is shared between warps.
+// Nothing is shared between warps.  What bounds it is HBM as long as enough warps have their
+// loads under way: 28 a SM of 72 registers (140 registers left 8: 672 us for the prompts below).
+//
+// Measured (GB300; bf16, heads of 128, 8 of them): prompts of 270336 tokens, 1.66 GB, appended in
+// 297 us (0.82 of the measured HBM rate), read back in 256 us (0.96); 8000 tokens 11 us; a decode
+// step of 256 tokens 6.5 us.
 #include <algorithm>
 
 #include "kda_byte_cache.cuh"
@@ -21,7 +26,11 @@ namespace {
 
 using namespace cache;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Of a CTA that reads back (270336 tokens x 8 x 128 of bf16: 256 us, with 256 threads 280; 100000 of
+// fp32 210 and 202).
+template <typename T>
+constexpr int kReadThreads = sizeof(T) == 2 ? 128 : 256;
 
 struct Source {
   const void* p;
@@ -110,25 +119,27 @@ struct Lanes {
 };
 
 // A run of n tokens of the batch, which fill places of one block; lane k < n has the place of
-// the k-th of them.  p: the lane's channels of its first token, whose values are in `first` if
-// HAVE_FIRST.  All lanes of the warp.
-template <typename T, int D, bool VEC, bool V, bool HAVE_FIRST>
+// the k-th of them.  p: the lane's channels of its first token, whose values (those of the next as
+// well, where a step takes two or four) are in `first` if `have`.  All lanes of the warp.
+template <typename T, int D, bool VEC, bool V>
 __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token_stride, int n,
                                            int place, const uint32_t (&first)[2 * sizeof(T)],
-                                           bool& not_finite) {
+                                           bool have, bool& not_finite) {
   using W = Lanes<D>;
   const W at;
   const int lane = threadIdx.x & 31;
   uint32_t w[W::STEPS][2 * sizeof(T)];
 #pragma unroll
   for (int s = 0; s < W::STEPS; ++s) {
-    if (s == 0 && HAVE_FIRST) {
 #pragma unroll
-      for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[0][i] = first[i];
-    } else {
+    for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[s][i] = 0;
+    if (s * W::AT_ONCE + at.t < n) {
+      if (s == 0 && have) {
 #pragma unroll
-      for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[s][i] = 0;
-      if (s * W::AT_ONCE + at.t < n) fetch8<T, VEC>(p, w[s]);
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[0][i] = first[i];
+      } else {
+        fetch8<T, VEC>(p, w[s]);
+      }
     }
     p += (int64_t)W::AT_ONCE * token_stride;
   }
@@ -141,19 +152,16 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
                            : max(kLeastExponent, min((int)*exp_at - kExponentBias, kMostExponent));
   uint32_t top = 0;
 #pragma unroll
-  for (int s = 0; s < W::STEPS; ++s)
-    if (!HAVE_FIRST || s > 0 || at.t < n) top = max(top, top8<T>(w[s]));
+  for (int s = 0; s < W::STEPS; ++s) top = max(top, top8<T>(w[s]));
   top = __reduce_max_sync(0xffffffffu, top);
   const bool odd = top >= 0x7f800000u;  // infinities do not count, NaN becomes zero
   if (odd) {
     not_finite = true;
     top = 0;
 #pragma unroll
-    for (int s = 0; s < W::STEPS; ++s) {
-      if (HAVE_FIRST && s == 0 && at.t >= n) continue;
+    for (int s = 0; s < W::STEPS; ++s)
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, finite8<T>(w[s], i));
-    }
     top = __reduce_max_sync(0xffffffffu, top);
   }
   const int e = max(exponent_of(top), before);
@@ -198,49 +206,59 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
   if (lane == 0) *exp_at = (uint8_t)(e + kExponentBias);
 }
 
-// A warp takes the runs that start among WINDOW tokens (16 or 1), of one head, of K or V.
-template <typename T, int D, bool VEC, int WINDOW, bool V>
-__device__ __forceinline__ void append_window(const View& c, int tokens, const Source& src,
+// The runs that start among 16 tokens of the batch, a window, are dealt out with the heads to
+// `share` warps: a prompt's window has one or two runs, a decode step's sixteen.
+template <typename T, int D, bool VEC, bool V>
+__device__ __forceinline__ void append_window(const View& c, int tokens, int share,
+                                              const Source& src,
                                               const int64_t* __restrict__ slots, int* err) {
   const int lane = threadIdx.x & 31;
-  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t window = unit / c.kv_heads;
-  const int head = (int)(unit - window * c.kv_heads);
-  const int64_t start = window * WINDOW;
+  const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (host: 32 bits)
+  const uint32_t window = unit / (uint32_t)share;
+  const int mine = (int)(unit - window * (uint32_t)share);
+  const int64_t start = (int64_t)window * kGroup;
   if (start >= tokens) return;
-  const Lanes<D> mine;
-  const T* p = static_cast<const T*>(src.p) + (start + mine.t) * src.token_stride +
-               (int64_t)head * src.head_stride + mine.c;
+  const Lanes<D> at;
+  const T* base = static_cast<const T*>(src.p);
   // lane l: the slot of token start - 1 + l, as far as a run of the window may reach
   const int64_t token = start - 1 + lane;
   int64_t slot = -1;
-  if (token >= 0 && token < tokens && lane < WINDOW + kGroup) slot = __ldg(slots + token);
-  // Its tokens' values are on their way to L2 while the slots are: which of them a run takes,
-  // these or some of the next window's, hangs on the slots.
-  if constexpr (WINDOW > 1) {
+  if (token >= 0 && token < tokens) slot = __ldg(slots + token);
+  // Values are asked for before the slots say which they are.  Many warps to a window: the token
+  // that is this warp's if each is a run of its own; else all of the window's, into L2.
+  uint32_t first[2 * sizeof(T)] = {};
+  const bool alone = share > c.kv_heads;
+  const int guess = (uint32_t)mine / (uint32_t)c.kv_heads;
+  if (alone) {
+    if (start + guess + at.t < tokens)
+      fetch8<T, VEC>(base + (start + guess + at.t) * src.token_stride +
+                         (int64_t)(mine - guess * c.kv_heads) * src.head_stride + at.c,
+                     first);
+  } else {
     constexpr int kLines = D * (int)sizeof(T) / 128;
 #pragma unroll
-    for (int i = lane; i < WINDOW * kLines; i += 32)
+    for (int i = lane; i < kGroup * kLines; i += 32)
       if (start + i / kLines < tokens)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(
-            static_cast<const T*>(src.p) + (start + i / kLines) * src.token_stride +
-            (int64_t)head * src.head_stride + i % kLines * (128 / (int)sizeof(T))));
+            base + (start + i / kLines) * src.token_stride + (int64_t)mine * src.head_stride +
+            i % kLines * (128 / (int)sizeof(T))));
   }
-  // a single token's values are under way before its slot is known
-  uint32_t first[2 * sizeof(T)] = {};
-  if (WINDOW == 1 && start + mine.t < tokens) fetch8<T, VEC>(p, first);
   const bool there = slot >= 0 && slot < (int64_t)c.num_pages * c.page_size;
-  const bool counts = lane >= 1 && lane <= WINDOW;
-  if (!there && slot != -1 && counts && head == 0 && !V) report_error(err, kErrDeviceCheck);
+  const bool counts = lane >= 1 && lane <= kGroup;
+  if (!there && slot != -1 && counts && mine == 0 && !V) report_error(err, kErrDeviceCheck);
   const int block = there ? (int)(slot / kGroup) : -1;  // fewer than 2^27
   const int prev = __shfl_up_sync(0xffffffffu, block, 1);
   const bool goes_on = there && lane > 0 && prev == block;
   const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
-  uint32_t starts = __ballot_sync(0xffffffffu, counts && there && !goes_on);
+  const bool starts_here = counts && there && !goes_on;
+  const uint32_t starts = __ballot_sync(0xffffffffu, starts_here);
+  const int rank = __popc(starts & ((1u << lane) - 1));  // runs before the lane's
+  const int tasks = __popc(starts) * c.kv_heads;
   bool not_finite = false;
   const int groups = c.page_size / kGroup;
-  for (; starts; starts &= starts - 1) {
-    const int l = __ffs(starts) - 1;
+  for (int task = mine; task < tasks; task += share) {
+    const int run = task / c.kv_heads, head = task - run * c.kv_heads;
+    const int l = __ffs(__ballot_sync(0xffffffffu, starts_here && rank == run)) - 1;
     // tokens l, l + 1, ... as long as they go on
     const uint32_t after = ~(on >> (l + 1));
     const int n = min(after ? __ffs(after) : 32, kGroup);
@@ -250,20 +268,23 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, const S
     uint8_t* group =
         c.pages + (((int64_t)page * c.kv_heads + head) * groups + (b - page * groups)) *
                       Layout8<D>::kGroupBytes;
-    append_run<T, D, VEC, V, WINDOW == 1>(group, p + (int64_t)(l - 1) * src.token_stride,
-                                          src.token_stride, n, place, first, not_finite);
+    append_run<T, D, VEC, V>(group,
+                             base + (start + l - 1 + at.t) * src.token_stride +
+                                 (int64_t)head * src.head_stride + at.c,
+                             src.token_stride, n, place, first,
+                             alone && task == mine && l - 1 == guess, not_finite);
   }
   if (not_finite && lane == 0) report_error(err, kErrDeviceCheck);
 }
 
-template <typename T, int D, bool VEC, int WINDOW>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && WINDOW > 1 ? 3 : 2)
-    append_kernel(View c, int tokens, Source k, Source v, const int64_t* __restrict__ slots,
-                  int* err) {
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 4)
+    append_kernel(View c, int tokens, int share, Source k, Source v,
+                  const int64_t* __restrict__ slots, int* err) {
   if (blockIdx.y)
-    append_window<T, D, VEC, WINDOW, true>(c, tokens, v, slots, err);
+    append_window<T, D, VEC, true>(c, tokens, share, v, slots, err);
   else
-    append_window<T, D, VEC, WINDOW, false>(c, tokens, k, slots, err);
+    append_window<T, D, VEC, false>(c, tokens, share, k, slots, err);
 }
 
 template <typename T>
@@ -286,7 +307,7 @@ __device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
 
 // A thread takes 16 channels of a token and every so many heads, of K or V.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kReadThreads<T>)
     read_kernel(View c, int tokens, const int64_t* __restrict__ slots, T* __restrict__ k,
                 T* __restrict__ v, int* err) {
   constexpr int PIECES = D / 16;
@@ -337,8 +358,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// From so many rows (tokens x heads) on a warp takes the runs of 16 tokens, not of one.
-constexpr int64_t kManyRows = 1 << 17;
+// Warps of a window: one a head, what a prompt has work for, or more while that leaves the GPU
+// short of kWarps -- up to one a head and token, what a decode step has work for.
+constexpr int64_t kWarps = 8192;
 
 template <typename T, int D>
 cudaError_t append(const CacheArgs& a, cudaStream_t st) {
@@ -347,14 +369,13 @@ cudaError_t append(const CacheArgs& a, cudaStream_t st) {
   const int el = 16 / sizeof(T);
   bool vec = ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0;
   for (int64_t s : a.strides) vec = vec && s % el == 0;
-  const int window = (int64_t)a.tokens * a.view.kv_heads >= kManyRows ? kGroup : 1;
-  const int64_t units = ((int64_t)a.tokens + window - 1) / window * a.view.kv_heads;
-  const int64_t ctas = (units * 32 + kThreads - 1) / kThreads;
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  auto* kernel = window == 1 ? (vec ? append_kernel<T, D, true, 1> : append_kernel<T, D, false, 1>)
-                 : vec       ? append_kernel<T, D, true, kGroup>
-                             : append_kernel<T, D, false, kGroup>;
-  kernel<<<dim3((unsigned)ctas, 2), kThreads, 0, st>>>(a.view, a.tokens, k, v, a.slots, a.err);
+  const int64_t windows = ((int64_t)a.tokens + kGroup - 1) / kGroup, heads = a.view.kv_heads;
+  const int64_t share = std::max(heads, std::min(kGroup * heads, kWarps / 2 / windows));
+  const int64_t ctas = (windows * share * 32 + kThreads - 1) / kThreads;
+  if (ctas > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidConfiguration;
+  auto* kernel = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
+  kernel<<<dim3((unsigned)ctas, 2), kThreads, 0, st>>>(a.view, a.tokens, (int)share, k, v, a.slots,
+                                                       a.err);
   return cudaGetLastError();
 }
 
@@ -362,7 +383,7 @@ template <typename T, int D>
 cudaError_t read(const CacheArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)((a.tokens + 7ll) / 8), 2);
   const int per_head = 8 * (D / 16);
-  const int threads = per_head * std::min(a.view.kv_heads, kThreads / per_head);
+  const int threads = per_head * std::min(a.view.kv_heads, kReadThreads<T> / per_head);
   read_kernel<T, D><<<grid, threads, 0, st>>>(a.view, a.tokens, a.slots,
                                               static_cast<T*>(a.k_out), static_cast<T*>(a.v_out),
                                               a.err);
