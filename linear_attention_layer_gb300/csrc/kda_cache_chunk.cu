@@ -23,7 +23,7 @@
 // blocks' q in tensor memory, 822 us; apart, 779).
 //
 // Warps.  0-3 and 4-7: softmax of the two blocks, a thread a row; 8-11: dequantisation;
-// 12: issues the matrix products; 13: copies pages into a ring.  Measured slower: two
+// 12 (and 14): issues the matrix products; 13: copies pages into a ring.  Measured slower: two
 // threads a row (16 softmax warps of 80 registers, 862 us against 822), eight warps for the
 // dequantisation with registers moved to the softmax (876 against 746), and, for up to 128
 // rows, the two blocks on alternate tiles of the same rows (no faster than one block).
@@ -53,7 +53,21 @@ constexpr int kKeys = 64;               // keys of a tile
 constexpr int kGroups = kKeys / kGroup;
 constexpr int kRawStages = 4, kTileStages = 3;
 constexpr int kValidRing = 16;          // more tiles than can be under way
-constexpr int kThreads = 14 * 32;
+// With 8 bits a block of rows has an issuing warp of its own, and the softmax's warps take registers
+// from the others (8 bits, the chunk above: 787 us with one issuer and 128 registers for all, 764;
+// 4 bits 744 and 756).  160 x 8 + 112 x 4 + 80 x 4 = the launch's 128 x 16.
+template <int BITS>
+constexpr int kIssuers = BITS == 8 ? 2 : 1;
+template <int BITS>
+constexpr int kThreads = 32 * (BITS == 8 ? 16 : 14);
+template <int BITS, int REGS>
+__device__ __forceinline__ void take_registers() {
+  if constexpr (BITS == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int BITS, int REGS>
+__device__ __forceinline__ void leave_registers() {
+  if constexpr (BITS == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 constexpr uint32_t kCols = 512;
 
 struct Plan {
@@ -277,7 +291,7 @@ struct Dequant8 {
 };
 
 template <int BITS, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<BITS>, 1)
     chunk_kernel(View c, AttentionArgs a, RowRange range, Plan plan, int q_vec) {
   using L = FormLayout<BITS, D>;
   using S = Smem<BITS, D>;
@@ -300,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kTileStages; ++i) {
       tc::mbar_init(&sm.k_full[i], 4);
       tc::mbar_init(&sm.v_full[i], 4);
-      tc::mbar_init(&sm.k_empty[i], 1);
-      tc::mbar_init(&sm.v_empty[i], 1);
+      tc::mbar_init(&sm.k_empty[i], kIssuers<BITS>);
+      tc::mbar_init(&sm.v_empty[i], kIssuers<BITS>);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.q_full[i], 4);
@@ -310,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sm.p_full[i], 4);
       tc::mbar_init(&sm.o_full[i], 1);
     }
-    tc::mbar_init(&sm.issued, 1);
+    tc::mbar_init(&sm.issued, kIssuers<BITS>);
     sm.failed = 0;
     tc::mbar_fence_init();
   }
@@ -338,8 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto all_ok = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
 
+  // the warps that issue matrix products, and the blocks of rows that this one is for
+  const bool issues = warp == 12 || (kIssuers<BITS> == 2 && warp == 14);
+  const int first_blk = kIssuers<BITS> == 2 ? (warp - 12) / 2 : 0;
   if (warp < 8) {
     // ------------------------------------------------------------ softmax ----
+    take_registers<BITS, 160>();
     const int blk = warp >> 2;
     const int row = tid & (kBlock - 1);
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -579,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 12) {
     // ----------------------------------------------------- dequantisation ----
+    leave_registers<BITS, 112>();
     const int dw = warp - 8;
     Ring<kRawStages> raw;
     Ring<kTileStages> st;
@@ -692,128 +711,134 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (st.i == 0) empty_parity ^= 1;
       }
     }
-  } else if (warp == 12) {
-    // ------------------------------------------------------ matrix products ----
-    if (tc::elect_one()) {  // (2048-token chunk over 32768 keys: 869 us; by lane == 0: 1392)
-      const uint64_t kd = tc::make_sdesc(tc::smem_u32(sm.k), 0, 1024, tc::kSwizzle128);
-      const uint64_t vd = tc::make_sdesc(tc::smem_u32(sm.v), kKeys * 128, 1024, tc::kSwizzle128);
-      const uint64_t qd = tc::make_sdesc(tc::smem_u32(sm.q), 0, 1024, tc::kSwizzle128);
-      const uint32_t id_s = tc::make_idesc_f16(128, kKeys, false, false);
-      const uint32_t id_o = tc::make_idesc_f16(128, D, false, true);
-      Ring<kTileStages> ks, vs;
-      Ring<1> q_full[2], p_full[2];
-      uint32_t free_parity[2] = {1, 1};
+  } else {
+    leave_registers<BITS, 80>();
+    if (issues) {
+      // ------------------------------------------------------ matrix products ----
+      constexpr int kMine = 2 / kIssuers<BITS>;  // blocks
+      if (tc::elect_one()) {  // (2048-token chunk over 32768 keys: 869 us; by lane == 0: 1392)
+        const uint64_t kd = tc::make_sdesc(tc::smem_u32(sm.k), 0, 1024, tc::kSwizzle128);
+        const uint64_t vd = tc::make_sdesc(tc::smem_u32(sm.v), kKeys * 128, 1024, tc::kSwizzle128);
+        const uint64_t qd = tc::make_sdesc(tc::smem_u32(sm.q), 0, 1024, tc::kSwizzle128);
+        const uint32_t id_s = tc::make_idesc_f16(128, kKeys, false, false);
+        const uint32_t id_o = tc::make_idesc_f16(128, D, false, true);
+        Ring<kTileStages> ks, vs;
+        Ring<1> q_full[kMine], p_full[kMine];
+        uint32_t free_parity[2] = {1, 1};
+        bool ok = true;
+        for (unsigned long long x = x0; x < x1 && ok;) {
+          Piece p;
+          p.set(c, a, range, plan, entries, x, x1);
+          x += p.end - p.begin;
+          const int blocks = min((p.rows() > kBlock ? 2 : 1) - first_blk, kMine);  // of this warp
+          const int n = p.end - p.begin;
+          // scores of the next tile, as soon as the softmax has the tile before in registers
+          auto scores = [&]() {
+            ok = wait(&sm.k_full[ks.i], ks.parity);
+            const uint64_t b0 = kd + (uint64_t)(ks.i * S::kTile >> 4);
+            for (int i = 0; i < blocks && ok; ++i) {
+              const int blk = first_blk + i;
+              ok = wait(&sm.s_free[blk], free_parity[i]);
+              if (!ok) break;
+              free_parity[i] ^= 1;
+              tc::tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t b1 =
+                    b0 + (uint64_t)(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4);
+                if (QS && blk == 1)
+                  tc::mma_bf16_ss(tmem + TS + kKeys,
+                                  qd + (uint64_t)(((kk >> 2) * (kBlock * 128) + (kk & 3) * 32) >> 4),
+                                  b1, id_s, kk > 0);
+                else
+                  tc::mma_ts(tmem + TS + blk * kKeys, tmem + TQ + blk * (D / 2) + kk * 8, b1, id_s,
+                             kk > 0);
+              }
+              tc::mma_commit(&sm.s_full[blk]);
+            }
+            tc::mma_commit(&sm.k_empty[ks.i]);
+            ks.step();
+          };
+          for (int i = 0; i < blocks && ok; ++i) {
+            ok = wait(&sm.q_full[first_blk + i], q_full[i].parity);
+            q_full[i].step();
+          }
+          if (ok) scores();
+          for (int j = 0; j < n && ok; ++j) {
+            if (j + 1 < n) scores();
+            if (ok) ok = wait(&sm.v_full[vs.i], vs.parity);
+            const uint64_t b0 = vd + (uint64_t)(vs.i * S::kTile >> 4);
+            for (int i = 0; i < blocks && ok; ++i) {
+              const int blk = first_blk + i;
+              ok = wait(&sm.p_full[blk], p_full[i].parity);
+              if (!ok) break;
+              p_full[i].step();
+              tc::tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc::mma_ts(tmem + TO + blk * D, tmem + TP + blk * (kKeys / 2) + kk * 8,
+                           b0 + (uint64_t)(kk * 2048 >> 4), id_o, j > 0 || kk > 0);
+              tc::mma_commit(&sm.o_full[blk]);
+            }
+            tc::mma_commit(&sm.v_empty[vs.i]);
+            vs.step();
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // ---------------------------------------------------------------- pages ----
+      const int GP = c.page_size / kGroup;
+      Ring<kRawStages> raw;
+      uint32_t empty_parity = 1, tile_no = 0;
       bool ok = true;
       for (unsigned long long x = x0; x < x1 && ok;) {
         Piece p;
         p.set(c, a, range, plan, entries, x, x1);
         x += p.end - p.begin;
-        const int blocks = p.rows() > kBlock ? 2 : 1;
-        const int n = p.end - p.begin;
-        // scores of the next tile, as soon as the softmax has the tile before in registers
-        auto scores = [&]() {
-          ok = wait(&sm.k_full[ks.i], ks.parity);
-          const uint64_t b0 = kd + (uint64_t)(ks.i * S::kTile >> 4);
-          for (int blk = 0; blk < blocks && ok; ++blk) {
-            ok = wait(&sm.s_free[blk], free_parity[blk]);
-            if (!ok) break;
-            free_parity[blk] ^= 1;
-            tc::tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t b1 =
-                  b0 + (uint64_t)(((kk >> 2) * (kKeys * 128) + (kk & 3) * 32) >> 4);
-              if (QS && blk == 1)
-                tc::mma_bf16_ss(tmem + TS + kKeys,
-                                qd + (uint64_t)(((kk >> 2) * (kBlock * 128) + (kk & 3) * 32) >> 4),
-                                b1, id_s, kk > 0);
-              else
-                tc::mma_ts(tmem + TS + blk * kKeys, tmem + TQ + blk * (D / 2) + kk * 8, b1, id_s,
-                           kk > 0);
+        const uint8_t* src = nullptr;
+        uint32_t present = 0;  // of the 32 groups from 32 n on, for the n being loaded
+        for (int j = p.begin; j < p.end; ++j, ++tile_no) {
+          const int first = j * kGroups & 31;
+          if (first == 0 || j == p.begin) {
+            const int gi = (j * kGroups & ~31) + lane;
+            const bool in = gi < (p.q.kv + kGroup - 1) / kGroup;
+            const int page =
+                in ? __ldg(a.block_table + (int64_t)p.b * a.max_blocks + gi / GP) : 0;
+            const bool sound = page >= 0 && page < c.num_pages;
+            if (in && !sound) report_error(a.err, kErrDeviceCheck);
+            src = c.pages + (((int64_t)page * c.kv_heads + p.h) * GP + gi % GP) * L::kGroupBytes;
+            present = __ballot_sync(0xffffffffu, in && sound);
+          }
+          ok = all_ok(wait(&sm.raw_empty[raw.i], empty_parity));
+          if (!ok) break;
+          if ((lane ^ first) < kGroups) {
+            const int u = lane ^ first;
+            if (u == 0)
+              *(volatile uint32_t*)&sm.valid[tile_no % kValidRing] =
+                  present >> first & ((1u << kGroups) - 1);
+            if (present >> lane & 1) {
+              tc::mbar_arrive_expect_tx(&sm.raw_full[raw.i], L::kGroupBytes);
+              tc::bulk_load(sm.raw[raw.i] + u * L::kGroupBytes, src, L::kGroupBytes,
+                            &sm.raw_full[raw.i]);
+            } else {
+              tc::mbar_arrive(&sm.raw_full[raw.i]);
             }
-            tc::mma_commit(&sm.s_full[blk]);
           }
-          tc::mma_commit(&sm.k_empty[ks.i]);
-          ks.step();
-        };
-        for (int blk = 0; blk < blocks && ok; ++blk) {
-          ok = wait(&sm.q_full[blk], q_full[blk].parity);
-          q_full[blk].step();
-        }
-        if (ok) scores();
-        for (int j = 0; j < n && ok; ++j) {
-          if (j + 1 < n) scores();
-          if (ok) ok = wait(&sm.v_full[vs.i], vs.parity);
-          const uint64_t b0 = vd + (uint64_t)(vs.i * S::kTile >> 4);
-          for (int blk = 0; blk < blocks && ok; ++blk) {
-            ok = wait(&sm.p_full[blk], p_full[blk].parity);
-            if (!ok) break;
-            p_full[blk].step();
-            tc::tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              tc::mma_ts(tmem + TO + blk * D, tmem + TP + blk * (kKeys / 2) + kk * 8,
-                         b0 + (uint64_t)(kk * 2048 >> 4), id_o, j > 0 || kk > 0);
-            tc::mma_commit(&sm.o_full[blk]);
-          }
-          tc::mma_commit(&sm.v_empty[vs.i]);
-          vs.step();
+          __syncwarp();
+          raw.step();
+          if (raw.i == 0) empty_parity ^= 1;
         }
       }
+      if (lane == 0) sm.copied = tile_no;
     }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- pages ----
-    const int GP = c.page_size / kGroup;
-    Ring<kRawStages> raw;
-    uint32_t empty_parity = 1, tile_no = 0;
-    bool ok = true;
-    for (unsigned long long x = x0; x < x1 && ok;) {
-      Piece p;
-      p.set(c, a, range, plan, entries, x, x1);
-      x += p.end - p.begin;
-      const uint8_t* src = nullptr;
-      uint32_t present = 0;  // of the 32 groups from 32 n on, for the n being loaded
-      for (int j = p.begin; j < p.end; ++j, ++tile_no) {
-        const int first = j * kGroups & 31;
-        if (first == 0 || j == p.begin) {
-          const int gi = (j * kGroups & ~31) + lane;
-          const bool in = gi < (p.q.kv + kGroup - 1) / kGroup;
-          const int page =
-              in ? __ldg(a.block_table + (int64_t)p.b * a.max_blocks + gi / GP) : 0;
-          const bool sound = page >= 0 && page < c.num_pages;
-          if (in && !sound) report_error(a.err, kErrDeviceCheck);
-          src = c.pages + (((int64_t)page * c.kv_heads + p.h) * GP + gi % GP) * L::kGroupBytes;
-          present = __ballot_sync(0xffffffffu, in && sound);
-        }
-        ok = all_ok(wait(&sm.raw_empty[raw.i], empty_parity));
-        if (!ok) break;
-        if ((lane ^ first) < kGroups) {
-          const int u = lane ^ first;
-          if (u == 0)
-            *(volatile uint32_t*)&sm.valid[tile_no % kValidRing] =
-                present >> first & ((1u << kGroups) - 1);
-          if (present >> lane & 1) {
-            tc::mbar_arrive_expect_tx(&sm.raw_full[raw.i], L::kGroupBytes);
-            tc::bulk_load(sm.raw[raw.i] + u * L::kGroupBytes, src, L::kGroupBytes,
-                          &sm.raw_full[raw.i]);
-          } else {
-            tc::mbar_arrive(&sm.raw_full[raw.i]);
-          }
-        }
-        __syncwarp();
-        raw.step();
-        if (raw.i == 0) empty_parity ^= 1;
-      }
-    }
-    if (lane == 0) sm.copied = tile_no;
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   // After a wait gave up, what is under way ends before its memory goes away: the products (of
   // the thread that elect.sync elects each time) and the copies of the last tiles.
-  if (*failed && warp == 12 && tc::elect_one()) {
+  if (*failed && issues && tc::elect_one()) {
     tc::mma_commit(&sm.issued);
     wait_phase(&sm.issued, 0, a.wait_cycles, nullptr);
   }
@@ -872,7 +897,7 @@ cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cu
                     a.q_head_stride % 8 == 0;
   plan_kernel<<<1, 1024, 0, st>>>(c, a, range, plan, (int)max_entries(c, a));
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  chunk_kernel<BITS, D><<<ctas, kThreads, kSmem, st>>>(c, a, range, plan, q_vec);
+  chunk_kernel<BITS, D><<<ctas, kThreads<BITS>, kSmem, st>>>(c, a, range, plan, q_vec);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, D, 4, 1>(c, a, plan.open, plan.o, plan.ml, 0, kRows, ctas, st);
 }
