@@ -9,8 +9,12 @@
 // a word, so 131072 pages are four words a thread.
 //
 // What bounds the calls is the chain of dependent loads, and launches: the steps of a call (rows
-// settled, pages marked, sums, new rows) run in one cluster of CTAs with barriers between them,
-// or, for large tables, as a kernel each over the whole GPU.
+// settled, pages marked, sums, new rows) run in one CTA or one cluster of them with barriers between
+// the steps, or, for large tables, as a kernel each over the whole GPU.  The copies are bound by HBM.
+//
+// Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 10 us and its 7 copies 3 us; of
+// 256 beams over 4096 tokens at most 17 us and 73 copies in two caches 7 us; a compaction of 4096
+// pages 14 us and its 930 moves of 128 KB 41 us, 0.88 of the measured HBM rate.
 #include <algorithm>
 
 #include "kda_common.cuh"
@@ -38,6 +42,15 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.arrive.release.aligned;\n\t"
       "barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
+}
+
+// Between the steps of a call that one CTA takes, or one cluster.
+template <bool ONE>
+__device__ __forceinline__ void step_sync() {
+  if constexpr (ONE)
+    __syncthreads();
+  else
+    cluster_sync();
 }
 
 // The CTAs that share a step: this one's number and how many they are.
@@ -291,16 +304,15 @@ __device__ __forceinline__ void fork_settle(const ForkArgs& a, const ForkScratch
 
 constexpr int kCluster = 8;  // CTAs of kThreads that take a call in one launch
 
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, ForkScratch s, int words) {
   __shared__ int warp_sums[32];
   fork_rows(a, s, words, grid_crew());
-  cluster_sync();
+  step_sync<ONE>();
   const Crew half{blockIdx.x % (kCluster / 2), kCluster / 2};  // side by side, not in turn
-  if (blockIdx.x < kCluster / 2)
-    fork_mark_old(a, s, half);
-  else
-    fork_mark_new(a, s, half);
-  cluster_sync();
+  if (ONE || blockIdx.x < kCluster / 2) fork_mark_old(a, s, ONE ? grid_crew() : half);
+  if (ONE || blockIdx.x >= kCluster / 2) fork_mark_new(a, s, ONE ? grid_crew() : half);
+  step_sync<ONE>();
   if (blockIdx.x == 0) fork_settle(a, s, words, warp_sums);
 }
 // The same as a kernel each.
@@ -432,16 +444,17 @@ __device__ __forceinline__ void compact_rows(const CompactArgs& a, const Compact
     a.free_pages[i] = L + (int)i;
 }
 
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, CompactScratch s,
                                                            int words) {
   __shared__ int warp_sums[32];
   __shared__ int before_l;
   compact_clear(a, s, words, grid_crew());
-  cluster_sync();
+  step_sync<ONE>();
   compact_mark(a, s, grid_crew());
-  cluster_sync();
+  step_sync<ONE>();
   if (blockIdx.x == 0) compact_plan(a, s, words, warp_sums, before_l);
-  cluster_sync();
+  step_sync<ONE>();
   compact_rows(a, s, grid_crew());
 }
 // The same as a kernel each.
@@ -558,9 +571,20 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// One cluster, whose CTAs wait for one another at the barriers between the steps.
+// Entries of tables that one CTA takes, and entries and pages that one cluster does.  Compactions
+// of 600 entries took 8.6 us with one CTA, 10.4 with the cluster, 13.7 as four kernels; of 5200 16.6,
+// 14.4 and 14.9; a fork of 35000 entries 29, 16.7 and 15.5 (and two launches more of the host's time).
+constexpr int64_t kOneEntries = 1 << 11, kClusterEntries = 1 << 18;
+constexpr int kOnePages = 1 << 15, kClusterPages = 1 << 20;
+
+// One CTA, or one cluster whose CTAs wait for one another at the barriers between the steps.
 template <typename... P, typename... A>
-cudaError_t launch_cluster(void (*kernel)(P...), cudaStream_t st, A... args) {
+cudaError_t launch_steps(bool one, void (*one_kernel)(P...), void (*kernel)(P...), cudaStream_t st,
+                         A... args) {
+  if (one) {
+    one_kernel<<<1, kThreads, 0, st>>>(args...);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kThreads);
@@ -573,10 +597,6 @@ cudaError_t launch_cluster(void (*kernel)(P...), cudaStream_t st, A... args) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-
-// Up to so many entries of tables, and pages, the cluster takes.
-constexpr int64_t kClusterEntries = 1 << 18;
-constexpr int kClusterPages = 1 << 20;
 
 // CTAs of a kernel over a table's entries.
 unsigned entry_ctas(int64_t entries, int most) {
@@ -626,8 +646,10 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
   fork_layout(a, static_cast<uint8_t*>(a.workspace), &s);
   const int words = words_of(a.num_pages);
   const int64_t rows = (int64_t)a.old_seqs + a.num_seqs;
-  if (rows * std::max(a.max_blocks, 1) <= kClusterEntries && a.num_pages <= kClusterPages)
-    return launch_cluster(fork_kernel, st, a, s, words);
+  const int64_t entries = rows * std::max(a.max_blocks, 1);
+  if (entries <= kClusterEntries && a.num_pages <= kClusterPages)
+    return launch_steps(entries <= kOneEntries && a.num_pages <= kOnePages, fork_kernel<true>,
+                        fork_kernel<false>, st, a, s, words);
   const int most = 8 * sm_count();
   fork_rows_kernel<<<(unsigned)std::min<int64_t>(std::max<int64_t>(words, rows) / 256 + 1, most),
                      256, 0, st>>>(
@@ -643,9 +665,10 @@ cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
   CompactScratch s;
   compact_layout(a, static_cast<uint8_t*>(a.workspace), &s);
   const int words = words_of(a.num_pages);
-  if ((int64_t)a.num_seqs * std::max(a.max_blocks, 1) <= kClusterEntries &&
-      a.num_pages <= kClusterPages)
-    return launch_cluster(compact_kernel, st, a, s, words);
+  const int64_t entries = (int64_t)a.num_seqs * std::max(a.max_blocks, 1);
+  if (entries <= kClusterEntries && a.num_pages <= kClusterPages)
+    return launch_steps(entries <= kOneEntries && a.num_pages <= kOnePages, compact_kernel<true>,
+                        compact_kernel<false>, st, a, s, words);
   const int most = 8 * sm_count();
   compact_clear_kernel<<<std::min(std::max(words, a.num_seqs) / 256 + 1, most), 256, 0, st>>>(
       a, s, words);
