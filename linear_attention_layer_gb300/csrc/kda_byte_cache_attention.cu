@@ -13,13 +13,30 @@
 namespace kda {
 namespace {
 
+// Calls f with the variant for the call's types and expected rows per kv head (kda_cache_attention.cu
+// has what tiles of 8 and 16 rows are for).  Warps, stages, CTAs a SM by measurement; us of 100
+// requests of 256 to 8192 tokens, 8 kv heads, 4 query heads each, one or four new tokens:
+//     bf16 128   8 rows   4 x 2 x 3  154   8 x 3 x 1  157   12 x 2 x 1  151
+//               16 rows   8 x 3 x 1  171   4 x 2 x 3  256   12 x 2 x 1  254 (these spill)
+//     bf16  64   8 rows   8 x 3 x 2   87   4 x 4 x 3   90    4 x 2 x 5  123
+//               16 rows   8 x 4 x 1  113   4 x 4 x 3  112    8 x 3 x 2  171
+//     fp32 128   8 rows   8 x 3 x 1  153   4 x 2 x 3  184
+//               16 rows   8 x 2 x 1  268   4 x 2 x 2  266    4 x 3 x 1  332
+//     fp32  64   8 rows   8 x 3 x 2  119   4 x 4 x 3  105    4 x 2 x 4  113
+//               16 rows   8 x 4 x 1  158   4 x 3 x 3  172    8 x 2 x 2  214
+// Few units, fewer than half the SMs, are each cut over many CTAs, whose parts a second kernel joins:
+// one CTA of 8 warps leaves it a third of the parts that three of 4 do (one request
+// of 2048 tokens 13.2 us for 14.6, of 131072 on one kv head 22 for 33; 256 requests 349 for 335).
 template <typename F>
 auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
   const bool few = (int64_t)a.max_new * (a.num_heads / c.kv_heads) <= 8;
+  const bool few_units = (int64_t)a.num_seqs * c.kv_heads <= 64;
   if (a.bf16) {
     using T = __nv_bfloat16;
-    if (a.head_dim == 128)
+    if (a.head_dim == 128) {
+      if (few && few_units) return f(Split<8, T, 128, 1, 8, 3, 1>{});
       return few ? f(Split<8, T, 128, 1, 4, 2, 3>{}) : f(Split<8, T, 128, 2, 8, 3, 1>{});
+    }
     return few ? f(Split<8, T, 64, 1, 8, 3, 2>{}) : f(Split<8, T, 64, 2, 8, 4, 1>{});
   }
   if (a.head_dim == 128)
