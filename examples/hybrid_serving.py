@@ -1,15 +1,18 @@
 """Serving a small hybrid model: three KDA layers, then one layer of grouped-query attention.
 
 A KDA layer's memory of a request is a state of fixed size (fp32, updated in place); the
-attention layer's is the 4-bit paged cache.  One step of the server, whatever each request
+attention layer's is the paged cache, in 4 bits or in 8.  One step of the server, whatever each request
 brings -- a prompt, a chunk of one, one token, a window of drafts -- is
 
     cache_tables      pages for the new tokens, given back for rejected ones
     per block         chunk_fwd (or decode_step) three times,
                       cache_append + cache_attention once
 
-with random weights: ``python examples/hybrid_serving.py`` runs a prompt phase, decode
-steps and a window of drafts that is partly rejected, and prints what the cache holds.
+and a request may go on as several (``fork``: cache_fork and cache_copy for the attention
+layers' pages, which they share, a copy of the state for the KDA layers).  With random
+weights: ``python examples/hybrid_serving.py`` runs a prompt phase, decode steps, a window of
+drafts that is partly rejected and a fork, packs the pages (``compact``) and prints what the
+cache holds.
 """
 import os
 import sys
@@ -49,13 +52,15 @@ def _norm(x):
 class Server:
     """Up to ``slots`` requests at a time; one ``step`` feeds each of them some tokens."""
 
-    def __init__(self, model, slots, pages, page_size=64, max_blocks=64):
+    def __init__(self, model, slots, pages, page_size=64, max_blocks=64, bits=4):
         m, dev = model, model.device
-        self.model, self.page_size = model, page_size
+        self.model, self.page_size, self.pages = model, page_size, pages
+        empty, self.append, self.attend = {
+            4: (kda.cache_empty, kda.cache_append, kda.cache_attention),
+            8: (kda.byte_cache_empty, kda.byte_cache_append, kda.byte_cache_attention)}[bits]
         self.states = [[torch.zeros((slots, m.kda_heads, m.dim, m.dim), device=dev)
                         for _ in range(3)] for _ in range(m.blocks)]
-        self.caches = [kda.cache_empty(pages, page_size, m.kv_heads, m.dim, dev)
-                       for _ in range(m.blocks)]
+        self.caches = [empty(pages, page_size, m.kv_heads, m.dim, dev) for _ in range(m.blocks)]
         self.table = torch.full((slots, max_blocks), -1, dtype=torch.int32, device=dev)
         self.free = torch.arange(pages, dtype=torch.int32, device=dev)
         self.free_range = torch.tensor([0, pages], device=dev)
@@ -104,9 +109,30 @@ class Server:
         m, T = self.model, x.shape[0]
         qkv = (x @ w["qkv"]).view(T, m.heads + 2 * m.kv_heads, m.dim)
         q, k, v = qkv.split([m.heads, m.kv_heads, m.kv_heads], dim=1)  # views: strides, no copies
-        kda.cache_append(k, v, slots, cache)
-        o = kda.cache_attention(q, cache, self.table, lens, cu, max_new=longest)
+        self.append(k, v, slots, cache)
+        o = self.attend(q, cache, self.table, lens, cu, max_new=longest)
         return o.reshape(T, -1) @ w["out"]
+
+    def fork(self, parents):
+        """Slot b goes on from where the request in slot parents[b] is (-1: empty).  Requests
+        whose slot nobody names are over.  Once pages are shared, requests end here and not by
+        ``step``, which gives back pages whoever else holds them."""
+        p = torch.tensor(parents, dtype=torch.int32, device=self.held.device)
+        keep = torch.where(p >= 0, self.held[p.clamp(min=0).long()], 0).int()
+        self.held, self.table, copies, self.free_range = kda.cache_fork(
+            self.held, self.table, p, keep, self.free, self.free_range, page_size=self.page_size,
+            num_pages=self.pages)
+        kda.cache_copy(self.caches, copies)
+        live = (p >= 0).view(-1, 1, 1, 1)
+        for states in self.states:
+            for state in states:
+                state.copy_(torch.where(live, state[p.clamp(min=0).long()], 0.0))
+
+    def compact(self):
+        """Moves the pages in use to the lowest numbers; the others are free."""
+        self.table, copies, self.free_range = kda.cache_compact(
+            self.held, self.table, self.free, page_size=self.page_size, num_pages=self.pages)
+        kda.cache_copy(self.caches, copies)
 
     def snapshot(self):
         return [[s.clone() for s in states] for states in self.states]
@@ -135,6 +161,10 @@ def main():
     accepted = [3, 0, 1, 2]
     server.step(tokens(sum(accepted)), accepted, keep=lens)
     server.step(tokens(3), [1, 1, -1, 1])  # the third request is over
+    server.fork([0, 1, 0, 0])  # three answers to the first, the fourth request is over
+    server.step(tokens(4), [1, 1, 1, 1])
+    server.compact()
+    server.step(tokens(4), [1, 1, 1, 1])
     head, tail = server.free_range.tolist()
     error = kda.get_device_error()
     print(f"lengths {server.held.tolist()}, free pages {tail - head} of 64, "
