@@ -9,12 +9,14 @@
 // a word, so 131072 pages are four words a thread.
 //
 // What bounds the calls is the chain of dependent loads, and launches: the steps of a call (rows
-// settled, pages marked, sums, new rows) run in one CTA or one cluster of them with barriers between
-// the steps, or, for large tables, as a kernel each over the whole GPU.  The copies are bound by HBM.
+// settled, pages marked, sums, new rows) run in one CTA or one cluster of them, with the bitmaps in
+// shared memory and barriers between the steps, or, for large tables, as a kernel each over the
+// whole GPU.  The copies are bound by HBM.
 //
-// Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 10 us and its 7 copies 3 us; of
-// 256 beams over 4096 tokens at most 17 us and 73 copies in two caches 7 us; a compaction of 4096
-// pages 14 us and its 930 moves of 128 KB 41 us, 0.88 of the measured HBM rate.
+// Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 9 us and its 7 copies 3 us; of
+// 256 beams over 4096 tokens at most 12.5 us and 73 copies in two caches 7 us; a compaction of 4096
+// pages 12.5 us and its 930 moves of 128 KB 41 us, 0.88 of the measured HBM rate (in the kernel
+// alone 37, all of it).
 #include <algorithm>
 
 #include "kda_common.cuh"
@@ -44,13 +46,12 @@ __device__ __forceinline__ void cluster_sync() {
           : "memory");
 }
 
-// Between the steps of a call that one CTA takes, or one cluster.
-template <bool ONE>
-__device__ __forceinline__ void step_sync() {
-  if constexpr (ONE)
-    __syncthreads();
-  else
-    cluster_sync();
+// A word of shared memory of another CTA of the cluster, at this CTA's address of it.
+__device__ __forceinline__ uint32_t of_cta(const uint32_t* p, int cta) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(p), x;
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(cta));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
 }
 
 // The CTAs that share a step: this one's number and how many they are.
@@ -158,15 +159,15 @@ struct ForkScratch {
 };
 
 // Zeroes the bitmaps and settles each new row: a row whose parent or length does not make sense
-// keeps nothing.
+// keeps nothing.  Of crews that do the same, the lead speaks for all.
 __device__ __forceinline__ void fork_rows(const ForkArgs& a, const ForkScratch& s, int words,
-                                          Crew crew) {
+                                          Crew crew, bool lead) {
   const uint32_t i = crew.thread(), n = crew.threads();
   for (uint32_t w = i; w < (uint32_t)words; w += n)
     s.old_map[w] = s.whole_map[w] = s.tail_map[w] = 0;
   const int P = a.page_size;
   for (uint32_t r = i; r < (uint32_t)a.old_seqs; r += n)  // its pages stay where they are
-    if (!sound(a.held_lens[r], P, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
+    if (lead && !sound(a.held_lens[r], P, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
   for (uint32_t b = i; b < (uint32_t)a.num_seqs; b += n) {
     const int parent = a.parents[b];
     Row r{0, -1};
@@ -178,13 +179,13 @@ __device__ __forceinline__ void fork_rows(const ForkArgs& a, const ForkScratch& 
           const int page = a.block_table[(int64_t)parent * a.max_blocks + keep / P];
           if (page >= 0 && page < a.num_pages) {
             r.tail = page;
-            s.first[page] = INT32_MAX;
+            if (lead) s.first[page] = INT32_MAX;
           }
         }
-      } else {
+      } else if (lead) {
         report_error(a.err, kErrDeviceCheck);
       }
-    } else if (parent != -1) {
+    } else if (lead && parent != -1) {
       report_error(a.err, kErrDeviceCheck);
     }
     s.rows[b] = r;
@@ -196,13 +197,17 @@ __device__ __forceinline__ void fork_mark_old(const ForkArgs& a, const ForkScrat
             a.num_pages, a.err, crew);
 }
 
-// Writes the new rows and marks their pages.
-__device__ __forceinline__ void fork_mark_new(const ForkArgs& a, const ForkScratch& s, Crew crew) {
-  const int P = a.page_size;
+// The lowest row that ends inside each page.
+__device__ __forceinline__ void fork_first(const ForkArgs& a, const ForkScratch& s, Crew crew) {
   for (uint32_t b = crew.thread(); b < (uint32_t)a.num_seqs; b += crew.threads()) {
     const int tail = s.rows[b].tail;
     if (tail >= 0) atomicMin(s.first + tail, (int)b);
   }
+}
+
+// Writes the new rows and marks their pages.
+__device__ __forceinline__ void fork_mark_new(const ForkArgs& a, const ForkScratch& s, Crew crew) {
+  const int P = a.page_size;
   const uint64_t total = (uint64_t)a.num_seqs * a.max_blocks, step = crew.threads();
   for (uint64_t i = crew.thread(); i < total; i += kBatch * step) {
     int keep[kBatch], parent[kBatch], page[kBatch];
@@ -234,19 +239,27 @@ __device__ __forceinline__ void fork_mark_new(const ForkArgs& a, const ForkScrat
   }
 }
 
-// Settles the unfinished last pages and gives back what nobody holds: one CTA.
-__device__ __forceinline__ void fork_settle(const ForkArgs& a, const ForkScratch& s, int words,
-                                            int* warp_sums) {
-  const int P = a.page_size;
-  int64_t head = a.free_range[0], tail = a.free_range[1];
-  if (!(head >= 0 && tail >= head && tail - head <= a.ring_size)) {
-    head = tail = 0;
-    if (threadIdx.x == 0) report_error(a.err, kErrDeviceCheck);
+// The ring of free pages as a call finds it; empty if its range makes no sense.  It runs on from
+// head0 and tail0 without a division.
+struct FreeRing {
+  int64_t head, tail, head0, tail0;
+};
+__device__ __forceinline__ FreeRing load_ring(const ForkArgs& a, bool lead) {
+  FreeRing r{a.free_range[0], a.free_range[1], 0, 0};
+  if (!(r.head >= 0 && r.tail >= r.head && r.tail - r.head <= a.ring_size)) {
+    r.head = r.tail = 0;
+    if (lead && threadIdx.x == 0) report_error(a.err, kErrDeviceCheck);
   }
-  const int64_t avail = tail - head;
-  // the ring runs on from its head without a division: a row's place in it is less than two turns
-  // off as long as no more pages are asked for than there are
-  const int64_t head0 = head % a.ring_size, tail0 = tail % a.ring_size;
+  r.head0 = r.head % a.ring_size;
+  r.tail0 = r.tail % a.ring_size;
+  return r;
+}
+
+// Settles the unfinished last pages and gives back what nobody holds: one CTA.
+__device__ __forceinline__ void fork_settle(const ForkArgs& a, const ForkScratch& s,
+                                            const FreeRing& ring, int words, int* warp_sums) {
+  const int P = a.page_size;
+  const int64_t avail = ring.tail - ring.head;
   auto in_ring = [&](int64_t at) { return at < a.ring_size ? at : at % a.ring_size; };
   int64_t asked = 0;
   for (uint32_t base = 0; base < (uint32_t)a.num_seqs; base += kThreads) {
@@ -268,7 +281,7 @@ __device__ __forceinline__ void fork_settle(const ForkArgs& a, const ForkScratch
         int32_t* entry = a.block_table_out + (int64_t)b * a.max_blocks + r.keep / P;
         if (at < avail) {
           copy[0] = r.tail;
-          copy[1] = a.free_pages[in_ring(head0 + at)];
+          copy[1] = a.free_pages[in_ring(ring.head0 + at)];
           copy[2] = r.keep % P;
           *entry = copy[1];
         } else {  // no page is left: the row ends with its last whole one
@@ -290,37 +303,68 @@ __device__ __forceinline__ void fork_settle(const ForkArgs& a, const ForkScratch
   int count = 0, freed;
   for (int w = w0; w < w1; ++w)
     count += __popc(s.old_map[w] & ~(s.whole_map[w] | *(volatile uint32_t*)(s.tail_map + w)));
-  int64_t at = block_scan(count, warp_sums, freed) + tail0;
+  int64_t at = block_scan(count, warp_sums, freed) + ring.tail0;
   for (int w = w0; w < w1; ++w) {
     uint32_t gone = s.old_map[w] & ~(s.whole_map[w] | *(volatile uint32_t*)(s.tail_map + w));
     for (; gone; gone &= gone - 1) a.free_pages[in_ring(at++)] = w * 32 + __ffs(gone) - 1;
   }
   if (threadIdx.x == 0) {
-    a.free_range_out[0] = head + taken;
-    a.free_range_out[1] = tail + freed;
+    a.free_range_out[0] = ring.head + taken;
+    a.free_range_out[1] = ring.tail + freed;
     if (avail - taken + freed > a.ring_size) report_error(a.err, kErrDeviceCheck);
   }
 }
 
-constexpr int kCluster = 8;  // CTAs of kThreads that take a call in one launch
+// A call in one launch: CTAs CTAs, one or a cluster, with their bitmaps and rows in shared memory.
+// Each settles all rows for itself; marks its part of the entries in its own bitmap, half of the
+// CTAs the old rows', half the new ones'; and the first one puts the bitmaps together.
+constexpr int kCluster = 8;
+constexpr int kMapWords = 2048, kMostRows = 1024;
 
-template <bool ONE>
-__global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, ForkScratch s, int words) {
+template <int CTAS>
+__global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, int32_t* first, int words) {
+  __shared__ uint32_t maps[3][kMapWords];
+  __shared__ Row rows[kMostRows];
   __shared__ int warp_sums[32];
-  fork_rows(a, s, words, grid_crew());
-  step_sync<ONE>();
-  const Crew half{blockIdx.x % (kCluster / 2), kCluster / 2};  // side by side, not in turn
-  if (ONE || blockIdx.x < kCluster / 2) fork_mark_old(a, s, ONE ? grid_crew() : half);
-  if (ONE || blockIdx.x >= kCluster / 2) fork_mark_new(a, s, ONE ? grid_crew() : half);
-  step_sync<ONE>();
-  if (blockIdx.x == 0) fork_settle(a, s, words, warp_sums);
+  const ForkScratch s{maps[0], maps[1], maps[2], first, rows};
+  const bool lead = blockIdx.x == 0;
+  const Crew alone{0, 1};
+  const FreeRing ring = load_ring(a, lead);
+  fork_rows(a, s, words, alone, lead);
+  __syncthreads();
+  if (lead) fork_first(a, s, alone);
+  if constexpr (CTAS == 1) {
+    fork_mark_old(a, s, alone);
+    fork_mark_new(a, s, alone);
+    __syncthreads();
+  } else {
+    const Crew half{blockIdx.x % (CTAS / 2), CTAS / 2};
+    if (blockIdx.x < CTAS / 2)
+      fork_mark_old(a, s, half);
+    else
+      fork_mark_new(a, s, half);
+    cluster_sync();
+    if (lead)
+      for (int w = threadIdx.x; w < words; w += kThreads) {
+        uint32_t held = maps[0][w], whole = 0;
+#pragma unroll
+        for (int i = 1; i < CTAS / 2; ++i) held |= of_cta(&maps[0][w], i);
+#pragma unroll
+        for (int i = CTAS / 2; i < CTAS; ++i) whole |= of_cta(&maps[1][w], i);
+        maps[0][w] = held;
+        maps[1][w] = whole;
+      }
+    cluster_sync();  // before the others leave
+  }
+  if (lead) fork_settle(a, s, ring, words, warp_sums);
 }
 // The same as a kernel each.
 __global__ void __launch_bounds__(256) fork_rows_kernel(ForkArgs a, ForkScratch s, int words) {
-  fork_rows(a, s, words, grid_crew());
+  fork_rows(a, s, words, grid_crew(), true);
 }
 __global__ void __launch_bounds__(256) fork_mark_kernel(ForkArgs a, ForkScratch s) {
   wait_for_previous();
+  fork_first(a, s, grid_crew());
   fork_mark_old(a, s, grid_crew());
   fork_mark_new(a, s, grid_crew());
 }
@@ -328,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) fork_settle_kernel(ForkArgs a, ForkS
                                                                int words) {
   __shared__ int warp_sums[32];
   wait_for_previous();
-  fork_settle(a, s, words, warp_sums);
+  fork_settle(a, s, load_ring(a, true), words, warp_sums);
 }
 
 // --------------------------------------------------------------- compact ----
@@ -339,24 +383,23 @@ struct CompactScratch {
   int32_t* count;    // pages in use
 };
 
-__device__ __forceinline__ void compact_clear(const CompactArgs& a, const CompactScratch& s,
-                                              int words, Crew crew) {
-  for (uint32_t w = crew.thread(); w < (uint32_t)words; w += crew.threads()) s.live[w] = 0;
+__device__ __forceinline__ void compact_clear(const CompactArgs& a, uint32_t* live, int words,
+                                              Crew crew, bool lead) {
+  for (uint32_t w = crew.thread(); w < (uint32_t)words; w += crew.threads()) live[w] = 0;
   for (uint32_t r = crew.thread(); r < (uint32_t)a.num_seqs; r += crew.threads())
-    if (!sound(a.held_lens[r], a.page_size, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
+    if (lead && !sound(a.held_lens[r], a.page_size, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
 }
 
-__device__ __forceinline__ void compact_mark(const CompactArgs& a, const CompactScratch& s,
-                                             Crew crew) {
-  mark_rows(s.live, a.block_table, a.held_lens, a.num_seqs, a.max_blocks, a.page_size, a.num_pages,
+__device__ __forceinline__ void compact_mark(const CompactArgs& a, uint32_t* live, Crew crew) {
+  mark_rows(live, a.block_table, a.held_lens, a.num_seqs, a.max_blocks, a.page_size, a.num_pages,
             a.err, crew);
 }
 
 // Pages in use before each word, and the list of moves: the i-th page in use at or past their
 // number L goes to the i-th free one below it.
-// One CTA.
+// One CTA, or several that do the same, of which the lead writes.
 __device__ __forceinline__ void compact_plan(const CompactArgs& a, const CompactScratch& s,
-                                             int words, int* warp_sums, int& before_l) {
+                                             int words, int* warp_sums, int& before_l, bool lead) {
   const int per = (words + kThreads - 1) / kThreads;
   const int w0 = min(words, per * (int)threadIdx.x), w1 = min(words, w0 + per);
   int count = 0, L;
@@ -371,11 +414,14 @@ __device__ __forceinline__ void compact_plan(const CompactArgs& a, const Compact
   }
   if (threadIdx.x == 0) {
     s.count[0] = L;
-    a.free_range_out[0] = 0;
-    a.free_range_out[1] = a.num_pages - L;
+    if (lead) {
+      a.free_range_out[0] = 0;
+      a.free_range_out[1] = a.num_pages - L;
+    }
     if (L >> 5 >= words) before_l = L;  // L == num_pages, the words full
   }
   __syncthreads();
+  if (!lead) return;
   const int stay = before_l, moves = L - stay;
   at = at0;
   for (int w = w0; w < w1; ++w) {
@@ -444,34 +490,50 @@ __device__ __forceinline__ void compact_rows(const CompactArgs& a, const Compact
     a.free_pages[i] = L + (int)i;
 }
 
-template <bool ONE>
-__global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, CompactScratch s,
-                                                           int words) {
-  __shared__ int warp_sums[32];
-  __shared__ int before_l;
-  compact_clear(a, s, words, grid_crew());
-  step_sync<ONE>();
-  compact_mark(a, s, grid_crew());
-  step_sync<ONE>();
-  if (blockIdx.x == 0) compact_plan(a, s, words, warp_sums, before_l);
-  step_sync<ONE>();
+// A call in one launch, as fork_kernel; every CTA puts the bitmaps together for itself.
+template <int CTAS>
+__global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, int words) {
+  __shared__ uint32_t mine[kMapWords], live[CTAS == 1 ? 1 : kMapWords];
+  __shared__ int before[kMapWords], warp_sums[32], before_l, count;
+  const CompactScratch s{CTAS == 1 ? mine : live, before, &count};
+  const bool lead = blockIdx.x == 0;
+  compact_clear(a, mine, words, Crew{0, 1}, lead);
+  __syncthreads();
+  compact_mark(a, mine, grid_crew());
+  if constexpr (CTAS == 1) {
+    __syncthreads();
+  } else {
+    cluster_sync();
+    for (int w = threadIdx.x; w < words; w += kThreads) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < CTAS; ++i) x |= of_cta(&mine[w], i);
+      live[w] = x;
+    }
+    __syncthreads();
+  }
+  compact_plan(a, s, words, warp_sums, before_l, lead);
+  if constexpr (CTAS == 1)
+    __syncthreads();
+  else
+    cluster_sync();  // the moves; and before a CTA leaves, whose bitmap the others read
   compact_rows(a, s, grid_crew());
 }
 // The same as a kernel each.
 __global__ void __launch_bounds__(256) compact_clear_kernel(CompactArgs a, CompactScratch s,
                                                             int words) {
-  compact_clear(a, s, words, grid_crew());
+  compact_clear(a, s.live, words, grid_crew(), true);
 }
 __global__ void __launch_bounds__(256) compact_mark_kernel(CompactArgs a, CompactScratch s) {
   wait_for_previous();
-  compact_mark(a, s, grid_crew());
+  compact_mark(a, s.live, grid_crew());
 }
 __global__ void __launch_bounds__(kThreads) compact_plan_kernel(CompactArgs a, CompactScratch s,
                                                                 int words) {
   __shared__ int warp_sums[32];
   __shared__ int before_l;
   wait_for_previous();
-  compact_plan(a, s, words, warp_sums, before_l);
+  compact_plan(a, s, words, warp_sums, before_l, true);
 }
 __global__ void __launch_bounds__(256) compact_rows_kernel(CompactArgs a, CompactScratch s) {
   wait_for_previous();
@@ -571,11 +633,12 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Entries of tables that one CTA takes, and entries and pages that one cluster does.  Compactions
-// of 600 entries took 8.6 us with one CTA, 10.4 with the cluster, 13.7 as four kernels; of 5200 16.6,
-// 14.4 and 14.9; a fork of 35000 entries 29, 16.7 and 15.5 (and two launches more of the host's time).
+// Entries of tables that one CTA takes, and that one cluster does (pages and rows as far as its
+// shared memory has room).  Compactions of 600 entries took 8.6 us with one CTA, 10.3 with the
+// cluster, 13.7 as four kernels; of 5200 15.1, 12.4 and 14.9.  A fork of 35000 entries took 12.5 us
+// with the cluster, 15.5 as three kernels.
 constexpr int64_t kOneEntries = 1 << 11, kClusterEntries = 1 << 18;
-constexpr int kOnePages = 1 << 15, kClusterPages = 1 << 20;
+constexpr int kClusterPages = 32 * kMapWords;
 
 // One CTA, or one cluster whose CTAs wait for one another at the barriers between the steps.
 template <typename... P, typename... A>
@@ -647,9 +710,9 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
   const int words = words_of(a.num_pages);
   const int64_t rows = (int64_t)a.old_seqs + a.num_seqs;
   const int64_t entries = rows * std::max(a.max_blocks, 1);
-  if (entries <= kClusterEntries && a.num_pages <= kClusterPages)
-    return launch_steps(entries <= kOneEntries && a.num_pages <= kOnePages, fork_kernel<true>,
-                        fork_kernel<false>, st, a, s, words);
+  if (entries <= kClusterEntries && a.num_pages <= kClusterPages && a.num_seqs <= kMostRows)
+    return launch_steps(entries <= kOneEntries, fork_kernel<1>, fork_kernel<kCluster>, st, a, s.first,
+                        words);
   const int most = 8 * sm_count();
   fork_rows_kernel<<<(unsigned)std::min<int64_t>(std::max<int64_t>(words, rows) / 256 + 1, most),
                      256, 0, st>>>(
@@ -667,8 +730,8 @@ cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
   const int words = words_of(a.num_pages);
   const int64_t entries = (int64_t)a.num_seqs * std::max(a.max_blocks, 1);
   if (entries <= kClusterEntries && a.num_pages <= kClusterPages)
-    return launch_steps(entries <= kOneEntries && a.num_pages <= kOnePages, compact_kernel<true>,
-                        compact_kernel<false>, st, a, s, words);
+    return launch_steps(entries <= kOneEntries, compact_kernel<1>, compact_kernel<kCluster>, st, a,
+                        words);
   const int most = 8 * sm_count();
   compact_clear_kernel<<<std::min(std::max(words, a.num_seqs) / 256 + 1, most), 256, 0, st>>>(
       a, s, words);
