@@ -389,8 +389,8 @@ kda_status_t kda_chunk_fwd_noalloc(const kda_desc_t* desc, const void* q, const 
 /*
  * kda_testing_inject_wait_timeout -- testing aid for the failure path (the
  * device-side waits are bounded; this makes one of them run out).  The next
- * `launches` tensor-core prefill launches and kda_cache_attention calls issued
- * from the calling host thread arm their first input barriers with 16 bytes
+ * `launches` tensor-core prefill launches and kda_cache_attention or
+ * kda_byte_cache_attention calls issued from the calling host thread arm their first input barriers with 16 bytes
  * that no copy delivers (an arrival that does not come) and cut the wait
  * budget to ~10 ms: the wait expires, the kernel records KDA_ERR_TIMEOUT in
  * the device error word, cancels the phantom bytes (makes up the arrival), lets
@@ -903,8 +903,8 @@ kda_status_t kda_byte_cache_attention_workspace_size(const kda_byte_cache_t* cac
  * again: where keep_lens[b] ends inside a page that other new rows hold as well, the
  * lowest of the rows that end inside it keeps it -- none, if some row holds more of it
  * as a whole page -- and each other one gets a page from free_pages, in row order, and
- * a copy to be made.  Pages that old rows held and no new row holds go back to
- * free_pages, in rising order.
+ * a copy to be made, before anything is appended.  Pages that old rows held and no new
+ * row holds go back to free_pages, in rising order.
  *
  *   held_lens        device, [old_seqs] int32
  *   block_table      device, [old_seqs][max_blocks] int32
@@ -941,8 +941,9 @@ kda_status_t kda_cache_fork_workspace_size(int32_t num_pages, int32_t num_seqs, 
  * that a cache can go on in fewer pages.
  *
  * Pages below L that are in use stay; the i-th one in use from L on moves to the i-th
- * free one below L.  All other pages are free afterwards: the ring holds L ..
- * num_pages - 1, in order, from its first entry on.
+ * free one below L; the copies have to be made before anything is appended or read.
+ * All other pages are free afterwards: the ring holds L .. num_pages - 1, in order,
+ * from its first entry on.
  *
  *   held_lens        device, [num_seqs] int32
  *   block_table      device, [num_seqs][max_blocks] int32

@@ -856,7 +856,7 @@ def get_device_error(stream=None) -> int:
 
 def testing_inject_wait_timeout(launches: int = 1) -> None:
     """Make the next `launches` tensor-core prefill launches or ``cache_attention``
-    calls of this thread hit an expired device wait
+    and ``byte_cache_attention`` calls of this thread hit an expired device wait
     (``kda_testing_inject_wait_timeout``)."""
     load().kda_testing_inject_wait_timeout(int(launches))
 
@@ -1177,7 +1177,8 @@ def cache_fork(held_lens, block_table, parents, keep_lens, free_pages, free_rang
     pages; pages that no new row holds go back to ``free_pages`` (int32, updated).
     Returns (kv_lens [R], block_table [R, max_blocks], copies [R, 3],
     free_range_out [2]): ``cache_copy(caches, copies)`` then fills the pages of rows
-    that would go on writing into a page that another row holds.  Serves for
+    that would go on writing into a page that another row holds (call it before
+    anything is appended).  Serves for
     several answers to a prompt, beams, kept prefixes, and to end or cut requests
     that share pages.  ``workspace``: a uint8 tensor of
     ``cache_fork_workspace_size`` bytes, else allocated here."""

@@ -152,6 +152,14 @@ struct Row {
   int32_t keep, tail;
 };
 
+// Rows that make no sense: their pages stay where they are.
+__device__ __forceinline__ void check_rows(const int32_t* lens, int rows, int columns,
+                                           int page_size, int* err) {
+  const Crew crew = grid_crew();
+  for (uint32_t r = crew.thread(); r < (uint32_t)rows; r += crew.threads())
+    if (!sound(lens[r], page_size, columns)) report_error(err, kErrDeviceCheck);
+}
+
 struct ForkScratch {
   uint32_t *old_map, *whole_map, *tail_map;  // pages of old rows, of new rows whole, kept tails
   int32_t* first;                            // [num_pages] lowest row with the page as its tail
@@ -166,8 +174,6 @@ __device__ __forceinline__ void fork_rows(const ForkArgs& a, const ForkScratch& 
   for (uint32_t w = i; w < (uint32_t)words; w += n)
     s.old_map[w] = s.whole_map[w] = s.tail_map[w] = 0;
   const int P = a.page_size;
-  for (uint32_t r = i; r < (uint32_t)a.old_seqs; r += n)  // its pages stay where they are
-    if (lead && !sound(a.held_lens[r], P, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
   for (uint32_t b = i; b < (uint32_t)a.num_seqs; b += n) {
     const int parent = a.parents[b];
     Row r{0, -1};
@@ -330,6 +336,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, int32_t* fir
   const bool lead = blockIdx.x == 0;
   const Crew alone{0, 1};
   const FreeRing ring = load_ring(a, lead);
+  check_rows(a.held_lens, a.old_seqs, a.max_blocks, a.page_size, a.err);
   fork_rows(a, s, words, alone, lead);
   __syncthreads();
   if (lead) fork_first(a, s, alone);
@@ -360,6 +367,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, int32_t* fir
 }
 // The same as a kernel each.
 __global__ void __launch_bounds__(256) fork_rows_kernel(ForkArgs a, ForkScratch s, int words) {
+  check_rows(a.held_lens, a.old_seqs, a.max_blocks, a.page_size, a.err);
   fork_rows(a, s, words, grid_crew(), true);
 }
 __global__ void __launch_bounds__(256) fork_mark_kernel(ForkArgs a, ForkScratch s) {
@@ -384,10 +392,9 @@ struct CompactScratch {
 };
 
 __device__ __forceinline__ void compact_clear(const CompactArgs& a, uint32_t* live, int words,
-                                              Crew crew, bool lead) {
+                                              Crew crew) {
   for (uint32_t w = crew.thread(); w < (uint32_t)words; w += crew.threads()) live[w] = 0;
-  for (uint32_t r = crew.thread(); r < (uint32_t)a.num_seqs; r += crew.threads())
-    if (lead && !sound(a.held_lens[r], a.page_size, a.max_blocks)) report_error(a.err, kErrDeviceCheck);
+  check_rows(a.held_lens, a.num_seqs, a.max_blocks, a.page_size, a.err);
 }
 
 __device__ __forceinline__ void compact_mark(const CompactArgs& a, uint32_t* live, Crew crew) {
@@ -497,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, int wo
   __shared__ int before[kMapWords], warp_sums[32], before_l, count;
   const CompactScratch s{CTAS == 1 ? mine : live, before, &count};
   const bool lead = blockIdx.x == 0;
-  compact_clear(a, mine, words, Crew{0, 1}, lead);
+  compact_clear(a, mine, words, Crew{0, 1});
   __syncthreads();
   compact_mark(a, mine, grid_crew());
   if constexpr (CTAS == 1) {
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, int wo
 // The same as a kernel each.
 __global__ void __launch_bounds__(256) compact_clear_kernel(CompactArgs a, CompactScratch s,
                                                             int words) {
-  compact_clear(a, s.live, words, grid_crew(), true);
+  compact_clear(a, s.live, words, grid_crew());
 }
 __global__ void __launch_bounds__(256) compact_mark_kernel(CompactArgs a, CompactScratch s) {
   wait_for_previous();

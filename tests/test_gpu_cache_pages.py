@@ -44,6 +44,23 @@ def test_fork(seed, B, R, N):
     _check_fork(held, table, parents, keep, ring, span, 16, N)
 
 
+@pytest.mark.parametrize("B,R,blocks,N", [(60, 300, 30, 700), (9, 1024, 5, 900), (9, 1025, 5, 900),
+                                          (40, 40, 100, 65536), (40, 40, 100, 65537),
+                                          (300, 400, 374, 1300), (300, 400, 376, 1300)])
+def test_fork_at_the_borders_of_its_forms(B, R, blocks, N):
+    """One CTA, one cluster and a kernel a step: by entries of the tables, rows and pages."""
+    for seed in range(3):
+        rng = np.random.RandomState(seed)
+        held, table, ring, span = _random_state(rng, B, 16, blocks, N)
+        parents = rng.randint(-1, B, R)
+        keep = [int(rng.choice([held[p], rng.randint(0, held[p] + 1)])) if p >= 0 else 0
+                for p in parents]
+        need = sum(1 for k in keep if k % 16)
+        if need > span[1] - span[0]:
+            keep = [k // 16 * 16 if i % 4 else k for i, k in enumerate(keep)]
+        _check_fork(held, table, parents, keep, ring, span, 16, N)
+
+
 @pytest.mark.parametrize("R,rows", [(2500, 3), (3, 2500)])
 def test_fork_of_many_rows_and_long_ones(R, rows):
     """More rows than a pass of the CTA that settles them, rows of more columns than a CTA takes,
@@ -123,6 +140,16 @@ def test_compact(seed, B, N):
     rng = np.random.RandomState(seed)
     held, table, ring, _ = _random_state(rng, B, 16, 5, N)
     _check_compact(held, table, ring, 16, N)
+
+
+@pytest.mark.parametrize("B,blocks,N", [(64, 30, 256), (64, 34, 256), (200, 50, 1024),
+                                        (40, 100, 65536), (40, 100, 65537), (300, 873, 1300),
+                                        (300, 875, 1300)])
+def test_compact_at_the_borders_of_its_forms(B, blocks, N):
+    for seed in range(3):
+        rng = np.random.RandomState(seed)
+        held, table, ring, _ = _random_state(rng, B, 16, blocks, N)
+        _check_compact(held, table, ring, 16, N)
 
 
 @pytest.mark.parametrize("N", [1, 2, 31, 32, 33, 64])
