@@ -870,7 +870,9 @@ kda_status_t kda_byte_cache_read(const kda_byte_cache_t* cache, int32_t io_dtype
  * are fp32.  A weight enters the product with v times 2^(e - E), e its block's
  * exponent and E the largest of the request's that the row's part has met, as one
  * fp16 for bf16 outputs (2^-11 of it, 2^-32 of the row's largest weight under E) and
- * as two for fp32 outputs (2^-22 and 2^-43).  Values of magnitude below 2^80.
+ * as two for fp32 outputs (2^-22 and 2^-43).  In prefill chunks (bf16, more than 48
+ * rows a kv head) keys and values enter as halves in units of 2^E instead, exact to
+ * 2^-24 of it.  Values of magnitude below 2^80.
  */
 kda_status_t kda_byte_cache_attention(const kda_byte_cache_t* cache, const kda_attention_t* desc,
                                   const void* q, const int32_t* block_table,

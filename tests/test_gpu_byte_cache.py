@@ -242,7 +242,8 @@ class Problem:
     """Requests over a cache of random pages; the bytes no request holds are random too, codes
     of NaN among them.  ``spread``: range of the blocks' powers of two."""
 
-    def __init__(self, kv, new, Hq, Hk, D, P, dtype, seed=0, extra_pages=2, qscale=1.5, spread=2):
+    def __init__(self, kv, new, Hq, Hk, D, P, dtype, seed=0, extra_pages=2, qscale=1.5, spread=2,
+                 k_spread=0):
         rng = np.random.RandomState(seed)
         self.kv, self.new, self.Hq, self.Hk, self.D, self.P = kv, new, Hq, Hk, D, P
         need = [-(-n // P) for n in kv]
@@ -257,6 +258,8 @@ class Problem:
             self.table[b, :need[b]] = ids[at:at + need[b]]
             at += need[b]
             k = rng.randn(n, Hk, D) * np.exp2(rng.randint(-2, 2, (Hk, D)))
+            if k_spread:
+                k *= np.repeat(np.exp2(rng.randint(-k_spread, 1, (n // 16 + 1, Hk, 1))), 16, 0)[:n]
             v = rng.randn(n, Hk, D)
             v *= np.repeat(np.exp2(rng.randint(-spread, spread + 1, (n // 16 + 1, Hk, 1))), 16, 0)[:n]
             if n:
@@ -352,6 +355,15 @@ def test_row_counts_at_the_kernels_borders(rows):
 def test_values_of_unequal_size(dtype, new, spread):
     """Blocks of V whose powers of two lie far apart, rising and falling along a request."""
     p = Problem([500, 77, 130], [new, new, 1], 4, 2, 128, 32, dtype, seed=new, spread=spread)
+    p.check(*p.call())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [1, 3, 60])
+@pytest.mark.parametrize("spread", [6, 40])
+def test_keys_of_unequal_size(dtype, new, spread):
+    """The same of K: scores of most blocks are small beside those of a few."""
+    p = Problem([500, 77, 130], [new, new, 1], 4, 2, 128, 32, dtype, seed=new, k_spread=spread)
     p.check(*p.call())
 
 
@@ -577,6 +589,47 @@ def test_expired_wait_reports_timeout_and_recovers(dtype, kv, new):
     assert kda.get_device_error() == 4
     for a, b in zip(base, p.call()):
         assert torch.equal(a, b)
+
+
+def test_calls_on_two_streams_at_once():
+    """Append, attention and read of two caches on a stream each, workspaces of their own."""
+    ps = [Problem([700, 90], [n, n], 8, 2, 128, 32, torch.bfloat16, seed=n) for n in (1, 60)]
+    base = [p.call() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, (p, st) in enumerate(zip(ps, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(p.call())
+    torch.cuda.synchronize()
+    for b, gs in zip(base, got):
+        for g in gs:
+            assert all(torch.equal(x, y) for x, y in zip(b, g))
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls, of another shape each, with one workspace, replayed in turn."""
+    ps = [Problem([700, 90], [n, n], 8, 2, 128, 32, torch.bfloat16, seed=n) for n in (1, 60)]
+    base = [p.call() for p in ps]
+    size = max(kda.byte_cache_attention_workspace_size(
+        p.cache, 2, p.q.shape[0], 8, max(p.new), p.table.shape[1], torch.bfloat16) for p in ps)
+    ws = torch.full((size,), 0xff, dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for p in ps:
+        args = [i32(x) for x in (p.table, p.kv, p.cu)]
+        g = torch.cuda.CUDAGraph()
+        out = torch.zeros_like(p.q)
+        with torch.cuda.graph(g):
+            kda.byte_cache_attention(p.q, p.cache, *args, max_new=max(p.new), out=out, workspace=ws)
+        graphs.append((g, args))
+        outs.append(out)
+    for _ in range(3):
+        for (g, _), out, b in zip(graphs, outs, base):
+            out.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, b[0])
 
 
 @pytest.mark.parametrize("D,new", [(64, 1), (128, 1), (128, 3)])

@@ -255,6 +255,42 @@ def test_graph_and_side_stream():
         assert np.array_equal(cache.cpu().numpy(), before)
 
 
+def test_graphs_that_share_a_workspace():
+    """A fork and a compaction captured with one workspace and replayed in turn, on a side stream."""
+    P, N = 16, 60
+    rng = np.random.RandomState(5)
+    held, table, ring, span = _random_state(rng, 7, P, 5, N)
+    parents = [0, 0, 1, 3, 3, 5, -1, 6]
+    keep = [held[p] if p >= 0 else 0 for p in parents]
+    ws = torch.full((max(kda.cache_fork_workspace_size(N, 8), kda.cache_compact_workspace_size(N)),),
+                    0xff, dtype=torch.uint8, device=DEV)
+    h, t, p, k, sp = i32(held), i32(table), i32(parents), i32(keep), _i64(span)
+    r1, r2 = i32(ring), i32(ring)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g1, stream=s):
+            a = kda.cache_fork(h, t, p, k, r1, sp, page_size=P, num_pages=N, workspace=ws)
+        with torch.cuda.graph(g2, stream=s):
+            b = kda.cache_compact(h, t, r2, page_size=P, num_pages=N, workspace=ws)
+    want_a = p8.fork(held, table, parents, keep, ring, span, P, N)
+    want_b = p8.compact(held, table, ring, P, N)
+    for _ in range(3):
+        for x in (*a, *b):
+            x.fill_(-7)
+        r1.copy_(i32(ring)), r2.copy_(i32(ring))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g1.replay()
+            g2.replay()
+        torch.cuda.synchronize()
+        for x, w in zip((*a, r1), want_a):
+            assert np.array_equal(x.cpu().numpy(), np.array(w))
+        for x, w in zip((*b, r2), want_b):
+            assert np.array_equal(x.cpu().numpy(), np.array(w))
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_a_server_forks_and_compacts(bits):
     """Prompts, several answers each, beams, ends and a compaction into fewer pages: after every
