@@ -49,11 +49,11 @@ __device__ __forceinline__ void fetch8(const T* p, uint32_t (&w)[2 * sizeof(T)])
   } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = __float_as_uint(IO<T>::ld(p + 2 * i)) >> 16 |
-             __float_as_uint(IO<T>::ld(p + 2 * i + 1));
+      w[i] = reinterpret_cast<const uint16_t*>(p)[2 * i] |
+             (uint32_t)reinterpret_cast<const uint16_t*>(p)[2 * i + 1] << 16;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(IO<T>::ld(p + i));
+    for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
   }
 }
 
@@ -210,8 +210,7 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
 // `share` warps: a prompt's window has one or two runs, a decode step's sixteen.
 template <typename T, int D, bool VEC, bool V>
 __device__ __forceinline__ void append_window(const View& c, int tokens, int share,
-                                              const Source& src,
-                                              const int64_t* __restrict__ slots, int* err) {
+                                              const Source& src, const int64_t* slots, int* err) {
   const int lane = threadIdx.x & 31;
   const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (host: 32 bits)
   const uint32_t window = unit / (uint32_t)share;
@@ -223,7 +222,7 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
   // lane l: the slot of token start - 1 + l, as far as a run of the window may reach
   const int64_t token = start - 1 + lane;
   int64_t slot = -1;
-  if (token >= 0 && token < tokens) slot = __ldg(slots + token);
+  if (token >= 0 && token < tokens) slot = slots[token];
   // Values are asked for before the slots say which they are.  Many warps to a window: the token
   // that is this warp's if each is a run of its own; else all of the window's, into L2.
   uint32_t first[2 * sizeof(T)] = {};
@@ -280,7 +279,8 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 4)
     append_kernel(View c, int tokens, int share, Source k, Source v,
-                  const int64_t* __restrict__ slots, int* err) {
+                  const int64_t* slots, int* err) {
+  wait_for_previous();
   if (blockIdx.y)
     append_window<T, D, VEC, true>(c, tokens, share, v, slots, err);
   else
@@ -308,14 +308,14 @@ __device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
 // A thread takes 16 channels of a token and every so many heads, of K or V.
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads<T>)
-    read_kernel(View c, int tokens, const int64_t* __restrict__ slots, T* __restrict__ k,
-                T* __restrict__ v, int* err) {
+    read_kernel(View c, int tokens, const int64_t* slots, T* k, T* v, int* err) {
+  wait_for_previous();
   constexpr int PIECES = D / 16;
   const int piece = threadIdx.x % PIECES;
   const int first = threadIdx.x / (8 * PIECES), step = blockDim.x / (8 * PIECES);
   const int64_t token = (int64_t)blockIdx.x * 8 + threadIdx.x / PIECES % 8;
   if (token >= tokens) return;
-  const int64_t slot = __ldg(slots + token);
+  const int64_t slot = slots[token];
   const bool there = slot >= 0 && slot < (int64_t)c.num_pages * c.page_size;
   if (!there && slot != -1) report_error(err, kErrDeviceCheck);
   const bool is_v = blockIdx.y;
@@ -374,9 +374,8 @@ cudaError_t append(const CacheArgs& a, cudaStream_t st) {
   const int64_t ctas = (windows * share * 32 + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidConfiguration;
   auto* kernel = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
-  kernel<<<dim3((unsigned)ctas, 2), kThreads, 0, st>>>(a.view, a.tokens, (int)share, k, v, a.slots,
-                                                       a.err);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3((unsigned)ctas, 2), kThreads, 0, st, a.view, a.tokens, (int)share,
+                      k, v, a.slots, a.err);
 }
 
 template <typename T, int D>
@@ -384,10 +383,8 @@ cudaError_t read(const CacheArgs& a, cudaStream_t st) {
   const dim3 grid((unsigned)((a.tokens + 7ll) / 8), 2);
   const int per_head = 8 * (D / 16);
   const int threads = per_head * std::min(a.view.kv_heads, kReadThreads<T> / per_head);
-  read_kernel<T, D><<<grid, threads, 0, st>>>(a.view, a.tokens, a.slots,
-                                              static_cast<T*>(a.k_out), static_cast<T*>(a.v_out),
-                                              a.err);
-  return cudaGetLastError();
+  return launch_after(read_kernel<T, D>, grid, threads, 0, st, a.view, a.tokens, a.slots,
+                      static_cast<T*>(a.k_out), static_cast<T*>(a.v_out), a.err);
 }
 
 }  // namespace

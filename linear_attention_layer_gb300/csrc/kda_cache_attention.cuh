@@ -59,13 +59,24 @@ struct Request {
   int64_t rows;  // per kv head; 0: not of this launch
 };
 
+// What a kernel ahead may still be writing when this one's CTAs start (launch_after) is not read by
+// the path for data that does not change while a kernel runs.
+template <bool AFTER, typename T>
+__device__ __forceinline__ T fetch(const T* p) {
+  if constexpr (AFTER)
+    return *p;
+  else
+    return __ldg(p);
+}
+
+template <bool AFTER = false>
 __device__ __forceinline__ bool load_request(const View& c, const AttentionArgs& a, int b,
                                              const RowRange& range, bool report, Request& r) {
   int eos;
   // a decreasing offset takes both of its neighbours out: their tokens may overlap others'
   const bool ok = seq_range(a.cu_new, b, a.total_tokens, report ? a.err : nullptr, r.bos, eos) &&
-                  (b == 0 || __ldg(a.cu_new + b - 1) <= r.bos);
-  r.kv = __ldg(a.kv_lens + b);
+                  (b == 0 || fetch<AFTER>(a.cu_new + b - 1) <= r.bos);
+  r.kv = fetch<AFTER>(a.kv_lens + b);
   r.rows = 0;
   r.n = 0;
   if (!ok) return false;
@@ -202,15 +213,6 @@ struct OpenUnit {
   int last;
 };
 
-// Programmatic dependent launch: a kernel lets the next one's CTAs start, which wait here
-// until the memory of the one before is complete.
-__device__ __forceinline__ void let_next_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Joins open units: a CTA has PER rows of one, WPR warps a row.
 template <typename T, int D, int PER, int WPR>
 __global__ void __launch_bounds__(32 * PER * WPR)
@@ -262,16 +264,8 @@ template <typename T, int D, int PER, int WPR>
 cudaError_t launch_join(const View& c, const AttentionArgs& a, const OpenUnit* units,
                         const float* o, const float2* ml, int slot0, int unit_rows, int ctas,
                         cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, unit_rows / PER);
-  cfg.blockDim = dim3(32 * PER * WPR);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, PER, WPR>, c, a, units, o, ml, slot0, unit_rows);
+  return launch_after(join_kernel<T, D, PER, WPR>, dim3(ctas, unit_rows / PER), 32 * PER * WPR, 0, st,
+                      c, a, units, o, ml, slot0, unit_rows);
 }
 
 inline int sm_count() {

@@ -19,23 +19,20 @@
 // alone 37, all of it).
 #include <algorithm>
 
-#include "kda_common.cuh"
+#include "kda_cache.cuh"
 #include "kda_launch.h"
 
 namespace kda {
 namespace {
+
+using cache::launch_after;
+using cache::wait_for_previous;
 
 constexpr int kThreads = 1024;  // of the CTA that sums
 constexpr int kBatch = 4;       // entries of a table that a thread has under way
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int page) {
   return (int)((tokens + page - 1) / page);
-}
-
-// Programmatic dependent launch: the kernels of a call wait here for the memory of the one
-// before.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // All CTAs of the cluster, and their memory.
@@ -335,6 +332,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(ForkArgs a, int32_t* fir
   const ForkScratch s{maps[0], maps[1], maps[2], first, rows};
   const bool lead = blockIdx.x == 0;
   const Crew alone{0, 1};
+  wait_for_previous();
   const FreeRing ring = load_ring(a, lead);
   check_rows(a.held_lens, a.old_seqs, a.max_blocks, a.page_size, a.err);
   fork_rows(a, s, words, alone, lead);
@@ -504,6 +502,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, int wo
   __shared__ int before[kMapWords], warp_sums[32], before_l, count;
   const CompactScratch s{CTAS == 1 ? mine : live, before, &count};
   const bool lead = blockIdx.x == 0;
+  wait_for_previous();
   compact_clear(a, mine, words, Crew{0, 1});
   __syncthreads();
   compact_mark(a, mine, grid_crew());
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(256, 4) copy_kernel(CopyArgs a, Layers layers,
     if (item < items) {
       const uint64_t i = item / per_copy;
       const int32_t* copy = a.copies + 3 * i;
-      const int from = __ldg(copy), to = __ldg(copy + 1), tokens = __ldg(copy + 2);
+      const int from = copy[0], to = copy[1], tokens = copy[2];
       if (from != -1 && tokens != 0 && from != to) {
         if (from >= 0 && from < a.num_pages && to >= 0 && to < a.num_pages && tokens > 0 &&
             tokens <= a.groups * 16)
@@ -625,21 +624,6 @@ int sm_count() {
   return sms;
 }
 
-// Launches a kernel that may start before the one ahead of it in the stream has ended.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Entries of tables that one CTA takes, and that one cluster does (pages and rows as far as its
 // shared memory has room).  Compactions of 600 entries took 8.6 us with one CTA, 10.3 with the
 // cluster, 13.7 as four kernels; of 5200 15.1, 12.4 and 14.9.  A fork of 35000 entries took 12.5 us
@@ -651,20 +635,19 @@ constexpr int kClusterPages = 32 * kMapWords;
 template <typename... P, typename... A>
 cudaError_t launch_steps(bool one, void (*one_kernel)(P...), void (*kernel)(P...), cudaStream_t st,
                          A... args) {
-  if (one) {
-    one_kernel<<<1, kThreads, 0, st>>>(args...);
-    return cudaGetLastError();
-  }
+  if (one) return launch_after(one_kernel, dim3(1), kThreads, 0, st, args...);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -726,9 +709,9 @@ cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t st) {
       a, s, words);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(fork_mark_kernel, dim3(entry_ctas(rows * a.max_blocks, most)), 256, st, a, s);
+  e = launch_after(fork_mark_kernel, dim3(entry_ctas(rows * a.max_blocks, most)), 256, 0, st, a, s);
   if (e != cudaSuccess) return e;
-  return launch_after(fork_settle_kernel, dim3(1), kThreads, st, a, s, words);
+  return launch_after(fork_settle_kernel, dim3(1), kThreads, 0, st, a, s, words);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
@@ -745,11 +728,11 @@ cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 ctas(entry_ctas((int64_t)a.num_seqs * a.max_blocks, most));
-  e = launch_after(compact_mark_kernel, ctas, 256, st, a, s);
+  e = launch_after(compact_mark_kernel, ctas, 256, 0, st, a, s);
   if (e != cudaSuccess) return e;
-  e = launch_after(compact_plan_kernel, dim3(1), kThreads, st, a, s, words);
+  e = launch_after(compact_plan_kernel, dim3(1), kThreads, 0, st, a, s, words);
   if (e != cudaSuccess) return e;
-  return launch_after(compact_rows_kernel, ctas, 256, st, a, s);
+  return launch_after(compact_rows_kernel, ctas, 256, 0, st, a, s);
 }
 
 cudaError_t launch_cache_copy(const CopyArgs& a, uint8_t* const* pages, cudaStream_t st) {
@@ -764,7 +747,7 @@ cudaError_t launch_cache_copy(const CopyArgs& a, uint8_t* const* pages, cudaStre
     const int64_t items = (int64_t)b.num_copies * b.num_layers * parts;
     const cudaError_t e =
         launch_after(copy_kernel, dim3((unsigned)std::min<int64_t>(items, 4ll * sm_count())), 256,
-                     st, b, layers, parts, part_vecs);
+                     0, st, b, layers, parts, part_vecs);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -47,6 +47,7 @@ __device__ __forceinline__ int tiles_of(const Request& r) {
 }
 
 // A place in the sequence of all tiles.
+template <bool AFTER>
 struct Cursor {
   int b;  // request (relative to the launch)
   int h;  // kv head
@@ -58,7 +59,7 @@ struct Cursor {
 
   __device__ __forceinline__ bool load(const View& c, const AttentionArgs& a, int seq0,
                                        const RowRange& range, int rows_per_tile) {
-    const bool live = load_request(c, a, seq0 + b, range, false, q);
+    const bool live = load_request<AFTER>(c, a, seq0 + b, range, false, q);
     tiles = tiles_of(q);
     rt = (int)((q.rows + rows_per_tile - 1) / rows_per_tile);
     return live;
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   constexpr int KM = D / 16;      // products along the channels of K, and 16-channel tiles of V
   constexpr int VC = D / 8;       // channels of V per lane
   constexpr bool QREG = !S::kQueriesHere;
+  constexpr bool AFTER = BITS == 8;  // launched after
   // A lane's words of a key that are loaded at a time (a word is two products with 4 bits, one
   // with 8), loads of a key, and words of a value.
   constexpr int KW = BITS == 4 ? D / 32 : 4, KLOADS = BITS == 4 ? 1 : D / 64;
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   const int group = a.num_heads / c.kv_heads;
   const int GP = c.page_size / kGroup;
 
+  if constexpr (AFTER) wait_for_previous();
   // ---- the plan: tiles before each request ----
   if (tid <= WARPS) sm.job[tid].rows = 0;
   if (lane == 0) {
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
       const int b = b0 + i;
       if (b >= nseq) break;
       Request r;
-      const bool live = load_request(c, a, seq0 + b, range, blockIdx.x == 0, r);
+      const bool live = load_request<AFTER>(c, a, seq0 + b, range, blockIdx.x == 0, r);
       sm.plan[b] = mine;
       if (live)
         mine += (unsigned long long)((r.rows + ROWS - 1) / ROWS) * tiles_of(r) * c.kv_heads;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
   const Shape shape{(int)gridDim.x, WARPS};
 
   if (x0 < x1) {
-    Cursor ld, cp;
+    Cursor<AFTER> ld, cp;
     cp.seek(c, a, seq0, nseq, range, ROWS, sm.plan, x0);
     ld = cp;
     auto open_job = [&](int i, unsigned long long end) {
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
       const int gi = (ld.tile * kTileGroups & ~31) + lane;
       const bool in = gi < (ld.q.kv + kGroup - 1) / kGroup;
       const int page =
-          in ? __ldg(a.block_table + (int64_t)(seq0 + ld.b) * a.max_blocks + gi / GP) : 0;
+          in ? fetch<AFTER>(a.block_table + (int64_t)(seq0 + ld.b) * a.max_blocks + gi / GP) : 0;
       const bool sound = page >= 0 && page < c.num_pages;
       if (in && !sound) report_error(a.err, kErrDeviceCheck);
       src = c.pages + (((int64_t)page * c.kv_heads + ld.h) * GP + gi % GP) * L::kGroupBytes;
@@ -288,18 +291,20 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS)
         } else if (q_vec) {
 #pragma unroll
           for (int i = 0; i < QC * (int)sizeof(T) / 16; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const uint4 u = fetch<AFTER>(reinterpret_cast<const uint4*>(p) + i);
             raw_q[n][4 * i] = u.x, raw_q[n][4 * i + 1] = u.y;
             raw_q[n][4 * i + 2] = u.z, raw_q[n][4 * i + 3] = u.w;
           }
         } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-          for (int i = 0; i < QC; ++i) raw_q[n][i] = __float_as_uint(IO<T>::ld(p + i));
+          for (int i = 0; i < QC; ++i)
+            raw_q[n][i] = fetch<AFTER>(reinterpret_cast<const uint32_t*>(p) + i);
         } else {
 #pragma unroll
           for (int i = 0; i < QC / 2; ++i)
-            raw_q[n][i] = __float_as_uint(IO<T>::ld(p + 2 * i)) >> 16 |
-                          __float_as_uint(IO<T>::ld(p + 2 * i + 1));
+            raw_q[n][i] = fetch<AFTER>(reinterpret_cast<const uint16_t*>(p) + 2 * i) |
+                          (uint32_t)fetch<AFTER>(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1)
+                              << 16;
         }
       }
     };
@@ -916,8 +921,14 @@ struct Split {
                       a.q_token_stride * es % 16 == 0 && a.q_head_stride * es % 16 == 0;
     for (int64_t seq0 = 0; seq0 < a.num_seqs; seq0 += kMaxSeqs) {
       const int nseq = (int)std::min<int64_t>(kMaxSeqs, a.num_seqs - seq0);
-      kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, (int)seq0, nseq, range, parts, q_vec);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if constexpr (BITS == 8) {
+        e = launch_after(kernel, dim3(sh.ctas), WARPS * 32, sizeof(S), st, c, a, (int)seq0, nseq,
+                         range, parts, q_vec);
+      } else {
+        kernel<<<sh.ctas, WARPS * 32, sizeof(S), st>>>(c, a, (int)seq0, nseq, range, parts, q_vec);
+        e = cudaGetLastError();
+      }
+      if (e != cudaSuccess) return e;
       e = launch_join<T, D, 1, 4>(c, a, parts.open, parts.o, parts.ml, sh.warp_slots(), ROWS, sh.ctas,
                                st);
       if (e != cudaSuccess) return e;
