@@ -26,7 +26,7 @@ namespace {
 //               16 rows   8 x 4 x 1  158   4 x 3 x 3  172    8 x 2 x 2  214
 // Few units, fewer than half the SMs, are each cut over many CTAs, whose parts a second kernel joins:
 // one CTA of 8 warps leaves it a third of the parts that three of 4 do (one request
-// of 2048 tokens 13.2 us for 14.6, of 131072 on one kv head 22 for 33; 256 requests 349 for 335).
+// of 2048 tokens 11.5 us for 12.1, of 131072 on one kv head 20 for 31; 256 requests 349 for 335).
 template <typename F>
 auto dispatch(const View& c, const AttentionArgs& a, F&& f) {
   const bool few = (int64_t)a.max_new * (a.num_heads / c.kv_heads) <= 8;

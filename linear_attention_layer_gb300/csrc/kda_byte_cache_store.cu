@@ -13,8 +13,8 @@
 // loads under way: 28 a SM of 72 registers (140 registers left 8: 672 us for the prompts below).
 //
 // Measured (GB300; bf16, heads of 128, 8 of them): prompts of 270336 tokens, 1.66 GB, appended in
-// 297 us (0.82 of the measured HBM rate), read back in 256 us (0.96); 8000 tokens 11 us; a decode
-// step of 256 tokens 6.5 us.
+// 296 us (0.83 of the measured HBM rate), read back in 256 us (0.96); 8000 tokens 9.3 us; a decode
+// step of 256 tokens 4.6 us.
 #include <algorithm>
 
 #include "kda_byte_cache.cuh"

@@ -13,10 +13,10 @@
 // shared memory and barriers between the steps, or, for large tables, as a kernel each over the
 // whole GPU.  The copies are bound by HBM.
 //
-// Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 9 us and its 7 copies 3 us; of
-// 256 beams over 4096 tokens at most 12.5 us and 73 copies in two caches 7 us; a compaction of 4096
-// pages 12.5 us and its 930 moves of 128 KB 41 us, 0.88 of the measured HBM rate (in the kernel
-// alone 37, all of it).
+// Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 7 us and its 7 copies 2.5 us
+// (replayed; called, the host takes 7.5 and 3); of 256 beams over 4096 tokens at most 10.4 us and 73
+// copies in two caches 7 us; a compaction of 4096 pages 9.6 us and its 930 moves of 128 KB 41 us,
+// 0.89 of the measured HBM rate (in the kernel alone 37, 0.98).
 #include <algorithm>
 
 #include "kda_cache.cuh"
@@ -625,9 +625,9 @@ int sm_count() {
 }
 
 // Entries of tables that one CTA takes, and that one cluster does (pages and rows as far as its
-// shared memory has room).  Compactions of 600 entries took 8.6 us with one CTA, 10.3 with the
-// cluster, 13.7 as four kernels; of 5200 15.1, 12.4 and 14.9.  A fork of 35000 entries took 12.5 us
-// with the cluster, 15.5 as three kernels.
+// shared memory has room).  Before the launches overlapped compactions of 600 entries took 8.6 us
+// with one CTA, 10.3 with the cluster, 13.7 as four kernels; of 5200 15.1, 12.4 and 14.9; a fork of
+// 35000 entries 12.5 us with the cluster, 15.5 as three kernels.
 constexpr int64_t kOneEntries = 1 << 11, kClusterEntries = 1 << 18;
 constexpr int kClusterPages = 32 * kMapWords;
 
