@@ -846,7 +846,8 @@ typedef struct {
  *              rows load faster.
  *   slots      device, [num_tokens] int64, no slot twice; -1 skips a token.  The
  *              tokens of one block stand next to one another in the batch, in any
- *              order (kda_cache_tables gives a request's in rising order)
+ *              order but with none between them, not even a skipped one (as
+ *              kda_cache_tables gives them)
  * A slot outside the cache is skipped and sets the device error word.  An
  * infinity does not count for the exponent and is stored as the block's largest
  * value of its sign, a NaN as zero; either sets the error word.

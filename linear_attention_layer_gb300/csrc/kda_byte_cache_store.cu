@@ -152,7 +152,8 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
                            : max(kLeastExponent, min((int)*exp_at - kExponentBias, kMostExponent));
   uint32_t top = 0;
 #pragma unroll
-  for (int s = 0; s < W::STEPS; ++s) top = max(top, top8<T>(w[s]));
+  for (int s = 0; s < W::STEPS; ++s)
+    if (s == 0 || s * W::AT_ONCE < n) top = max(top, top8<T>(w[s]));
   top = __reduce_max_sync(0xffffffffu, top);
   const bool odd = top >= 0x7f800000u;  // infinities do not count, NaN becomes zero
   if (odd) {
@@ -192,6 +193,7 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
   const float down = __int_as_float((127 - e) << 23);
 #pragma unroll
   for (int s = 0; s < W::STEPS; ++s) {
+    if (s > 0 && s * W::AT_ONCE >= n) break;  // all lanes: a decode step's run is one token
     const int i = __shfl_sync(0xffffffffu, place, (s * W::AT_ONCE + at.t) & 31);
     if (s * W::AT_ONCE + at.t < n) {
       uint32_t b[4];

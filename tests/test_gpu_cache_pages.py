@@ -255,6 +255,49 @@ def test_graph_and_side_stream():
         assert np.array_equal(cache.cpu().numpy(), before)
 
 
+@pytest.mark.parametrize("where", ["first", "after a memset", "after another stream",
+                                   "on another stream"])
+def test_copy_captured_behind_anything(where):
+    """The copies' kernel may start before what is ahead of it has ended: as a graph's first node,
+    behind a memset or kernels of its own stream and of another one it still waits for them."""
+    caches = [torch.randint(0, 256, (8, 2, 2, 2064), dtype=torch.uint8, device=DEV)
+              for _ in range(2)]
+    copies, room = i32([[0, 5, 32], [1, 6, 17]]), torch.zeros(1 << 22, device=DEV)
+    given = copies.clone()
+    side = torch.cuda.Stream()
+    kda.cache_copy(caches, copies)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cur = torch.cuda.current_stream()
+        if where == "after a memset":
+            copies.zero_()
+            copies.copy_(given)
+            room.zero_()
+        elif where == "after another stream":
+            side.wait_stream(cur)
+            with torch.cuda.stream(side):
+                copies.zero_()
+                for _ in range(20):
+                    room.add_(1)
+                copies.copy_(given)
+            cur.wait_stream(side)
+        if where == "on another stream":
+            side.wait_stream(cur)
+            kda.cache_copy(caches, copies, stream=side)
+            cur.wait_stream(side)
+        else:
+            kda.cache_copy(caches, copies)
+    for _ in range(3):
+        for c in caches:
+            c[5:].zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for c in caches:
+            assert torch.equal(c[5], c[0]) and torch.equal(c[6], c[1]) and not c[7].any()
+
+
 def test_graphs_that_share_a_workspace():
     """A fork and a compaction captured with one workspace and replayed in turn, on a side stream."""
     P, N = 16, 60
