@@ -13,8 +13,8 @@
 // loads under way: 28 a SM of 72 registers (140 registers left 8: 672 us for the prompts below).
 //
 // Measured (GB300; bf16, heads of 128, 8 of them): prompts of 270336 tokens, 1.66 GB, appended in
-// 296 us (0.83 of the measured HBM rate), read back in 256 us (0.96); 8000 tokens 9.3 us; a decode
-// step of 256 tokens 4.6 us.
+// 297 us (0.82 of the measured HBM rate), read back in 256 us (0.96); 8000 tokens 9.4 us; a decode
+// step of 256 tokens 3.9 us, of 4096 26 us.
 #include <algorithm>
 
 #include "kda_byte_cache.cuh"
@@ -120,8 +120,11 @@ struct Lanes {
 
 // A run of n tokens of the batch, which fill places of one block; lane k < n has the place of
 // the k-th of them.  p: the lane's channels of its first token, whose values (those of the next as
-// well, where a step takes two or four) are in `first` if `have`.  All lanes of the warp.
-template <typename T, int D, bool VEC, bool V>
+// well, where a step takes two or four) are in `first` if `have`.  SHORT: runs of one step go a way of
+// their own, which saves decode steps of thousands a quarter and costs prompts 2% -- but for fp32
+// with 128 channels, where the compiler then finds room for what it spills otherwise (100000 tokens
+// 163 us for 183).  All lanes of the warp.
+template <typename T, int D, bool VEC, bool V, bool SHORT>
 __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token_stride, int n,
                                            int place, const uint32_t (&first)[2 * sizeof(T)],
                                            bool have, bool& not_finite) {
@@ -150,10 +153,12 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
   // (a byte that append did not write is held to the range of those it does)
   const int before = fresh ? kLeastExponent
                            : max(kLeastExponent, min((int)*exp_at - kExponentBias, kMostExponent));
-  uint32_t top = 0;
+  const bool one_step = SHORT && n <= W::AT_ONCE;  // all lanes
+  uint32_t top = top8<T>(w[0]);
+  if (!one_step) {
 #pragma unroll
-  for (int s = 0; s < W::STEPS; ++s)
-    if (s == 0 || s * W::AT_ONCE < n) top = max(top, top8<T>(w[s]));
+    for (int s = 1; s < W::STEPS; ++s) top = max(top, top8<T>(w[s]));
+  }
   top = __reduce_max_sync(0xffffffffu, top);
   const bool odd = top >= 0x7f800000u;  // infinities do not count, NaN becomes zero
   if (odd) {
@@ -191,9 +196,7 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
     }
   }
   const float down = __int_as_float((127 - e) << 23);
-#pragma unroll
-  for (int s = 0; s < W::STEPS; ++s) {
-    if (s > 0 && s * W::AT_ONCE >= n) break;  // all lanes: a decode step's run is one token
+  auto put = [&](int s) {
     const int i = __shfl_sync(0xffffffffu, place, (s * W::AT_ONCE + at.t) & 31);
     if (s * W::AT_ONCE + at.t < n) {
       uint32_t b[4];
@@ -204,13 +207,18 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
       if (odd) codes = make_uint2(without_nan(codes.x), without_nan(codes.y));
       *reinterpret_cast<uint2*>(group + place8<D, V>(i, at.c)) = codes;
     }
+  };
+  put(0);
+  if (!one_step) {
+#pragma unroll
+    for (int s = 1; s < W::STEPS; ++s) put(s);
   }
   if (lane == 0) *exp_at = (uint8_t)(e + kExponentBias);
 }
 
 // The runs that start among 16 tokens of the batch, a window, are dealt out with the heads to
 // `share` warps: a prompt's window has one or two runs, a decode step's sixteen.
-template <typename T, int D, bool VEC, bool V>
+template <typename T, int D, bool VEC, bool V, bool ALONE>
 __device__ __forceinline__ void append_window(const View& c, int tokens, int share,
                                               const Source& src, const int64_t* slots, int* err) {
   const int lane = threadIdx.x & 31;
@@ -228,9 +236,8 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
   // Values are asked for before the slots say which they are.  Many warps to a window: the token
   // that is this warp's if each is a run of its own; else all of the window's, into L2.
   uint32_t first[2 * sizeof(T)] = {};
-  const bool alone = share > c.kv_heads;
   const int guess = (uint32_t)mine / (uint32_t)c.kv_heads;
-  if (alone) {
+  if constexpr (ALONE) {
     if (start + guess + at.t < tokens)
       fetch8<T, VEC>(base + (start + guess + at.t) * src.token_stride +
                          (int64_t)(mine - guess * c.kv_heads) * src.head_stride + at.c,
@@ -269,24 +276,24 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
     uint8_t* group =
         c.pages + (((int64_t)page * c.kv_heads + head) * groups + (b - page * groups)) *
                       Layout8<D>::kGroupBytes;
-    append_run<T, D, VEC, V>(group,
-                             base + (start + l - 1 + at.t) * src.token_stride +
-                                 (int64_t)head * src.head_stride + at.c,
-                             src.token_stride, n, place, first,
-                             alone && task == mine && l - 1 == guess, not_finite);
+    const T* from = base + (start + l - 1 + at.t) * src.token_stride +
+                    (int64_t)head * src.head_stride + at.c;
+    append_run<T, D, VEC, V, ALONE || (sizeof(T) == 4 && D == 128)>(
+        group, from, src.token_stride, n, place, first, ALONE && task == mine && l - 1 == guess,
+        not_finite);
   }
   if (not_finite && lane == 0) report_error(err, kErrDeviceCheck);
 }
 
-template <typename T, int D, bool VEC>
+template <typename T, int D, bool VEC, bool ALONE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 4)
     append_kernel(View c, int tokens, int share, Source k, Source v,
                   const int64_t* slots, int* err) {
   wait_for_previous();
   if (blockIdx.y)
-    append_window<T, D, VEC, true>(c, tokens, share, v, slots, err);
+    append_window<T, D, VEC, true, ALONE>(c, tokens, share, v, slots, err);
   else
-    append_window<T, D, VEC, false>(c, tokens, share, k, slots, err);
+    append_window<T, D, VEC, false, ALONE>(c, tokens, share, k, slots, err);
 }
 
 template <typename T>
@@ -375,7 +382,9 @@ cudaError_t append(const CacheArgs& a, cudaStream_t st) {
   const int64_t share = std::max(heads, std::min(kGroup * heads, kWarps / 2 / windows));
   const int64_t ctas = (windows * share * 32 + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidConfiguration;
-  auto* kernel = vec ? append_kernel<T, D, true> : append_kernel<T, D, false>;
+  const bool few = share > heads;
+  auto* kernel = vec ? (few ? append_kernel<T, D, true, true> : append_kernel<T, D, true, false>)
+                     : (few ? append_kernel<T, D, false, true> : append_kernel<T, D, false, false>);
   return launch_after(kernel, dim3((unsigned)ctas, 2), kThreads, 0, st, a.view, a.tokens, (int)share,
                       k, v, a.slots, a.err);
 }
