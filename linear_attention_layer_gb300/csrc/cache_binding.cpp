@@ -430,6 +430,33 @@ PyObject* attention8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Small outputs out of one allocation, which costs the host most of a microsecond each: the
+// caller's where it gave one, else a piece of `room`, made large enough for all that follow.
+struct Pieces {
+  c10::Device dev;
+  size_t bytes;  // of all pieces, each rounded up to 16
+  Tensor room;
+  size_t used = 0;
+  template <typename P>
+  P* output(PyObject* o, const char* name, ScalarType type, IntArrayRef shape, Tensor& keep) {
+    if (o != Py_None) {
+      need<P>(o, name, type, shape, dev);
+      keep = THPVariable_Unpack(o);
+      return static_cast<P*>(keep.data_ptr());
+    }
+    if (!room.defined()) {
+      const int64_t size[] = {(int64_t)bytes};
+      room = at::detail::empty_cuda(size, ScalarType::Byte, dev, std::nullopt);
+    }
+    keep = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(room.storage()), room.key_set(),
+                                                    c10::scalarTypeToTypeMeta(type));
+    keep.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    keep.unsafeGetTensorImpl()->set_storage_offset((int64_t)(used / sizeof(P)));
+    used += ((size_t)keep.numel() * sizeof(P) + 15) / 16 * 16;
+    return static_cast<P*>(keep.data_ptr());
+  }
+};
+
 // held_lens, block_table, parents, keep_lens, free_pages, free_range, page_size, num_pages,
 // kv_lens, block_table_out, copies, free_range_out, workspace (None: allocated here)
 PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -459,10 +486,11 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   kda_status_t st = kda_cache_fork_workspace_size((int32_t)pages, (int32_t)R, &bytes);
   if (st != KDA_OK) return status_object(st);
   Tensor kv, out, copies, span, ws;
-  int32_t* kv_p = output<int32_t>(a[8], "kv_lens", I, lens, dev, kv);
+  Pieces pieces{dev, (size_t)(16 * R + 64), {}};
+  int64_t* span_out = pieces.output<int64_t>(a[11], "free_range_out", L, two, span);
+  int32_t* kv_p = pieces.output<int32_t>(a[8], "kv_lens", I, lens, kv);
+  int32_t* copies_p = pieces.output<int32_t>(a[10], "copies", I, three, copies);
   int32_t* out_p = output<int32_t>(a[9], "block_table_out", I, out_shape, dev, out);
-  int32_t* copies_p = output<int32_t>(a[10], "copies", I, three, dev, copies);
-  int64_t* span_out = output<int64_t>(a[11], "free_range_out", L, two, dev, span);
   void* ws_p = scratch(a[12], bytes, dev, ws, have);
   st = kda_cache_fork((int32_t)page_size, (int32_t)pages, (int32_t)B, (int32_t)R, (int32_t)blocks,
                       (int32_t)cap, held_p, table_p, parents_p, keep_p, ring_p, span_p, span_out,
@@ -498,9 +526,10 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   kda_status_t st = kda_cache_compact_workspace_size((int32_t)pages, &bytes);
   if (st != KDA_OK) return status_object(st);
   Tensor out, copies, span, ws;
+  Pieces pieces{dev, (size_t)(12 * moves[0] + 48), {}};
+  int64_t* span_p = pieces.output<int64_t>(a[7], "free_range_out", L, two, span);
+  int32_t* copies_p = pieces.output<int32_t>(a[6], "copies", I, moves, copies);
   int32_t* out_p = output<int32_t>(a[5], "block_table_out", I, table_shape, dev, out);
-  int32_t* copies_p = output<int32_t>(a[6], "copies", I, moves, dev, copies);
-  int64_t* span_p = output<int64_t>(a[7], "free_range_out", L, two, dev, span);
   void* ws_p = scratch(a[8], bytes, dev, ws, have);
   st = kda_cache_compact((int32_t)page_size, (int32_t)pages, (int32_t)B, (int32_t)blocks,
                          (int32_t)cap, held_p, table_p, out_p, copies_p, ring_p, span_p, ws_p,

@@ -14,7 +14,7 @@
 // whole GPU.  The copies are bound by HBM.
 //
 // Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 7 us and its 7 copies 2.5 us
-// (replayed; called, the host takes 7.5 and 3); of 256 beams over 4096 tokens at most 10.4 us and 73
+// (the host takes 6 and 3); of 256 beams over 4096 tokens at most 10.4 us and 73
 // copies in two caches 7 us; a compaction of 4096 pages 9.6 us and its 930 moves of 128 KB 41 us,
 // 0.89 of the measured HBM rate (in the kernel alone 37, 0.98).
 #include <algorithm>
