@@ -1110,8 +1110,9 @@ def byte_cache_append(k, v, slots, cache, *, stream=None):
     """``kda_byte_cache_append``: quantise k, v [T, kv heads, head_dim] (fp32 or bf16;
     slices of a larger tensor will do, the channels contiguous) into ``cache`` at
     ``slots`` int64 [T] (-1 skips a token).  Tokens of the same 16 slots stand next
-    to one another, as ``cache_tables`` gives them; one that raises its block's
-    exponent takes the codes along that the block holds."""
+    to one another, as ``cache_tables`` gives them (up to 16 tokens apart they are left out and
+    reported by ``get_device_error``); one that raises its block's exponent takes the codes
+    along that the block holds."""
     if stream is not None:
         with _on(stream, "cache", cache):
             return byte_cache_append(k, v, slots, cache)

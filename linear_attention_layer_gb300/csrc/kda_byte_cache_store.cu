@@ -120,14 +120,14 @@ struct Lanes {
 
 // A run of n tokens of the batch, which fill places of one block; lane k < n has the place of
 // the k-th of them.  p: the lane's channels of its first token, whose values (those of the next as
-// well, where a step takes two or four) are in `first` if `have`.  SHORT: runs of one step go a way of
-// their own, which saves decode steps of thousands a quarter and costs prompts 2% -- but for fp32
-// with 128 channels, where the compiler then finds room for what it spills otherwise (100000 tokens
-// 163 us for 183).  All lanes of the warp.
+// well, where a step takes two or four) are in `first` if `have`.  leave_out: nothing is written.
+// SHORT: runs of one step go a way of their own, which saves decode steps of thousands a quarter and
+// costs prompts 2% -- but for fp32 with 128 channels, where the compiler then finds room for what it
+// spills otherwise (100000 tokens 163 us for 183).  All lanes of the warp.
 template <typename T, int D, bool VEC, bool V, bool SHORT>
 __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token_stride, int n,
                                            int place, const uint32_t (&first)[2 * sizeof(T)],
-                                           bool have, bool& not_finite) {
+                                           bool have, bool leave_out, bool& not_finite) {
   using W = Lanes<D>;
   const W at;
   const int lane = threadIdx.x & 31;
@@ -171,6 +171,7 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
     top = __reduce_max_sync(0xffffffffu, top);
   }
   const int e = max(exponent_of(top), before);
+  if (leave_out) return;  // asked only here, behind the loads
   if (!fresh && e > before) {
     // pieces of 8 codes, each of one token: 2 D of them, four of a lane asked for at once
     const uint32_t f = half_power(e - before);
@@ -216,12 +217,35 @@ __device__ __forceinline__ void append_run(uint8_t* group, const T* p, int token
   if (lane == 0) *exp_at = (uint8_t)(e + kExponentBias);
 }
 
-// The runs that start among 16 tokens of the batch, a window, are dealt out with the heads to
-// `share` warps: a prompt's window has one or two runs, a decode step's sixteen.
-template <typename T, int D, bool VEC, bool V, bool ALONE>
+// A run of a block that one of the 16 tokens before the run is of already is left out: two warps
+// would read and write that block's exponent and codes.  (A block that the batch comes back to
+// further on is not found out.)  `back`: lane l has the block of the window's token l - 16.
+//
+// Whether that is so of the run of block b that starts at the window's token i: a vote for each run.
+__device__ __forceinline__ bool second_run(int back, int b, int i) {
+  return (__ballot_sync(0xffffffffu, back == b) & 0xffffu << i) != 0;
+}
+// Bit i for each such token i: 16 shuffles a window (a match over the warp instead: a decode step of
+// 256 tokens 4.7 us for 4.4).  Where a warp has several short runs one after the other, the votes
+// cost more (4096 fp32 tokens 44 us for 34), elsewhere less (256 tokens 4.1 us).
+__device__ __forceinline__ uint32_t second_runs(int back) {
+  bool met = false;
+#pragma unroll
+  for (int d = 2; d <= kGroup; ++d) met |= __shfl_up_sync(0xffffffffu, back, d) == back;
+  const bool starts = __shfl_up_sync(0xffffffffu, back, 1) != back;
+  return __ballot_sync(0xffffffffu, met && starts && back >= 0) >> kGroup;
+}
+
+// How the runs that start among 16 tokens of the batch, a window, are dealt out with the heads to
+// `share` warps: a warp a head, what a prompt's one or two runs want; more warps; or one for each
+// head and token, what a small decode step wants.
+enum Deal { kByHead, kMore, kByToken };
+
+template <typename T, int D, bool VEC, bool V, Deal DEAL>
 __device__ __forceinline__ void append_window(const View& c, int tokens, int share,
                                               const Source& src, const int64_t* slots, int* err) {
   const int lane = threadIdx.x & 31;
+  constexpr bool ALONE = DEAL != kByHead;
   const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // (host: 32 bits)
   const uint32_t window = unit / (uint32_t)share;
   const int mine = (int)(unit - window * (uint32_t)share);
@@ -231,8 +255,10 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
   const T* base = static_cast<const T*>(src.p);
   // lane l: the slot of token start - 1 + l, as far as a run of the window may reach
   const int64_t token = start - 1 + lane;
-  int64_t slot = -1;
+  const int64_t token_back = token - (kGroup - 1);
+  int64_t slot = -1, slot_back = -1;
   if (token >= 0 && token < tokens) slot = slots[token];
+  if (token_back >= 0 && token_back < tokens) slot_back = slots[token_back];
   // Values are asked for before the slots say which they are.  Many warps to a window: the token
   // that is this warp's if each is a run of its own; else all of the window's, into L2.
   uint32_t first[2 * sizeof(T)] = {};
@@ -258,11 +284,15 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
   const int prev = __shfl_up_sync(0xffffffffu, block, 1);
   const bool goes_on = there && lane > 0 && prev == block;
   const uint32_t on = __ballot_sync(0xffffffffu, goes_on);
-  const bool starts_here = counts && there && !goes_on;
+  const bool there_back = slot_back >= 0 && slot_back < (int64_t)c.num_pages * c.page_size;
+  const int back = there_back ? (int)(slot_back / kGroup) : -1;
+  uint32_t second = 0;
+  if constexpr (DEAL == kMore) second = second_runs(back);
+  const bool starts_here = counts && there && !goes_on && !(second << 1 >> lane & 1);
   const uint32_t starts = __ballot_sync(0xffffffffu, starts_here);
   const int rank = __popc(starts & ((1u << lane) - 1));  // runs before the lane's
   const int tasks = __popc(starts) * c.kv_heads;
-  bool not_finite = false;
+  bool not_finite = false, met_again = second != 0;
   const int groups = c.page_size / kGroup;
   for (int task = mine; task < tasks; task += share) {
     const int run = task / c.kv_heads, head = task - run * c.kv_heads;
@@ -272,6 +302,8 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
     const int n = min(after ? __ffs(after) : 32, kGroup);
     const int place = __shfl_sync(0xffffffffu, (int)(slot & (kGroup - 1)), (l + lane) & 31);
     const int b = __shfl_sync(0xffffffffu, block, l);
+    const bool again = DEAL != kMore && second_run(back, b, l - 1);
+    met_again |= again;
     const int page = b / groups;
     uint8_t* group =
         c.pages + (((int64_t)page * c.kv_heads + head) * groups + (b - page * groups)) *
@@ -280,20 +312,20 @@ __device__ __forceinline__ void append_window(const View& c, int tokens, int sha
                     (int64_t)head * src.head_stride + at.c;
     append_run<T, D, VEC, V, ALONE || (sizeof(T) == 4 && D == 128)>(
         group, from, src.token_stride, n, place, first, ALONE && task == mine && l - 1 == guess,
-        not_finite);
+        again, not_finite);
   }
-  if (not_finite && lane == 0) report_error(err, kErrDeviceCheck);
+  if ((not_finite || met_again) && lane == 0) report_error(err, kErrDeviceCheck);
 }
 
-template <typename T, int D, bool VEC, bool ALONE>
+template <typename T, int D, bool VEC, Deal DEAL>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 4)
     append_kernel(View c, int tokens, int share, Source k, Source v,
                   const int64_t* slots, int* err) {
   wait_for_previous();
   if (blockIdx.y)
-    append_window<T, D, VEC, true, ALONE>(c, tokens, share, v, slots, err);
+    append_window<T, D, VEC, true, DEAL>(c, tokens, share, v, slots, err);
   else
-    append_window<T, D, VEC, false, ALONE>(c, tokens, share, k, slots, err);
+    append_window<T, D, VEC, false, DEAL>(c, tokens, share, k, slots, err);
 }
 
 template <typename T>
@@ -382,9 +414,14 @@ cudaError_t append(const CacheArgs& a, cudaStream_t st) {
   const int64_t share = std::max(heads, std::min(kGroup * heads, kWarps / 2 / windows));
   const int64_t ctas = (windows * share * 32 + kThreads - 1) / kThreads;
   if (ctas > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidConfiguration;
-  const bool few = share > heads;
-  auto* kernel = vec ? (few ? append_kernel<T, D, true, true> : append_kernel<T, D, true, false>)
-                     : (few ? append_kernel<T, D, false, true> : append_kernel<T, D, false, false>);
+  auto pick = [&](auto* by_head, auto* more, auto* by_token) {
+    return share == heads ? by_head : share < kGroup * heads ? more : by_token;
+  };
+  auto* kernel =
+      vec ? pick(append_kernel<T, D, true, kByHead>, append_kernel<T, D, true, kMore>,
+                 append_kernel<T, D, true, kByToken>)
+          : pick(append_kernel<T, D, false, kByHead>, append_kernel<T, D, false, kMore>,
+                 append_kernel<T, D, false, kByToken>);
   return launch_after(kernel, dim3((unsigned)ctas, 2), kThreads, 0, st, a.view, a.tokens, (int)share,
                       k, v, a.slots, a.err);
 }
