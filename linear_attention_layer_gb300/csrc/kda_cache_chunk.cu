@@ -55,11 +55,18 @@ constexpr int kRawStages = 4, kTileStages = 3;
 constexpr int kValidRing = 16;          // more tiles than can be under way
 // With 8 bits a block of rows has an issuing warp of its own, and the softmax's warps take registers
 // from the others (8 bits, the chunk above: 787 us with one issuer and 128 registers for all, 764;
-// 4 bits 744 and 756).  160 x 8 + 112 x 4 + 80 x 4 = the launch's 128 x 16.
+// 4 bits 744 and 756).
 template <int BITS>
 constexpr int kIssuers = BITS == 8 ? 2 : 1;
 template <int BITS>
 constexpr int kThreads = 32 * (BITS == 8 ? 16 : 14);
+constexpr int kSoftmaxRegs = 160, kDequantRegs = 112, kOtherRegs = 80;
+// Whether a launch with this many registers a thread has what the warps take: beyond that the
+// softmax's warps would wait without an end.
+constexpr bool registers_suffice(int a_thread) {
+  return 8 * kSoftmaxRegs + 4 * kDequantRegs + 4 * kOtherRegs <= kThreads<8> / 32 * a_thread;
+}
+static_assert(registers_suffice(128) && !registers_suffice(127), "the split is that of 128 a thread");
 template <int BITS, int REGS>
 __device__ __forceinline__ void take_registers() {
   if constexpr (BITS == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(kThreads<BITS>, 1)
   const int first_blk = kIssuers<BITS> == 2 ? (warp - 12) / 2 : 0;
   if (warp < 8) {
     // ------------------------------------------------------------ softmax ----
-    take_registers<BITS, 160>();
+    take_registers<BITS, kSoftmaxRegs>();
     const int blk = warp >> 2;
     const int row = tid & (kBlock - 1);
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(kThreads<BITS>, 1)
     }
   } else if (warp < 12) {
     // ----------------------------------------------------- dequantisation ----
-    leave_registers<BITS, 112>();
+    leave_registers<BITS, kDequantRegs>();
     const int dw = warp - 8;
     Ring<kRawStages> raw;
     Ring<kTileStages> st;
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(kThreads<BITS>, 1)
       }
     }
   } else {
-    leave_registers<BITS, 80>();
+    leave_registers<BITS, kOtherRegs>();
     if (issues) {
       // ------------------------------------------------------ matrix products ----
       constexpr int kMine = 2 / kIssuers<BITS>;  // blocks
@@ -886,6 +893,12 @@ cudaError_t run(const View& c, const AttentionArgs& a, const RowRange& range, cu
   constexpr int kSmem = (int)sizeof(Smem<BITS, D>) + 1024;
   static_assert(kSmem <= 227 * 1024, "more shared memory than a CTA has");
   cudaError_t e = init.run([&] {
+    if (BITS == 8) {  // the launch bounds are an upper limit only
+      cudaFuncAttributes f;
+      const cudaError_t err = cudaFuncGetAttributes(&f, chunk_kernel<BITS, D>);
+      if (err != cudaSuccess) return err;
+      if (!registers_suffice(f.numRegs)) return cudaErrorLaunchOutOfResources;
+    }
     return cudaFuncSetAttribute(chunk_kernel<BITS, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kSmem);
   });
