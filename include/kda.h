@@ -871,10 +871,11 @@ kda_status_t kda_byte_cache_read(const kda_byte_cache_t* cache, int32_t io_dtype
  * kda_byte_cache_attention -- kda_cache_attention over the 8-bit cache: the same
  * arguments, rows, masks, checks and outputs.  Scores, softmax statistics and sums
  * are fp32.  A weight enters the product with v times 2^(e - E), e its block's
- * exponent and E the largest of the request's that the row's part has met, as one
- * fp16 for bf16 outputs (2^-11 of it, 2^-32 of the row's largest weight under E) and
- * as two for fp32 outputs (2^-22 and 2^-43).  In prefill chunks (bf16, more than 48
- * rows a kv head) keys and values enter as halves in units of 2^E instead, exact to
+ * exponent and E the largest of the request's that the row's part has met -- in the
+ * blocks of its last tokens also one that this row does not see but a later one does
+ * -- as one fp16 for bf16 outputs (2^-11 of it, 2^-32 of the row's largest weight under
+ * E) and as two for fp32 outputs (2^-22 and 2^-43).  In prefill chunks (bf16, more than
+ * 48 rows a kv head) keys and values enter as halves in units of 2^E instead, exact to
  * 2^-24 of it.  Values of magnitude below 2^80.
  */
 kda_status_t kda_byte_cache_attention(const kda_byte_cache_t* cache, const kda_attention_t* desc,
