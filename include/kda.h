@@ -819,7 +819,10 @@ kda_status_t kda_cache_attention_workspace_size(const kda_cache_t* cache,
  * (larger ones saturate); it rises as tokens come in, and the codes that the block
  * holds are then taken along, e4m3(code 2^(e - e')), which changes a value only where
  * it runs into E4M3's smallest numbers (below 2^-6 2^e').  A token at a block's first
- * place begins it anew.
+ * place begins it anew.  Until then e does not fall: one that a rejected draft has
+ * raised stays for the tokens that follow in the block, and one appended to a block that
+ * none has begun (kda_cache_tables gives none) finds the e that its bytes give, whatever
+ * they are; of zeroed bytes -100.
  *
  * Layout.  pages is [num_pages][num_kv_heads][page_size / 16][32 * head_dim + 16]
  * bytes, D = head_dim.  A block's bytes, for token i = 0 .. 15 and channel c:

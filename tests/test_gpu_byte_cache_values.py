@@ -91,3 +91,31 @@ def test_scores_of_tens_of_millions(dtype, new):
     tol = want * (step + 12 * 2.0 ** -23)
     worst = float((np.abs(out.double().cpu().numpy() - want) / tol).max())
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_an_exponent_stays_until_the_block_is_begun_anew(dtype):
+    """In zeroed bytes from any place on; what a rejected draft has raised stays for the tokens that
+    follow, and falls with the next token at the first place."""
+    cache = torch.zeros((1, 1, 1, 32 * 64 + 16), dtype=torch.uint8, device=DEV)
+    small = 2.0 ** -12
+
+    def append(place, value):
+        x = torch.full((1, 1, 64), value, device=DEV).to(dtype)
+        kda.byte_cache_append(x, -x, torch.tensor([place], device=DEV), cache)
+
+    def held(place):
+        k, v = kda.byte_cache_read(torch.tensor([place], device=DEV), cache, dtype)
+        assert torch.equal(k, -v) and (k == k[0, 0, 0]).all()
+        return float(k[0, 0, 0]), int(cache[0, 0, 0, 32 * 64]) - 127
+
+    append(3, small)
+    assert held(3) == (small, -20)  # 2^-12 <= 448 2^-20
+    append(4, 1.0)
+    assert held(4) == (1.0, -8) and held(3)[0] == small
+    append(5, 64.0)  # a draft
+    assert held(5) == (64.0, -2) and held(3)[0] == 0.0  # 2^-10 of the unit, half of a step: to even
+    append(5, small)
+    assert held(5) == (0.0, -2) and held(4)[0] == 1.0
+    append(0, small)
+    assert held(0) == (small, -20)
