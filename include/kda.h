@@ -680,6 +680,13 @@ typedef struct {
  * pages that it does not need go back there, also in request order.  Entries of
  * a row past its length are left as they are and stand for nothing.
  *
+ * A page is taken to be one request's.  Where several requests hold pages
+ * (kda_cache_fork), a cut or an end here gives back pages that others still hold,
+ * which then stand on the ring twice, and tokens that follow a cut into such a page
+ * are written over what the others read: nothing reports it.  Cut and end such
+ * requests with kda_cache_fork; new tokens behind what they share, and the rejection of
+ * those, are safe here.
+ *
  * free_pages is a ring of ring_size entries.  Positions free_range[0] (head) to
  * free_range[1] - 1 (tail), taken modulo ring_size, are free pages; pages are
  * taken at the head and put back at the tail, where a later call finds them.

@@ -1010,7 +1010,9 @@ def cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_ra
     int32 [B, max_blocks] and free_pages int32 (a ring) updated in place,
     free_range int64 [2].  Returns (kv_lens [B], cu_new [B + 1], slots
     [max_tokens], free_range_out [2]); kv_lens may be held_lens or seq_lens and
-    free_range_out may be free_range, for a loop that updates in place."""
+    free_range_out may be free_range, for a loop that updates in place.  It gives back
+    pages whoever else holds them: cut (below what is shared) and end requests that
+    share pages with ``cache_fork``."""
     if stream is not None:
         with _on(stream, "held_lens", held_lens):
             return cache_tables(held_lens, seq_lens, new_lens, block_table, free_pages, free_range,
