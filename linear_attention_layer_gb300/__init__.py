@@ -855,8 +855,8 @@ def get_device_error(stream=None) -> int:
 
 
 def testing_inject_wait_timeout(launches: int = 1) -> None:
-    """Make the next `launches` tensor-core prefill launches or ``cache_attention``
-    and ``byte_cache_attention`` calls of this thread hit an expired device wait
+    """Make the next `launches` tensor-core prefill launches, ``cache_attention`` or
+    ``byte_cache_attention`` calls of this thread hit an expired device wait
     (``kda_testing_inject_wait_timeout``)."""
     load().kda_testing_inject_wait_timeout(int(launches))
 

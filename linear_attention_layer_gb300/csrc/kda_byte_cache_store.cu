@@ -10,11 +10,16 @@
 // One warp takes the new tokens of one block, a run of neighbours in the batch, and keeps
 // them in registers: 16 bytes of bf16 a lane and token, the largest magnitude by one redux.
 // Nothing is shared between warps.  What bounds it is HBM as long as enough warps have their
-// loads under way: 28 a SM of 72 registers (140 registers left 8: 672 us for the prompts below).
+// loads under way: with bf16 28 a SM of 72 registers (with 128 channels 12 to 36 bytes of them
+// spilled; CTAs of 256 threads of 140 registers left 8 warps, 672 us for the prompts below), with
+// fp32 16 of up to 127.
 //
-// Measured (GB300; bf16, heads of 128, 8 of them): prompts of 270336 tokens, 1.66 GB, appended in
-// 297 us (0.82 of the measured HBM rate), read back in 256 us (0.96); 8000 tokens 9.4 us; a decode
-// step of 256 tokens 3.9 us, of 4096 26 us.
+// Measured (GB300; bf16, 8 heads of 128; rates are the call's bytes over its time, of the measured HBM
+// rate): prompts of 270336 tokens, 1.66 GB, appended in 293 us (0.84), read back in 254 us (0.96; the
+// kernel keeps DRAM 82% busy); 8000 tokens 9.2 us; a decode step of 256 tokens 6.3 us into a cache that
+// it meets for the first time, 4.1 when the same tokens are appended again (no exponent rises, its
+// lines are in L2), of 4096 58 and 26.  fp32: 100000 tokens 163 us (0.93), with heads of 64 103 (0.73),
+// read back in 199 (0.76) and 101 (0.75); 4096 tokens 81 and 35.
 #include <algorithm>
 
 #include "kda_byte_cache.cuh"

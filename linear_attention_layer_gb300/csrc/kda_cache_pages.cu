@@ -15,8 +15,9 @@
 //
 // Measured (GB300): a fork of one prompt of 2000 tokens into 8 rows 7 us and its 7 copies 2.5 us
 // (the host takes 6 and 3); of 256 beams over 4096 tokens at most 10.4 us and 73
-// copies in two caches 7 us; a compaction of 4096 pages 9.6 us and its 930 moves of 128 KB 41 us,
-// 0.89 of the measured HBM rate (in the kernel alone 37, 0.98).
+// copies in two caches 7 us; a compaction of 4096 pages 9.6 us and its 930 moves of 128 KB, 245 MB in
+// and out, 41 us (37 in the kernel, a fifth of the bytes still in L2 at its end).  8192 copies of
+// 128 KB, 2.16 GB: 367 us, 357 in the kernel, 0.89 of the measured HBM rate, DRAM 76% busy.
 #include <algorithm>
 
 #include "kda_cache.cuh"
@@ -625,9 +626,11 @@ int sm_count() {
 }
 
 // Entries of tables that one CTA takes, and that one cluster does (pages and rows as far as its
-// shared memory has room).  Before the launches overlapped compactions of 600 entries took 8.6 us
-// with one CTA, 10.3 with the cluster, 13.7 as four kernels; of 5200 15.1, 12.4 and 14.9; a fork of
-// 35000 entries 12.5 us with the cluster, 15.5 as three kernels.
+// shared memory has room).  In a graph of 20 calls, with one CTA and with the cluster: compactions of
+// 600 entries 6.6 and 7.7 us, of 2048 8.3 and 9.3, of 4096 11.3 and 11.2, of 8192 18.9 and 15.1; forks of
+// 600 7.2 and 6.7, of 2368 8.6 and 7.7, of 16384 14.5 and 8.2 (a fork alone would take the cluster
+// at any size).  Before the launches overlapped: a compaction of 5200 12.4 us with the cluster and
+// 14.9 as four kernels, a fork of 35000 12.5 and 15.5 as three.
 constexpr int64_t kOneEntries = 1 << 11, kClusterEntries = 1 << 18;
 constexpr int kClusterPages = 32 * kMapWords;
 

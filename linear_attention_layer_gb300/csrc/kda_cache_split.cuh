@@ -23,7 +23,17 @@ constexpr int kMaxSeqs = 1024;                   // requests of one launch (thei
 // three passes here: 172 us, with the requests of more than 32 rows over there 203 (they
 // are a fifth of the keys, and the second set of launches costs 15 us); a pass over all of
 // these keys takes 95 us here, the chunk kernel's only one 200, so four passes lose.  Measured
-// with 8 query heads on a kv head and 128 channels; other shapes go by the same number.
+// with 8 query heads on a kv head, 128 channels and 4 bits; other shapes go by the same number.
+// 8 bits, here and over there (4 or 8 query heads a kv head alike):
+//     requests x keys, channels    16 rows    32 rows    48 rows    64 rows
+//     67 x 8000, 128               192  340   358  344   508  348   668  350
+//     67 x 8000,  64               117  332   221  332   326  334   425  336
+//     67 x 2000, 128                70  124   105  127   150  131   196  133
+//     67 x 2000,  64                44  116    73  117    96  118   128  120
+//      1 x 4000, 128                20   29    22   30    23   31    25   32
+//      1 x 32000, 128               29   46    36   47    42   48    52   49
+// so with 64 channels and for single requests 48 is about the border; batches of windows with
+// 128 channels would be served better by 32.
 constexpr int64_t kSplitRows = 48;
 
 // What a launch leaves in the workspace.
