@@ -858,11 +858,12 @@ typedef struct {
  *              tokens of one block stand next to one another in the batch, in any
  *              order but with none between them, not even a skipped one (as
  *              kda_cache_tables gives them)
- * A slot outside the cache is skipped and sets the device error word.  So are tokens
- * of a block that one of the 16 tokens before them is of, but not the one right before
- * (slots 0, -1, 1: the third); a batch that comes back to a block further on is not
- * found out, and what that block holds is then undefined.  An infinity does not count for the exponent and is stored as the block's largest
- * value of its sign, a NaN as zero; either sets the error word.
+ * A slot outside the cache is skipped and sets the device error word.  So is a token
+ * of a block that one of the 16 tokens before it is of, but not the one right before,
+ * with those of the block that follow it (slots 0, -1, 1, 2: the last two); a batch that
+ * comes back to a block further on is not found out, and what that block holds is then
+ * undefined.  An infinity does not count for the exponent and is stored as the block's
+ * largest value of its sign, a NaN as zero; either sets the error word.
  */
 kda_status_t kda_byte_cache_append(const kda_byte_cache_t* cache, int32_t io_dtype, int32_t num_tokens,
                                const void* k, const void* v, const int64_t* strides,
